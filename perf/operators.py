@@ -178,7 +178,7 @@ def prepare(case, seed):
              "x": normal(r, d, t=st), "f": normal(r, d, std=3.0, mean=0.2, t=bt),
              "w_post": normal(d, std=0.1, mean=1.0), "w_pre": normal(d, std=0.1, mean=1.0),
              "b_post": normal(d, std=0.1) if layer else None, "b_pre": normal(d, std=0.1) if layer else None}
-        s["gate"] = {"elem": lambda: normal(r, d, t=bt), "row": lambda: normal(r, t=bt), "col": lambda: normal(d),
+        s["gate"] = {"elem": lambda: normal(r, d, t=bt), "row": lambda: normal(r, 1, t=bt), "col": lambda: normal(d),
                      "none": lambda: None}[case["gate"]]()
         if op == "norm_bwd":   # what the forward left, and the gradients that come from above
             y, _, stats = _norm_fwd(s)
@@ -245,8 +245,7 @@ def _gate(s):
     kind = s["case"]["gate"]
     if kind == "none":
         return 1.0, 0.0
-    t = s["gate"].float()
-    a = torch.sigmoid(t[:, None] if kind == "row" else t)
+    a = torch.sigmoid(s["gate"].float())
     return a, a * (1.0 - a)
 
 
@@ -288,7 +287,7 @@ def _norm_bwd(s):
     if layer:
         out.update(db_post=dn.sum(0), db_pre=dh.sum(0))
     if kind != "none":
-        out["dgate"] = dg.sum(0) if kind == "col" else (dg.sum(1) if kind == "row" else dg).to(s["f"].dtype)
+        out["dgate"] = dg.sum(0) if kind == "col" else (dg.sum(1, keepdim=True) if kind == "row" else dg).to(s["f"].dtype)
     return out
 
 
@@ -420,9 +419,7 @@ def _exact_norm(s):
 
     def branch(z):
         n = _norm64(z, w["w_post"], w["b_post"], layer, eps)
-        if g is None:
-            return n
-        return n / (1.0 + torch.exp(-(g.unsqueeze(1) if kind == "row" else g)))
+        return n if g is None else n / (1.0 + torch.exp(-g))
 
     def stats(t):
         mean = t.mean(1) if layer else torch.zeros_like(t[:, 0])
