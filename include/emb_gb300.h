@@ -500,6 +500,183 @@ EMB_API emb_status emb_pipeline_release(emb_pipeline* pipe, int64_t ticket);
 EMB_API emb_status emb_pipeline_wait(emb_pipeline* pipe, int64_t ticket);
 
 /*
+ * The dense tower on the pooled output (JD ads article 4.2.1: the pooled
+ * embeddings feed a dense network, trained in mixed precision, 3.2.3 and
+ * 4.2.2; the pages give no formulas for it).  Four operators, each one call on
+ * a stream: the 8-bit quantiser and matrix product of a linear layer, the
+ * norms around a block, and the optimizer of the dense weights.  They take
+ * plain device matrices in row-major order and no table.  Kernel-side problems
+ * are reported by emb_check_op_flag().
+ */
+
+/* Element type of a dense array. */
+typedef enum { EMB_T_F32 = 0, EMB_T_BF16 = 1, EMB_T_F16 = 2 } emb_ftype;
+
+#define EMB_FP8_BLOCK 128 /* elements of a row, or rows of a tile, that share one 8-bit scale */
+
+/*
+ * emb_fp8_quantize -- 8-bit codes (e4m3: 4 exponent and 3 mantissa bits,
+ * largest value 448) of a matrix x[rows, cols], one float32 scale per block.
+ * A block is 128 columns of block_rows rows, block_rows 1 or 128 (fewer at the
+ * edges).  With A the largest finite magnitude of the block, at least 1e-30:
+ *   s = A * (1/448);  q = x * (448 * (1/A)), rounded to the nearest code (ties to even).
+ * x is q * s up to that rounding.  Values that are not finite get the code NaN.
+ *   x_d     x_t[rows, cols], rows ldx elements apart.
+ *   q_d     uint8[rows, cols], rows ldq bytes apart, 16-byte aligned, ldq a
+ *           multiple of 16 and >= cols; columns from cols to the next multiple
+ *           of 16 are set to zero.  s_d float32[ceil(cols/128), ceil(rows/block_rows)]:
+ *           one row of scales per 128 columns.
+ *   qt_d    the transposed matrix uint8[cols, rows], rows ldqt bytes apart
+ *           (the same rules), quantised in blocks of 128 of x's rows by
+ *           block_rows of its columns; st_d float32[ceil(rows/128), ceil(cols/block_rows)].
+ *           It is the operand of a weight gradient (block_rows 1) or of an
+ *           input gradient (block_rows 128), made in the same pass over x.
+ * Either pair may be NULL, not both.  Errors: INVALID_ARG, UNSUPPORTED
+ * (more than 2^31 - 1 tiles of 128 x 128).
+ */
+EMB_API emb_status emb_fp8_quantize(const void* x_d, emb_ftype x_t, int64_t rows, int64_t cols, int64_t ldx,
+                                    int32_t block_rows, void* q_d, int64_t ldq, float* s_d, void* qt_d, int64_t ldqt,
+                                    float* st_d, void* stream);
+
+/*
+ * emb_fp8_matmul -- product of two quantised matrices, both with the summed
+ * index k along their rows:
+ *   out[i, j] = bias[j] + sum over blocks b of 128 k's of
+ *               sa[b, i'] * sb[b, j'] * (sum over k in b of a[i, k] * b[j, k])
+ * with i' = i (a_block_rows 1) or i / 128 (128), j' likewise: the codes and
+ * scales emb_fp8_quantize writes.  Sums are float32; out is rounded once.
+ *   linear layer     y[B, O]  : a = x, b = W[O, I] (128)
+ *   its input grad   dx[B, I] : a = dy, b = W transposed (128)
+ *   its weight grad  dW[O, I] : a = dy transposed, b = x transposed (both 1)
+ *   a_d, b_d      uint8[m, k] and uint8[n, k], rows lda / ldb bytes apart,
+ *                 16-byte aligned, lda and ldb multiples of 16 and >= k.
+ *   sa_d, sb_d    float32[ceil(k/128), m or ceil(m/128)], likewise for n.
+ *   bias_d        float32[n] or NULL.
+ *   out_d         out_t[m, n], rows ldo elements apart, ldo >= n.
+ *   workspace_d   emb_fp8_matmul_workspace_size() bytes (may be 0: NULL),
+ *                 16-byte aligned; calls that share it must be ordered.
+ * The order of the sums depends on the sizes alone, so results repeat
+ * bitwise.  k = 0 gives the bias (or zeros).  Errors: INVALID_ARG, WORKSPACE,
+ * UNSUPPORTED (m, n or k above 2^31 - 1), CUDA.
+ */
+EMB_API emb_status emb_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+EMB_API emb_status emb_fp8_matmul(const void* a_d, int64_t lda, const float* sa_d, int32_t a_block_rows,
+                                  const void* b_d, int64_t ldb, const float* sb_d, int32_t b_block_rows, int64_t m,
+                                  int64_t n, int64_t k, const float* bias_d, void* out_d, emb_ftype out_t,
+                                  int64_t ldo, void* workspace_d, size_t ws_bytes, void* stream);
+
+/*
+ * emb_norm_gate_fwd -- the seam between two residual blocks in one pass: the
+ * norm after a block, its gate and residual scale, and the norm before the
+ * next block.  Per row of dim elements:
+ *   y = res_scale * x + act(gate) * (norm(f) * w_post + b_post)
+ *   h = norm(y) * w_pre + b_pre
+ *   norm(t) = t / sqrt(mean(t^2) + eps)                       (EMB_NORM_RMS)
+ *           = (t - mean(t)) / sqrt(mean((t - mean(t))^2) + eps)  (EMB_NORM_LAYER)
+ * x and y have type stream_t, f, h and a per-element or per-row gate block_t;
+ * stream_t is block_t or EMB_T_F32.  h is computed from y as stored.
+ *   f_d      the block's output, or NULL: the first norm of a tower, y = x
+ *            (y_d, gate_d and the post vectors must then be NULL).
+ *   h_d      NULL: the last block of a tower, no norm follows.
+ *   gate_d   by desc->gate: NULL, block_t[rows, dim], block_t[rows], or
+ *            float32[dim] (one gate per channel, a parameter).
+ *   w_*, b_* float32[dim] or NULL (ones, zeros); biases only with EMB_NORM_LAYER.
+ *   stats_d  float32[rows, 4]: mean and 1/sqrt of f's norm, then of y's (those
+ *            of a norm that is absent are 0); the backward reads them.  May be
+ *            NULL (serving).
+ * Arrays are contiguous; all arithmetic is float32, each output rounded once.
+ */
+typedef enum { EMB_NORM_RMS = 0, EMB_NORM_LAYER = 1 } emb_norm;
+typedef enum { EMB_GATE_NONE = 0, EMB_GATE_ELEM = 1, EMB_GATE_ROW = 2, EMB_GATE_COL = 3 } emb_gate;
+typedef enum { EMB_ACT_IDENTITY = 0, EMB_ACT_SIGMOID = 1 } emb_act;
+#define EMB_NORM_MAX_DIM 8192
+typedef struct {
+  int64_t rows;
+  int32_t dim;        /* 1..EMB_NORM_MAX_DIM (UNSUPPORTED beyond) */
+  emb_ftype stream_t;
+  emb_ftype block_t;
+  emb_norm norm;
+  emb_gate gate;
+  emb_act act;
+  float eps;          /* > 0 */
+  float res_scale;
+} emb_norm_gate_desc;
+EMB_API emb_status emb_norm_gate_fwd(const emb_norm_gate_desc* desc, const void* x_d, const void* f_d,
+                                     const void* gate_d, const float* w_post_d, const float* b_post_d,
+                                     const float* w_pre_d, const float* b_pre_d, void* y_d, void* h_d, float* stats_d,
+                                     void* stream);
+
+/*
+ * emb_norm_gate_bwd -- its gradients.  dy is the gradient that reaches y along
+ * the residual stream, dh the one that reaches h; either may be NULL (absent,
+ * not both).  With f NULL only dx and the pre vectors' gradients exist, and
+ * y_d is the forward's x.
+ *   dx_d       stream_t[rows, dim], df_d block_t[rows, dim], dgate_d the
+ *              gate's shape and type; dw_*_d, db_*_d float32[dim].  Each may
+ *              be NULL; those given are overwritten.  Sums over rows (vectors,
+ *              per-channel gate) are float32 in a fixed order.
+ *   workspace_d  emb_norm_gate_bwd_workspace_size() bytes, 16-byte aligned.
+ */
+EMB_API emb_status emb_norm_gate_bwd_workspace_size(const emb_norm_gate_desc* desc, size_t* bytes);
+EMB_API emb_status emb_norm_gate_bwd(const emb_norm_gate_desc* desc, const void* dy_d, const void* dh_d,
+                                     const void* y_d, const void* f_d, const void* gate_d, const float* stats_d,
+                                     const float* w_post_d, const float* b_post_d, const float* w_pre_d, void* dx_d,
+                                     void* df_d, void* dgate_d, float* dw_post_d, float* db_post_d, float* dw_pre_d,
+                                     float* db_pre_d, void* workspace_d, size_t ws_bytes, void* stream);
+
+/*
+ * emb_adamw_step -- one AdamW step (Loshchilov & Hutter, "Decoupled Weight
+ * Decay Regularization", ICLR 2019) over many tensors at once: the optimizer
+ * of the dense weights beside the table's sparse one (JD ads article 4.3:
+ * sparse and dense parts have their own optimizers and learning rates).  In
+ * float32, each operation rounded by itself, constants computed in double:
+ *   g = grad * grad_scale;  m = beta1 m + (1-beta1) g;  v = beta2 v + (1-beta2) g^2
+ *   w = w (1 - lr wd) - (m lr / (1-beta1^t)) / (sqrt(v) / sqrt(1-beta2^t) + eps)
+ * and w is rounded to nearest-even in its own type.
+ * State EMB_ADAM_F32: m and v are float32[n].  State EMB_ADAM_Q8: m and
+ * u = sqrt(v) are e4m3 codes uint8[n] with one float32 scale per 256
+ * consecutive elements of the tensor (s = A * (1/448) as emb_fp8_quantize).
+ * Codes are rounded stochastically: to nearest, an average that moves by 0.1 % a step would never leave its code
+ * (codes are up to 12.5 % apart).  The random numbers are a hash of (seed, t,
+ * first + element), so a step repeats bitwise.  A u > 0 is never stored as 0
+ * (the next update would divide by eps alone).  Moments that are not finite
+ * are stored as NaN and leave their block's scale alone.
+ */
+typedef enum { EMB_ADAM_F32 = 0, EMB_ADAM_Q8 = 1 } emb_adam_state;
+#define EMB_ADAM_BLOCK 256
+typedef struct {
+  void* param_d;    /* param_t[n], updated in place */
+  void* copy_d;     /* copy_t[n] or NULL: receives the updated weights rounded to copy_t */
+  void* m_d;        /* float32[n], or uint8[n] (Q8) */
+  void* v_d;
+  float* m_scale_d; /* Q8: float32[ceil(n/256)] */
+  float* v_scale_d;
+  int64_t n;        /* elements; 0 is allowed */
+  int64_t first;    /* Q8: number of this tensor's first element among all, for the random numbers */
+  emb_ftype param_t, grad_t, copy_t;
+} emb_adamw_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay; /* lr, weight_decay >= 0, 0 <= beta < 1, eps > 0 */
+  int64_t step;              /* t, from 1 */
+  emb_adam_state state;
+  uint32_t seed;
+  const float* grad_scale_d; /* device float32[1] or NULL: multiplies every gradient (clipping, loss scale) */
+} emb_adamw_params;
+/* tensors and grads (device pointers grad_t[n], one per tensor) are host
+ * arrays, read before the call returns.  Tensors must not overlap. */
+EMB_API emb_status emb_adamw_step(const emb_adamw_tensor* tensors, const void* const* grads, int32_t n_tensors,
+                                  const emb_adamw_params* params, void* stream);
+
+/*
+ * emb_check_op_flag -- synchronise `stream`, read and clear the flag word of
+ * the dense operators on the current device.  EMB_ERR_DEVICE_FLAG if a bit was
+ * set since the last check: EMB_FLAG_OP_TIMEOUT, a kernel's bounded wait ran
+ * out and its output is not valid.
+ */
+#define EMB_FLAG_OP_TIMEOUT 16u
+EMB_API emb_status emb_check_op_flag(void* stream, uint32_t* flags_out);
+
+/*
  * Fault injection, for tests of the failure paths (no counterpart in the
  * pages; everything is injected on the host, no kernel is made to fault).
  *  - emb_debug_fail_device_alloc(after): the next `after` device allocations

@@ -28,6 +28,9 @@ __all__ = [
     "emb_resolve", "emb_table_export", "emb_table_export_rows", "emb_table_slots", "emb_check_device_flag",
     "emb_status_string", "emb_last_error",
     "EMB_FLAG_PROBE_BOUND", "EMB_FLAG_BAD_OFFSETS", "EMB_FLAG_SLOT_MISMATCH", "EMB_FLAG_BAD_ROW",
+    "emb_fp8_quantize", "emb_fp8_matmul", "emb_fp8_matmul_workspace_size", "emb_norm_gate_fwd", "emb_norm_gate_bwd",
+    "emb_norm_gate_bwd_workspace_size", "emb_adamw_step", "AdamW", "emb_check_op_flag",
+    "EMB_FLAG_OP_TIMEOUT", "EMB_FP8_BLOCK", "EMB_ADAM_BLOCK", "EMB_NORM_MAX_DIM",
 ]
 
 EMB_OK = 0
@@ -37,10 +40,18 @@ STATUS = {0: "EMB_OK", 1: "EMB_ERR_INVALID_ARG", 2: "EMB_ERR_CUDA", 3: "EMB_ERR_
 EMB_FLAG_PROBE_BOUND, EMB_FLAG_BAD_OFFSETS, EMB_FLAG_SLOT_MISMATCH, EMB_FLAG_BAD_ROW = 1, 2, 4, 8
 EMB_NOALLOC_SCRATCH_BYTES = 64 << 20
 EMB_SORT_DIGIT_BITS = 7
+EMB_FLAG_OP_TIMEOUT = 16
+EMB_FP8_BLOCK = 128
+EMB_ADAM_BLOCK = 256
+EMB_NORM_MAX_DIM = 8192
 BWD_PHASES = ("expand", "sort", "reduce", "fixup")
 _DTYPE = {"f32": 0, "f16": 1, "f16m": 2}   # f16m: f32 master rows + the f16 copy the forward reads
 _POOL = {"sum": 0, "mean": 1}
 _OPT = {"adagrad": 0, "ftrl": 1, "rowwise_adagrad": 2}
+_FTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_NORM = {"rms": 0, "layer": 1}
+_ACT = {"identity": 0, "sigmoid": 1}
+_ADAM_STATE = {"f32": 0, "q8": 1}
 
 
 class LibraryNotBuilt(ImportError):
@@ -76,6 +87,24 @@ class _Stats(ctypes.Structure):
 
     def as_dict(self):
         return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class _NormGate(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int32), ("stream_t", ctypes.c_int), ("block_t", ctypes.c_int),
+                ("norm", ctypes.c_int), ("gate", ctypes.c_int), ("act", ctypes.c_int), ("eps", ctypes.c_float),
+                ("res_scale", ctypes.c_float)]
+
+
+class _AdamwTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("first", ctypes.c_int64), ("param_t", ctypes.c_int), ("grad_t", ctypes.c_int), ("copy_t", ctypes.c_int)]
+
+
+class _AdamwParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64), ("state", ctypes.c_int),
+                ("seed", ctypes.c_uint32), ("grad_scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -129,6 +158,15 @@ def lib():
             "emb_table_slots": [_vp, _vp, _vp, _vp],
             "emb_table_export_rows": [_vp, _vp, _i64, _vp, _vp, _vp],
             "emb_check_device_flag": [_vp, _vp, ctypes.POINTER(ctypes.c_uint32)],
+            "emb_fp8_quantize": [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int32, _vp, _i64, _vp, _vp, _i64, _vp, _vp],
+            "emb_fp8_matmul_workspace_size": [_i64, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)],
+            "emb_fp8_matmul": [_vp, _i64, _vp, ctypes.c_int32, _vp, _i64, _vp, ctypes.c_int32, _i64, _i64, _i64, _vp,
+                               _vp, ctypes.c_int, _i64, _vp, ctypes.c_size_t, _vp],
+            "emb_norm_gate_fwd": [ctypes.POINTER(_NormGate)] + [_vp] * 11,
+            "emb_norm_gate_bwd_workspace_size": [ctypes.POINTER(_NormGate), ctypes.POINTER(ctypes.c_size_t)],
+            "emb_norm_gate_bwd": [ctypes.POINTER(_NormGate)] + [_vp] * 17 + [ctypes.c_size_t, _vp],
+            "emb_adamw_step": [_vp, _vp, ctypes.c_int32, ctypes.POINTER(_AdamwParams), _vp],
+            "emb_check_op_flag": [_vp, ctypes.POINTER(ctypes.c_uint32)],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -534,3 +572,307 @@ class Pipeline:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------------------ the dense tower's operators
+
+
+def _alloc(stream, shape, dtype, device) -> torch.Tensor:
+    """A tensor for use on `stream`: torch's allocator then reuses its memory in that stream's order."""
+    if not isinstance(stream, torch.cuda.Stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _ftype(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _FTYPE:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return _FTYPE[t.dtype]
+
+
+def _matrix(t: torch.Tensor, dtype, name: str) -> int:
+    """Checks a CUDA matrix with neighbouring columns; returns its row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _codes(rows: int, cols: int, device, stream) -> torch.Tensor:
+    """An empty code matrix whose rows lie a multiple of 16 bytes apart."""
+    return _alloc(stream, (rows, -(-cols // 16) * 16), torch.float8_e4m3fn, device)[:, :cols]
+
+
+def _code_ld(t: torch.Tensor, name: str) -> int:
+    ld = _matrix(t, torch.float8_e4m3fn, name)
+    return -(-max(ld, t.shape[1]) // 16) * 16 if t.shape[0] <= 1 or t.shape[1] == 0 else ld
+
+
+def emb_fp8_quantize(x: torch.Tensor, block_rows: int = 1, transpose: bool = False, stream=None):
+    """e4m3 codes and scales of x[rows, cols] (float32, bfloat16 or float16; rows
+    may be strided): (q, s), with q[rows, cols] and s[ceil(cols/128),
+    ceil(rows/block_rows)]; with transpose=True (q, s, qt, st), the codes of
+    x.T in blocks along x's rows as well, from the same pass."""
+    ldx = _matrix(x, None, "x")
+    r, c = x.shape
+    q = _codes(r, c, x.device, stream)
+    s = _alloc(stream, (-(-c // EMB_FP8_BLOCK), -(-r // block_rows) if block_rows > 0 else 0), torch.float32, x.device)
+    qt = st = None
+    if transpose:
+        qt = _codes(c, r, x.device, stream)
+        st = _alloc(stream, (-(-r // EMB_FP8_BLOCK), -(-c // block_rows) if block_rows > 0 else 0), torch.float32, x.device)
+    _check(lib().emb_fp8_quantize(x.data_ptr(), _ftype(x, "x"), r, c, ldx, block_rows, q.data_ptr(), _code_ld(q, "q"),
+                                  s.data_ptr(), None if qt is None else qt.data_ptr(),
+                                  0 if qt is None else _code_ld(qt, "qt"), None if st is None else st.data_ptr(),
+                                  _stream(stream)))
+    return (q, s, qt, st) if transpose else (q, s)
+
+
+def emb_fp8_matmul_workspace_size(m: int, n: int, k: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().emb_fp8_matmul_workspace_size(m, n, k, ctypes.byref(b)))
+    return b.value
+
+
+def _block_rows(s: torch.Tensor, rows: int, k: int, name: str) -> int:
+    if s.dim() != 2 or s.shape[0] != -(-k // EMB_FP8_BLOCK) or s.shape[1] not in (rows, -(-rows // EMB_FP8_BLOCK)):
+        raise ValueError(f"{name} must be [ceil(k/128), rows] or [ceil(k/128), ceil(rows/128)], got {tuple(s.shape)}")
+    return 1 if s.shape[1] == rows else EMB_FP8_BLOCK
+
+
+def emb_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor,
+                   out_dtype: torch.dtype = torch.bfloat16, bias: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """a[m, k] @ b[n, k].T of codes and scales from emb_fp8_quantize (+ bias[n]).
+    workspace: emb_fp8_matmul_workspace_size bytes that the caller keeps; made
+    for the call if None."""
+    lda, ldb = _code_ld(a, "a"), _code_ld(b, "b")
+    (m, k), n = a.shape, b.shape[0]
+    if b.shape[1] != k:
+        raise ValueError(f"a and b must have the same columns, got {k} and {b.shape[1]}")
+    if bias is not None and bias.numel() != n:
+        raise ValueError(f"bias must have {n} elements")
+    if out is None:
+        out = _alloc(stream, (m, n), out_dtype, a.device)
+    elif tuple(out.shape) != (m, n):
+        raise ValueError(f"out must be [{m}, {n}]")
+    ldo = _matrix(out, None, "out")
+    if workspace is None:
+        workspace = _alloc(stream, (emb_fp8_matmul_workspace_size(m, n, k),), torch.uint8, a.device)
+    _check(lib().emb_fp8_matmul(a.data_ptr(), lda, _cuda(sa, torch.float32, "sa"), _block_rows(sa, m, k, "sa"),
+                                b.data_ptr(), ldb, _cuda(sb, torch.float32, "sb"), _block_rows(sb, n, k, "sb"), m, n, k,
+                                None if bias is None else _cuda(bias, torch.float32, "bias"), out.data_ptr(),
+                                _ftype(out, "out"), ldo, _cuda(workspace, None, "workspace"),
+                                workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+def _norm_gate(x: torch.Tensor, block_dtype: torch.dtype, gate, norm: str, act: str, eps: float,
+               res_scale: float) -> _NormGate:
+    if x.dim() != 2:
+        raise ValueError("x, f, y, h and their gradients must be matrices of one shape")
+    r, d = x.shape
+    kind = 0
+    if gate is not None:
+        kind = {(r, d): 1, (r, 1): 2, (d,): 3}.get(tuple(gate.shape), 0)
+        if kind == 0:
+            raise ValueError(f"gate must be [{r}, {d}], [{r}, 1] or [{d}], got {tuple(gate.shape)}")
+        if gate.dtype != (torch.float32 if kind == 3 else block_dtype):
+            raise TypeError("a gate per element or row has f's type, a gate per channel is float32")
+    if block_dtype not in _FTYPE:
+        raise TypeError(f"f and h must be float32, bfloat16 or float16, got {block_dtype}")
+    return _NormGate(r, d, _ftype(x, "x"), _FTYPE[block_dtype], _NORM[norm], kind, _ACT[act], eps, res_scale)
+
+
+def _vector(t: Optional[torch.Tensor], dim: int, name: str):
+    if t is not None and t.numel() != dim:
+        raise ValueError(f"{name} must have {dim} elements")
+    return None if t is None else _cuda(t, torch.float32, name)
+
+
+def _same(t: Optional[torch.Tensor], like: torch.Tensor, name: str):
+    if t is None:
+        return None
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must be {tuple(like.shape)}, got {tuple(t.shape)}")
+    return _cuda(t, like.dtype, name)
+
+
+def emb_norm_gate_fwd(x: torch.Tensor, f: Optional[torch.Tensor], gate: Optional[torch.Tensor] = None, *,
+                      w_post: Optional[torch.Tensor] = None, b_post: Optional[torch.Tensor] = None,
+                      w_pre: Optional[torch.Tensor] = None, b_pre: Optional[torch.Tensor] = None, norm: str = "rms",
+                      act: str = "sigmoid", eps: float = 1e-6, res_scale: float = 1.0, pre: bool = True,
+                      stats: bool = True, block_dtype: Optional[torch.dtype] = None, stream=None):
+    """y = res_scale * x + act(gate) * (norm(f) * w_post + b_post) and h = norm(y) *
+    w_pre + b_pre: (y, h, stats).  f=None: y is x (None is returned for it).
+    pre=False: no norm follows (h is None).  gate: [rows, dim] or [rows, 1] in f's
+    type, or float32 [dim].  stats: float32 [rows, 4] for the backward, or None
+    with stats=False.  block_dtype: h's type where f is None (default x's)."""
+    block_dtype = f.dtype if f is not None else block_dtype or x.dtype
+    d = _norm_gate(x, block_dtype, gate, norm, act, eps, res_scale)
+    if f is not None and f.shape != x.shape:
+        raise ValueError(f"f must be {tuple(x.shape)}, got {tuple(f.shape)}")
+    y = None if f is None else _alloc(stream, x.shape, x.dtype, x.device)
+    h = _alloc(stream, x.shape, block_dtype, x.device) if pre else None
+    st = _alloc(stream, (x.shape[0], 4), torch.float32, x.device) if stats else None
+    _check(lib().emb_norm_gate_fwd(ctypes.byref(d), _cuda(x, None, "x"), None if f is None else _cuda(f, None, "f"),
+                                   None if gate is None else _cuda(gate, None, "gate"),
+                                   _vector(w_post, d.dim, "w_post"), _vector(b_post, d.dim, "b_post"),
+                                   _vector(w_pre, d.dim, "w_pre"), _vector(b_pre, d.dim, "b_pre"), _ptr(y), _ptr(h),
+                                   _ptr(st), _stream(stream)))
+    return y, h, st
+
+
+def emb_norm_gate_bwd_workspace_size(rows: int, dim: int) -> int:
+    b = ctypes.c_size_t()
+    d = _NormGate(rows, dim, 0, 0, 0, 0, 0, 1.0, 1.0)
+    _check(lib().emb_norm_gate_bwd_workspace_size(ctypes.byref(d), ctypes.byref(b)))
+    return b.value
+
+
+def emb_norm_gate_bwd(dy: Optional[torch.Tensor], dh: Optional[torch.Tensor], y: torch.Tensor,
+                      f: Optional[torch.Tensor], gate: Optional[torch.Tensor], stats: torch.Tensor, *,
+                      w_post: Optional[torch.Tensor] = None, b_post: Optional[torch.Tensor] = None,
+                      w_pre: Optional[torch.Tensor] = None, b_pre: Optional[torch.Tensor] = None, norm: str = "rms",
+                      act: str = "sigmoid", eps: float = 1e-6, res_scale: float = 1.0,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients of emb_norm_gate_fwd from dy (of y, along the residual stream) and
+    dh (of h), either None if absent: {"dx", "df", "dgate", "dw_post", "db_post",
+    "dw_pre", "db_pre"}, None for those of an input that is absent.  y: the
+    forward's y (its x where f is None)."""
+    like = f if f is not None else dh
+    if like is None:
+        raise ValueError("f and dh are both None")
+    d = _norm_gate(y, like.dtype, gate, norm, act, eps, res_scale)
+    if like.shape != y.shape:
+        raise ValueError(f"f must be {tuple(y.shape)}, got {tuple(like.shape)}")
+    r, dim, dev = d.rows, d.dim, y.device
+    if tuple(stats.shape) != (r, 4):
+        raise ValueError(f"stats must be [{r}, 4]")
+
+    def vec(like):
+        return None if like is None else _alloc(stream, (dim,), torch.float32, dev)
+
+    dy_p, dh_p = _same(dy, y, "dy"), None
+    if dh is not None:
+        if dh.shape != y.shape:
+            raise ValueError(f"dh must be {tuple(y.shape)}, got {tuple(dh.shape)}")
+        dh_p = _cuda(dh, like.dtype, "dh")
+    out = {"dx": _alloc(stream, y.shape, y.dtype, dev), "df": None if f is None else _alloc(stream, f.shape, f.dtype, dev),
+           "dgate": None if gate is None else _alloc(stream, gate.shape, gate.dtype, dev),
+           "dw_post": vec(w_post), "db_post": vec(b_post), "dw_pre": vec(w_pre), "db_pre": vec(b_pre)}
+    if workspace is None:
+        workspace = _alloc(stream, (emb_norm_gate_bwd_workspace_size(r, dim),), torch.uint8, dev)
+    _vector(b_pre, dim, "b_pre")
+    _check(lib().emb_norm_gate_bwd(ctypes.byref(d), dy_p, dh_p, _cuda(y, None, "y"),
+                                   None if f is None else _cuda(f, None, "f"),
+                                   None if gate is None else _cuda(gate, None, "gate"), _cuda(stats, torch.float32, "stats"),
+                                   _vector(w_post, dim, "w_post"), _vector(b_post, dim, "b_post"),
+                                   _vector(w_pre, dim, "w_pre"), _ptr(out["dx"]), _ptr(out["df"]), _ptr(out["dgate"]),
+                                   _ptr(out["dw_post"]), _ptr(out["db_post"]), _ptr(out["dw_pre"]), _ptr(out["db_pre"]),
+                                   _cuda(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
+                                   _stream(stream)))
+    return out
+
+
+def emb_adamw_step(tensors, grads, params: _AdamwParams, stream=None) -> None:
+    """One step over a ctypes array of _AdamwTensor and one of gradient pointers (AdamW builds both)."""
+    _check(lib().emb_adamw_step(tensors, grads, len(tensors), ctypes.byref(params), _stream(stream)))
+
+
+class AdamW:
+    """AdamW over a list of tensors, one launch a step.  params: contiguous CUDA
+    tensors (float32, bfloat16 or float16), updated in place.  copies: for each
+    float32 parameter a bfloat16 or float16 tensor (or None) that receives the
+    updated weights, as the "f16m" tables keep them.  state "f32", or "q8": m and
+    sqrt(v) as e4m3 codes with a scale per 256 elements, stochastically rounded
+    from `seed`.  The states live in `arena` (m, v, m_scale, v_scale: all
+    tensors one after another, each from a multiple of 256 elements), which
+    with `step_count` is the checkpoint; load_state takes per-tensor lists."""
+
+    def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999),
+                 eps: float = 1e-8, weight_decay: float = 0.01, state: str = "f32", seed: int = 0,
+                 copies: Optional[Sequence[Optional[torch.Tensor]]] = None):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("params is empty")
+        self.lr, self.betas, self.eps, self.weight_decay, self.seed = lr, betas, eps, weight_decay, seed
+        self.state, self.step_count, self.device = state, 0, self.params[0].device
+        self._copies = list(copies) if copies is not None else [None] * len(self.params)
+        if len(self._copies) != len(self.params):
+            raise ValueError("copies must have one entry per parameter")
+        q8 = _ADAM_STATE[state] == 1
+        block = EMB_ADAM_BLOCK
+        self._n = [p.numel() for p in self.params]
+        self._at = [0]
+        for n in self._n:
+            self._at.append(self._at[-1] + -(-n // block) * block)
+        total = self._at[-1]
+        st = torch.float8_e4m3fn if q8 else torch.float32
+        zeros = lambda n, t: torch.zeros(n, dtype=torch.uint8 if t.itemsize == 1 else t, device=self.device).view(t)  # noqa: E731
+        self.arena = {"m": zeros(total, st), "v": zeros(total, st),
+                      "m_scale": zeros(total // block, torch.float32) if q8 else None,
+                      "v_scale": zeros(total // block, torch.float32) if q8 else None}
+        self._tensors = (_AdamwTensor * len(self.params))()
+        base = {k: 0 if v is None else v.data_ptr() for k, v in self.arena.items()}
+        for i, (p, c) in enumerate(zip(self.params, self._copies)):
+            if p.device != self.device:
+                raise ValueError("parameters must be on one device")
+            if c is not None and c.numel() != p.numel():
+                raise ValueError("a copy must have its parameter's size")
+            at = self._at[i]
+            self._tensors[i] = _AdamwTensor(_cuda(p, None, "param"), None if c is None else _cuda(c, None, "copy"),
+                                            base["m"] + at * st.itemsize, base["v"] + at * st.itemsize,
+                                            base["m_scale"] + at // block * 4 if q8 else None,
+                                            base["v_scale"] + at // block * 4 if q8 else None, self._n[i], at,
+                                            _ftype(p, "param"), _ftype(p, "param"), 0 if c is None else _ftype(c, "copy"))
+        self._grad_dtypes = [p.dtype for p in self.params]
+
+    def load_state(self, step: int, m, v, m_scale=None, v_scale=None) -> None:
+        """Sets the states from one tensor per parameter (the layout of `arena`, without its padding)."""
+        for key, parts in (("m", m), ("v", v), ("m_scale", m_scale), ("v_scale", v_scale)):
+            if (parts is None) != (self.arena[key] is None):
+                raise ValueError(f"{key} does not match the state kind {self.state}")
+            if parts is None:
+                continue
+            whole = self.arena[key]
+            for part, at, n in zip(parts, self._at, self._n):
+                if key.endswith("scale"):
+                    at, n = at // EMB_ADAM_BLOCK, -(-n // EMB_ADAM_BLOCK)
+                if part.numel() != n or part.dtype != whole.dtype:
+                    raise ValueError(f"{key}: expected {n} elements of {whole.dtype}")
+                whole[at:at + n].view(torch.uint8).copy_(part.reshape(-1).view(torch.uint8))
+        self.step_count = int(step)
+
+    def step(self, grads: Sequence[torch.Tensor], grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+        """One step.  grads: one contiguous tensor per parameter (float32, bfloat16 or
+        float16); grad_scale: device float32 scalar that multiplies them."""
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(self.params)} gradients are needed, got {len(grads)}")
+        if [g.numel() for g in grads] != self._n or not all([g.is_cuda and g.is_contiguous() for g in grads]):
+            raise ValueError("each gradient must be a contiguous CUDA tensor of its parameter's size")
+        dtypes = [g.dtype for g in grads]
+        if dtypes != self._grad_dtypes:
+            for t, g in zip(self._tensors, grads):
+                t.grad_t = _ftype(g, "grad")
+            self._grad_dtypes = dtypes
+        ptrs = (ctypes.c_void_p * len(grads))(*[g.data_ptr() for g in grads])
+        p = _AdamwParams(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, self.step_count + 1,
+                         _ADAM_STATE[self.state], self.seed & 0xFFFFFFFF,
+                         None if grad_scale is None else _cuda(grad_scale, torch.float32, "grad_scale"))
+        emb_adamw_step(self._tensors, ptrs, p, stream)
+        self.step_count += 1
+
+
+def emb_check_op_flag(stream=None) -> int:
+    """Synchronise, read and clear the dense operators' flag word (0 = clean)."""
+    f = ctypes.c_uint32()
+    rc = lib().emb_check_op_flag(_stream(stream), ctypes.byref(f))
+    if rc not in (EMB_OK, 8):
+        raise EmbError(rc, emb_last_error())
+    return f.value

@@ -1,0 +1,372 @@
+// AdamW over many tensors in one launch, states in float32 or in 8 bits.
+//
+// A pass over memory: w, m and v are read and written once, the gradient read
+// once.  28 bytes a weight in float32; 14 with bf16 gradients and 8-bit
+// states, whose sixty-odd instructions a weight (two 8-bit roundings with a
+// hash each, a division, a square root) then come near the issue rate.
+//
+// Work is cut into units of 256 consecutive elements of one tensor, one warp
+// each, eight elements a lane: the unit is the block that shares a scale, so
+// its largest magnitude is one warp reduction and no shared memory is needed.
+// The tensors' descriptors travel in the kernel's parameters (no table in
+// device memory to fill, so nothing to order or to free); a warp finds its
+// unit's tensor by bisection over their first units.
+#include <cmath>
+
+#include "emb_dense.cuh"
+
+namespace emb {
+namespace {
+
+struct TensorArg {
+  void* p;
+  void* copy;
+  const void* g;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+  long long n;
+  long long first;
+  unsigned unit0;       // first unit of this tensor among the launch's
+  unsigned char pt, gt, ct, vec;
+};
+
+// Launches of up to 40 tensors pass 4 KB of parameters, larger ones up to 32 KB.
+template <int N>
+struct StepArgs {
+  TensorArg t[N];
+  int n_tensors;
+  unsigned n_units;
+  unsigned span;        // consecutive units a block takes
+  float beta1, omb1, beta2, omb2, decay, lr_c1, rc2, eps;
+  unsigned key;
+  const float* grad_scale;
+};
+
+__device__ __forceinline__ void load8(const void* base, int type, long long i, float* o) {
+  if (type == EMB_T_F32) {
+    Raw8<float> r;
+    r.load((const float*)base + i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = r.get(k);
+  } else if (type == EMB_T_BF16) {
+    Raw8<__nv_bfloat16> r;
+    r.load((const __nv_bfloat16*)base + i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = r.get(k);
+  } else {
+    Raw8<__half> r;
+    r.load((const __half*)base + i);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = r.get(k);
+  }
+}
+__device__ __forceinline__ void store8(void* base, int type, long long i, const float* o) {
+  if (type == EMB_T_F32) {
+    Raw8<float> r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.set2(k, o[2 * k], o[2 * k + 1]);
+    r.store((float*)base + i);
+  } else if (type == EMB_T_BF16) {
+    Raw8<__nv_bfloat16> r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.set2(k, o[2 * k], o[2 * k + 1]);
+    r.store((__nv_bfloat16*)base + i);
+  } else {
+    Raw8<__half> r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.set2(k, o[2 * k], o[2 * k + 1]);
+    r.store((__half*)base + i);
+  }
+}
+__device__ __forceinline__ float load1(const void* base, int type, long long i) {
+  return type == EMB_T_F32 ? ((const float*)base)[i]
+         : type == EMB_T_BF16 ? __bfloat162float(((const __nv_bfloat16*)base)[i])
+                              : __half2float(((const __half*)base)[i]);
+}
+__device__ __forceinline__ void store1(void* base, int type, long long i, float x) {
+  if (type == EMB_T_F32) ((float*)base)[i] = x;
+  else if (type == EMB_T_BF16) ((__nv_bfloat16*)base)[i] = __float2bfloat16_rn(x);
+  else ((__half*)base)[i] = __float2half_rn(x);
+}
+
+// MurmurHash3 32-bit finaliser (Appleby, public domain).
+__device__ __forceinline__ unsigned fmix32(unsigned h) {
+  h ^= h >> 16;
+  h *= 0x85ebca6bu;
+  h ^= h >> 13;
+  h *= 0xc2b2ae35u;
+  return h ^ (h >> 16);
+}
+
+// A magnitude in code units (at most 448 after the clamp) to one of the two
+// codes around it, upwards with the probability of its distance from the lower
+// one.  Codes from 2^-6 on have 3 mantissa bits: adding 20 random bits below
+// them and cutting rounds to one of them.  Below 2^-6 codes are 2^-9 apart;
+// adding 2^-6 first puts that spacing at the same bit.  mag is finite.
+__device__ __forceinline__ float round_random(float mag, unsigned r20) {
+  mag = fminf(mag, kE4m3Max);
+  const float base = mag < 0.015625f ? 0.015625f : 0.0f;
+  const unsigned cut = (__float_as_uint(__fadd_rn(mag, base)) + r20) & ~0xFFFFFu;
+  return __fsub_rn(__uint_as_float(cut), base);
+}
+
+__device__ __forceinline__ float warp_amax(float a) {  // a >= 0: the bits order as the values
+  return fmaxf(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a))), kAmaxFloor);
+}
+
+template <bool kQ8, int N>
+__global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ StepArgs<N> a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
+  const unsigned end = min(a.n_units, (blockIdx.x + 1) * a.span);
+  unsigned unit = blockIdx.x * a.span + warp;
+  if (unit >= end) return;
+  int lo = 0, hi = a.n_tensors - 1;  // last tensor whose unit0 <= unit
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.t[mid].unit0 <= unit) lo = mid; else hi = mid - 1;
+  }
+  for (; unit < end; unit += 8) {
+    while (lo + 1 < a.n_tensors && a.t[lo + 1].unit0 <= unit) ++lo;
+    const TensorArg& t = a.t[lo];
+    const unsigned blk = unit - t.unit0;
+    const long long i0 = (long long)blk * EMB_ADAM_BLOCK + lane * 8;
+    const int cnt = (int)max(0LL, min(8LL, t.n - i0));
+    const bool vec = t.vec && cnt == 8;
+    float p[8], g[8], m[8], u[8];
+    if (vec) {
+      load8(t.g, t.gt, i0, g);
+      load8(t.p, t.pt, i0, p);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        g[k] = k < cnt ? load1(t.g, t.gt, i0 + k) : 0.0f;
+        p[k] = k < cnt ? load1(t.p, t.pt, i0 + k) : 0.0f;
+      }
+    }
+    if constexpr (kQ8) {
+      const float ms = t.ms[blk], vs = t.vs[blk];
+      unsigned char cm[8], cv[8];
+      if (vec) {
+        *reinterpret_cast<uint2*>(cm) = *reinterpret_cast<const uint2*>((const unsigned char*)t.m + i0);
+        *reinterpret_cast<uint2*>(cv) = *reinterpret_cast<const uint2*>((const unsigned char*)t.v + i0);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          cm[k] = k < cnt ? ((const unsigned char*)t.m)[i0 + k] : 0;
+          cv[k] = k < cnt ? ((const unsigned char*)t.v)[i0 + k] : 0;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = e4m3x2_to_f32(reinterpret_cast<unsigned short*>(cm)[k]);
+        const float2 y = e4m3x2_to_f32(reinterpret_cast<unsigned short*>(cv)[k]);
+        m[2 * k] = __fmul_rn(x.x, ms);
+        m[2 * k + 1] = __fmul_rn(x.y, ms);
+        u[2 * k] = __fmul_rn(y.x, vs);
+        u[2 * k + 1] = __fmul_rn(y.y, vs);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) u[k] = __fmul_rn(u[k], u[k]);
+    } else {
+      if (vec) {
+        load8(t.m, EMB_T_F32, i0, m);
+        load8(t.v, EMB_T_F32, i0, u);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          m[k] = k < cnt ? ((const float*)t.m)[i0 + k] : 0.0f;
+          u[k] = k < cnt ? ((const float*)t.v)[i0 + k] : 0.0f;
+        }
+      }
+    }
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float gk = a.grad_scale ? __fmul_rn(g[k], gs) : g[k];
+      m[k] = __fadd_rn(__fmul_rn(m[k], a.beta1), __fmul_rn(gk, a.omb1));
+      v[k] = __fadd_rn(__fmul_rn(u[k], a.beta2), __fmul_rn(__fmul_rn(gk, gk), a.omb2));
+      u[k] = __fsqrt_rn(v[k]);
+      const float den = __fadd_rn(__fmul_rn(u[k], a.rc2), a.eps);
+      p[k] = __fsub_rn(__fmul_rn(p[k], a.decay), __fdiv_rn(__fmul_rn(m[k], a.lr_c1), den));
+    }
+    if (vec) {
+      store8(t.p, t.pt, i0, p);
+      if (t.copy) store8(t.copy, t.ct, i0, p);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < cnt) {
+          store1(t.p, t.pt, i0 + k, p[k]);
+          if (t.copy) store1(t.copy, t.ct, i0 + k, p[k]);
+        }
+    }
+    if constexpr (kQ8) {
+      float am = 0.0f, au = 0.0f;  // elements past the end are zeros here and do not count
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k < cnt) {
+          am = fmaxf(am, finite_abs(m[k]));
+          au = fmaxf(au, finite_abs(u[k]));
+        }
+      }
+      am = warp_amax(am);
+      au = warp_amax(au);
+      const float im = inv_of(am), iu = inv_of(au);
+      const unsigned long long e0 = (unsigned long long)(t.first + i0);
+      float qm[8], qu[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const unsigned long long e = e0 + k;
+        const unsigned r = fmix32((unsigned)e ^ ((unsigned)(e >> 32) * 0x9e3779b9u) ^ a.key);
+        // a value that is not finite would carry out of its bits above: it becomes the code NaN here
+        const float xm = __fmul_rn(m[k], im);
+        const float a_m = round_random(fabsf(xm), ((r & 0xffffu) << 4) + 8u);
+        qm[k] = finite_f32(m[k]) ? (xm < 0.0f ? -a_m : a_m) : __uint_as_float(0x7fc00000u);
+        float a_u = round_random(__fmul_rn(u[k], iu), ((r >> 16) << 4) + 8u);
+        if (u[k] > 0.0f && a_u == 0.0f) a_u = 0.001953125f;
+        qu[k] = finite_f32(u[k]) ? a_u : __uint_as_float(0x7fc00000u);
+      }
+      unsigned wm[2], wu[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        wm[k] = e4m3x2(qm[4 * k], qm[4 * k + 1]) | (e4m3x2(qm[4 * k + 2], qm[4 * k + 3]) << 16);
+        wu[k] = e4m3x2(qu[4 * k], qu[4 * k + 1]) | (e4m3x2(qu[4 * k + 2], qu[4 * k + 3]) << 16);
+      }
+      if (vec) {
+        *reinterpret_cast<uint2*>((unsigned char*)t.m + i0) = make_uint2(wm[0], wm[1]);
+        *reinterpret_cast<uint2*>((unsigned char*)t.v + i0) = make_uint2(wu[0], wu[1]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < cnt) {
+            ((unsigned char*)t.m)[i0 + k] = (unsigned char)(wm[k >> 2] >> (8 * (k & 3)));
+            ((unsigned char*)t.v)[i0 + k] = (unsigned char)(wu[k >> 2] >> (8 * (k & 3)));
+          }
+      }
+      if (lane == 0) {
+        t.ms[blk] = scale_of(am);
+        t.vs[blk] = scale_of(au);
+      }
+    } else {
+      if (vec) {
+        store8(t.m, EMB_T_F32, i0, m);
+        store8(t.v, EMB_T_F32, i0, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < cnt) {
+            ((float*)t.m)[i0 + k] = m[k];
+            ((float*)t.v)[i0 + k] = v[k];
+          }
+      }
+    }
+  }
+}
+
+emb_status check_tensor(const emb_adamw_tensor& t, const void* g, bool q8, int i) {
+  const std::string at = "tensor " + std::to_string(i) + ": ";
+  if (t.n < 0 || t.first < 0) return fail(EMB_ERR_INVALID_ARG, at + "negative n or first");
+  if (!good_ftype(t.param_t) || !good_ftype(t.grad_t)) return fail(EMB_ERR_INVALID_ARG, at + "bad element type");
+  if (t.copy_d && (t.param_t != EMB_T_F32 || (t.copy_t != EMB_T_BF16 && t.copy_t != EMB_T_F16)))
+    return fail(EMB_ERR_INVALID_ARG, at + "a copy is bf16 or f16 of float32 weights");
+  if (t.n == 0) return EMB_OK;
+  if (!t.param_d || !g || !t.m_d || !t.v_d) return fail(EMB_ERR_INVALID_ARG, at + "param, grad, m or v is NULL");
+  if (q8 && (!t.m_scale_d || !t.v_scale_d)) return fail(EMB_ERR_INVALID_ARG, at + "8-bit states need their scales");
+  const size_t st = q8 ? 1 : 4;
+  if (!aligned_to(t.param_d, ftype_bytes(t.param_t)) || !aligned_to(g, ftype_bytes(t.grad_t)) ||
+      !aligned_to(t.m_d, st) || !aligned_to(t.v_d, st) || !aligned_to(t.copy_d, 2) || !aligned_to(t.m_scale_d, 4) ||
+      !aligned_to(t.v_scale_d, 4))
+    return fail(EMB_ERR_INVALID_ARG, at + "an array is not aligned to its elements");
+  return EMB_OK;
+}
+
+template <bool kQ8, int N>
+cudaError_t launch(const emb_adamw_tensor* ts, const void* const* grads, int n, const emb_adamw_params* p,
+                   unsigned n_units, cudaStream_t st) {
+  StepArgs<N> a;
+  unsigned unit = 0;
+  a.n_tensors = 0;
+  for (int i = 0; i < n; ++i) {
+    const emb_adamw_tensor& t = ts[i];
+    if (t.n == 0) continue;
+    TensorArg& o = a.t[a.n_tensors++];
+    o = {t.param_d, t.copy_d, grads[i], t.m_d, t.v_d, t.m_scale_d, t.v_scale_d, t.n, t.first, unit,
+         (unsigned char)t.param_t, (unsigned char)t.grad_t, (unsigned char)t.copy_t, 0};
+    const size_t sb = kQ8 ? 8 : 32;  // eight elements of a state
+    o.vec = aligned_to(t.param_d, 8 * ftype_bytes(t.param_t)) && aligned_to(grads[i], 8 * ftype_bytes(t.grad_t)) &&
+            aligned_to(t.m_d, sb) && aligned_to(t.v_d, sb) && aligned_to(t.copy_d, 16);
+    unit += (unsigned)((t.n + EMB_ADAM_BLOCK - 1) / EMB_ADAM_BLOCK);
+  }
+  if (a.n_tensors == 0) return cudaSuccess;
+  const double c1 = 1.0 - std::pow(p->beta1, (double)p->step), c2 = 1.0 - std::pow(p->beta2, (double)p->step);
+  a.n_units = n_units;
+  a.beta1 = (float)p->beta1;
+  a.omb1 = (float)(1.0 - p->beta1);
+  a.beta2 = (float)p->beta2;
+  a.omb2 = (float)(1.0 - p->beta2);
+  a.decay = (float)(1.0 - p->lr * p->weight_decay);
+  a.lr_c1 = (float)(p->lr / c1);
+  a.rc2 = (float)(1.0 / std::sqrt(c2));
+  a.eps = (float)p->eps;
+  a.key = p->seed * 0x9e3779b9u + (unsigned)p->step * 0x85ebca6bu;
+  a.grad_scale = p->grad_scale_d;
+  // a block takes up to 64 consecutive units (8 a warp), fewer when that would leave SMs without one
+  const unsigned blocks_wanted = 6u * (unsigned)sm_count();
+  a.span = 8;
+  while (a.span < 64 && n_units / (2 * a.span) >= blocks_wanted) a.span *= 2;
+  adamw_kernel<kQ8, N><<<(n_units + a.span - 1) / a.span, 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace emb
+
+using namespace emb;
+
+extern "C" emb_status emb_adamw_step(const emb_adamw_tensor* tensors, const void* const* grads, int32_t n_tensors,
+                                     const emb_adamw_params* params, void* stream) {
+  if (!params || n_tensors < 0 || (n_tensors > 0 && (!tensors || !grads)))
+    return fail(EMB_ERR_INVALID_ARG, "params, tensors or grads is NULL, or n_tensors negative");
+  const emb_adamw_params& p = *params;
+  if (!(p.lr >= 0) || !(p.weight_decay >= 0) || !(p.beta1 >= 0 && p.beta1 < 1) || !(p.beta2 >= 0 && p.beta2 < 1) ||
+      !(p.eps > 0) || !std::isfinite(p.lr) || !std::isfinite(p.weight_decay) || !std::isfinite(p.eps))
+    return fail(EMB_ERR_INVALID_ARG, "need lr, weight_decay >= 0, 0 <= beta < 1, eps > 0");
+  if (!((float)p.eps > 0)) return fail(EMB_ERR_INVALID_ARG, "eps is zero in float32");
+  if (p.step < 1) return fail(EMB_ERR_INVALID_ARG, "step counts from 1");
+  if (p.state != EMB_ADAM_F32 && p.state != EMB_ADAM_Q8) return fail(EMB_ERR_INVALID_ARG, "bad state kind");
+  const bool q8 = p.state == EMB_ADAM_Q8;
+  for (int i = 0; i < n_tensors; ++i) {
+    const emb_status rc = check_tensor(tensors[i], grads[i], q8, i);
+    if (rc != EMB_OK) return rc;
+    if (tensors[i].n / EMB_ADAM_BLOCK >= 0x7fffff00LL) return fail(EMB_ERR_UNSUPPORTED, "a tensor has over 2^39 elements");
+  }
+  constexpr int kFew = 40, kMany = 380;
+  static_assert(sizeof(StepArgs<kFew>) <= 4096 && sizeof(StepArgs<kMany>) <= 32764, "kernel parameters");
+  int done = 0;
+  while (done < n_tensors) {
+    // as many tensors as one launch takes: 380, or fewer so that units stay below 2^31
+    int k = done;
+    long long units = 0;
+    while (k < n_tensors && k - done < kMany) {
+      const long long u = (tensors[k].n + EMB_ADAM_BLOCK - 1) / EMB_ADAM_BLOCK;
+      if (k > done && units + u > 0x7fffff00LL) break;
+      units += u;
+      ++k;
+    }
+    const emb_adamw_tensor* t = tensors + done;
+    const void* const* g = grads + done;
+    cudaError_t e;
+    if (k - done <= kFew)
+      e = q8 ? launch<true, kFew>(t, g, k - done, params, (unsigned)units, (cudaStream_t)stream)
+             : launch<false, kFew>(t, g, k - done, params, (unsigned)units, (cudaStream_t)stream);
+    else
+      e = q8 ? launch<true, kMany>(t, g, k - done, params, (unsigned)units, (cudaStream_t)stream)
+             : launch<false, kMany>(t, g, k - done, params, (unsigned)units, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "adamw_kernel launch");
+    done = k;
+  }
+  return EMB_OK;
+}

@@ -1,0 +1,207 @@
+// 8-bit quantiser: codes and block scales of a matrix and of its transpose.
+//
+// Bound by memory: x in once, one byte an element out per orientation.  A block
+// of 256 threads takes one tile of 128 x 128: warp w holds rows 16w..16w+15, a
+// lane four neighbouring columns of each, so a warp reads and writes whole
+// 128-element row pieces.  The tile stays in registers while the largest
+// magnitudes of its rows (warp reductions), its columns (in shared memory over
+// the warps) or all of it are found; the transposed codes go through shared
+// memory so that they leave as whole rows too.
+#include <algorithm>
+
+#include "emb_dense.cuh"
+
+namespace emb {
+namespace {
+
+constexpr int kTile = EMB_FP8_BLOCK;
+
+struct QuantArgs {
+  const void* x;
+  unsigned char *q, *qt;
+  float *s, *st;
+  long long rows, cols, ldx, ldq, ldqt;
+  long long col_tiles;
+  long long srow, strow;  // scales in a row of s and of st
+  int vec;
+};
+
+__device__ __forceinline__ unsigned amax_bits(float a) { return __reduce_max_sync(0xffffffffu, __float_as_uint(a)); }
+
+// One code; values that are not finite become NaN (the conversion would saturate an infinity).
+__device__ __forceinline__ float scaled(float x, float inv) {
+  return finite_f32(x) ? __fmul_rn(x, inv) : __uint_as_float(0x7fc00000u);
+}
+
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, float* o);
+template <>
+__device__ __forceinline__ void load4<float>(const float* p, float* o) {
+  const float4 v = __ldcs(reinterpret_cast<const float4*>(p));
+  o[0] = v.x;
+  o[1] = v.y;
+  o[2] = v.z;
+  o[3] = v.w;
+}
+template <>
+__device__ __forceinline__ void load4<__half>(const __half* p, float* o) {
+  const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+  o[0] = a.x;
+  o[1] = a.y;
+  o[2] = b.x;
+  o[3] = b.y;
+}
+template <>
+__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float* o) {
+  const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+  o[0] = __uint_as_float(v.x << 16);
+  o[1] = __uint_as_float(v.x & 0xffff0000u);
+  o[2] = __uint_as_float(v.y << 16);
+  o[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+
+template <typename T, bool SQUARE>
+__global__ void __launch_bounds__(256, 2) quantize_kernel(const __grid_constant__ QuantArgs a) {
+  __shared__ __align__(16) unsigned char tile_t[kTile * kTile];  // transposed codes, 16-byte chunks swizzled
+  __shared__ float part[8][kTile];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const long long tr = blockIdx.x / a.col_tiles, tc = blockIdx.x % a.col_tiles;
+  const long long r0 = tr * kTile + w * 16, c0 = tc * kTile + lane * 4;
+  const T* x = (const T*)a.x;
+  float v[16][4];
+  const bool whole = a.vec && c0 + 4 <= a.cols;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const long long r = r0 + i;
+    if (r < a.rows && whole) {
+      load4<T>(x + r * a.ldx + c0, v[i]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[i][k] = r < a.rows && c0 + k < a.cols ? to_f32<T>(x[r * a.ldx + c0 + k]) : 0.0f;
+    }
+  }
+  float tile_amax = 0.0f;
+  if (SQUARE) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m = fmaxf(m, finite_abs(v[i][k]));
+    m = __uint_as_float(amax_bits(m));
+    if (lane == 0) part[0][w] = m;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) tile_amax = fmaxf(tile_amax, part[0][j]);
+    tile_amax = fmaxf(tile_amax, kAmaxFloor);
+    if (threadIdx.x == 0) {
+      if (a.s) a.s[tc * a.srow + tr] = scale_of(tile_amax);
+      if (a.st) a.st[tr * a.strow + tc] = scale_of(tile_amax);
+    }
+  }
+  if (a.q) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const long long r = r0 + i;
+      float amax = tile_amax;
+      if (!SQUARE) {
+        amax = fmaxf(fmaxf(finite_abs(v[i][0]), finite_abs(v[i][1])), fmaxf(finite_abs(v[i][2]), finite_abs(v[i][3])));
+        amax = fmaxf(__uint_as_float(amax_bits(amax)), kAmaxFloor);
+        if (lane == 0 && r < a.rows) a.s[tc * a.srow + r] = scale_of(amax);
+      }
+      const float inv = inv_of(amax);
+      const unsigned c = e4m3x2(scaled(v[i][0], inv), scaled(v[i][1], inv)) |
+                         (e4m3x2(scaled(v[i][2], inv), scaled(v[i][3], inv)) << 16);
+      // columns past the last one are zeros up to the row's next 16 bytes
+      if (r < a.rows && c0 < ((a.cols + 15) & ~15LL)) *reinterpret_cast<unsigned*>(a.q + r * a.ldq + c0) = c;
+    }
+  }
+  if (a.qt) {
+    float inv[4];
+    if (SQUARE) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) inv[k] = inv_of(tile_amax);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, finite_abs(v[i][k]));
+        part[w][lane * 4 + k] = m;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float m = kAmaxFloor;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, part[j][lane * 4 + k]);
+        inv[k] = inv_of(m);
+        if (w == 0 && c0 + k < a.cols) a.st[tr * a.strow + c0 + k] = scale_of(m);
+      }
+    }
+    // a lane's column k holds 16 codes of the transposed row 4 lane + k, at chunk w
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      unsigned c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        c[j] = e4m3x2(scaled(v[4 * j][k], inv[k]), scaled(v[4 * j + 1][k], inv[k])) |
+               (e4m3x2(scaled(v[4 * j + 2][k], inv[k]), scaled(v[4 * j + 3][k], inv[k])) << 16);
+      *reinterpret_cast<uint4*>(tile_t + (lane * 4 + k) * kTile + ((w ^ (lane & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
+    }
+    __syncthreads();
+    const long long row_end = (a.rows + 15) & ~15LL;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = j * 256 + threadIdx.x;  // 16-byte chunk of the tile: 8 to a transposed row
+      const int c = at >> 3, chunk = at & 7;
+      const long long col = tc * kTile + c, row = tr * kTile + chunk * 16;
+      if (col < a.cols && row < row_end)
+        *reinterpret_cast<uint4*>(a.qt + col * a.ldqt + row) =
+            *reinterpret_cast<const uint4*>(tile_t + c * kTile + ((chunk ^ ((c >> 2) & 7)) << 4));
+    }
+  }
+}
+
+}  // namespace
+}  // namespace emb
+
+using namespace emb;
+
+extern "C" emb_status emb_fp8_quantize(const void* x_d, emb_ftype x_t, int64_t rows, int64_t cols, int64_t ldx,
+                                       int32_t block_rows, void* q_d, int64_t ldq, float* s_d, void* qt_d, int64_t ldqt,
+                                       float* st_d, void* stream) {
+  if (!good_ftype(x_t)) return fail(EMB_ERR_INVALID_ARG, "bad element type");
+  if (rows < 0 || cols < 0) return fail(EMB_ERR_INVALID_ARG, "negative rows or cols");
+  if (block_rows != 1 && block_rows != EMB_FP8_BLOCK) return fail(EMB_ERR_INVALID_ARG, "block_rows must be 1 or 128");
+  if (rows == 0 || cols == 0) return EMB_OK;
+  if (!q_d && !qt_d) return fail(EMB_ERR_INVALID_ARG, "q and qt are NULL");
+  if ((q_d && !s_d) || (qt_d && !st_d)) return fail(EMB_ERR_INVALID_ARG, "codes need their scales");
+  if (ldx < cols) return fail(EMB_ERR_INVALID_ARG, "ldx below cols");
+  if ((q_d && (ldq < cols || ldq % 16)) || (qt_d && (ldqt < rows || ldqt % 16)))
+    return fail(EMB_ERR_INVALID_ARG, "a row of codes must be a multiple of 16 bytes and hold the row");
+  if (!aligned_to(q_d, 16) || !aligned_to(qt_d, 16)) return fail(EMB_ERR_INVALID_ARG, "codes must be 16-byte aligned");
+  if (!aligned_to(x_d, ftype_bytes(x_t)) || !aligned_to(s_d, 4) || !aligned_to(st_d, 4))
+    return fail(EMB_ERR_INVALID_ARG, "an array is not aligned to its elements");
+  if (!x_d) return fail(EMB_ERR_INVALID_ARG, "x is NULL");
+  const int64_t rt = (rows - 1) / kTile + 1, ct = (cols - 1) / kTile + 1;
+  if (rt > 0x7fffffffLL / ct) return fail(EMB_ERR_UNSUPPORTED, "more than 2^31 - 1 tiles");
+  const bool square = block_rows != 1;
+  const int vec = ldx % 4 == 0 && aligned_to(x_d, 4 * ftype_bytes(x_t));
+  const QuantArgs a{x_d, (unsigned char*)q_d, (unsigned char*)qt_d, q_d ? s_d : nullptr, qt_d ? st_d : nullptr, rows, cols,
+                    ldx, ldq, ldqt, ct, square ? rt : rows, square ? ct : cols, vec};
+  const int grid = (int)(rt * ct);
+  cudaStream_t st = (cudaStream_t)stream;
+#define EMB_QUANT(T)                                                        \
+  do {                                                                      \
+    if (square) quantize_kernel<T, true><<<grid, 256, 0, st>>>(a);          \
+    else quantize_kernel<T, false><<<grid, 256, 0, st>>>(a);                \
+  } while (0)
+  if (x_t == EMB_T_F32) EMB_QUANT(float);
+  else if (x_t == EMB_T_BF16) EMB_QUANT(__nv_bfloat16);
+  else EMB_QUANT(__half);
+#undef EMB_QUANT
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "quantize_kernel launch");
+  return EMB_OK;
+}

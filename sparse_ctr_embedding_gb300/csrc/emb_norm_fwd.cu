@@ -1,0 +1,196 @@
+// Norm, gate, residual and norm in one pass (forward).
+//
+//   y = res_scale * x + act(gate) * (norm(f) * w_post + b_post)
+//   h = norm(y) * w_pre + b_pre
+//
+// Bound by memory: x, f and a per-element gate in, y and h out, once each; the
+// vectors stay in registers over a team's rows.  Two row sums (four for a
+// layer norm) separate the loads from the stores, so each team loads its next
+// row before it reduces the current one.
+#include <algorithm>
+#include <cmath>
+
+#include "emb_norm.cuh"
+
+namespace emb {
+namespace {
+
+struct FwdArgs {
+  const void *x, *f, *gate;
+  const float *w_post, *b_post, *w_pre, *b_pre;
+  void *y, *h;
+  float4* stats;
+  long long rows;
+  int dim, team, gate_kind, act;
+  float eps, res_scale, inv_dim;
+};
+
+// MAXT: most threads of a block.  A thread of a 1024-thread team has 64
+// registers, too few to hold its vectors' elements over the rows: it reads
+// them again from L1 where it needs them.
+template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kernel(const __grid_constant__ FwdArgs a) {
+  __shared__ float2 slots[4][64];  // teams that need them: 64 threads or more, so at most 4 a block
+  const int team = a.team, dim = a.dim;
+  const int my_team = threadIdx.x / team;
+  TeamSum sum{team, (int)threadIdx.x % team, team >> 5, 1 + (my_team & 3), slots[my_team & 3]};
+  const int t = sum.t;
+  const int teams = blockDim.x / team;
+  const long long stride = (long long)gridDim.x * teams;
+  const bool has_f = a.f != nullptr, has_h = a.h != nullptr;
+  const bool gate_elem = a.gate_kind == EMB_GATE_ELEM;
+
+  constexpr bool kHold = MAXT < 1024;
+  const float* const gate_col = a.gate_kind == EMB_GATE_COL ? (const float*)a.gate : nullptr;
+  VecPart<VEC, kHold> wp(a.w_post, 1.0f, t, team, dim), wq(a.w_pre, 1.0f, t, team, dim);
+  VecPart<VEC, kHold> bp(LAYER ? a.b_post : nullptr, 0.0f, t, team, dim), bq(LAYER ? a.b_pre : nullptr, 0.0f, t, team, dim);
+  VecPart<VEC, kHold> gc(gate_col, 0.0f, t, team, dim);
+
+  RowPart<ST, VEC> rx;
+  RowPart<BT, VEC> rf, rg;
+  float grow = 0.0f;
+  auto load = [&](long long r) {
+    rx.load((const ST*)a.x + r * dim, t, team, dim);
+    if (has_f) rf.load((const BT*)a.f + r * dim, t, team, dim);
+    if (gate_elem) rg.load((const BT*)a.gate + r * dim, t, team, dim);
+    if (a.gate_kind == EMB_GATE_ROW) grow = to_f32<BT>(((const BT*)a.gate)[r]);
+  };
+  // norm of v in place; returns (mean, 1/sqrt)
+  auto norm = [&](float* v) {
+    float s = 0.0f, mean = 0.0f;
+    if (LAYER) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
+      mean = sum(s, 0.0f).x * a.inv_dim;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = part_col<VEC>(k, t, team) < dim ? v[k] - mean : 0.0f;
+    }
+    s = 0.0f;  // of v^2 / dim: the sum itself could overflow where the mean does not
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += (v[k] * a.inv_dim) * v[k];
+    const float r = 1.0f / sqrtf(sum(s, 0.0f).x + a.eps);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= r;
+    return make_float2(mean, r);
+  };
+
+  // teams of one warp take rows next to one another, so the loop is uniform over a warp
+  const long long r_first = (long long)blockIdx.x * teams + my_team;
+  const long long rounds = a.rows > (long long)blockIdx.x * teams ? (a.rows - (long long)blockIdx.x * teams + stride - 1) / stride : 0;
+  if (r_first < a.rows) load(r_first);
+  for (long long i = 0; i < rounds; ++i) {
+    const long long r = r_first + i * stride;
+    const bool live = r < a.rows;
+    float x[8], f[8], g[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool in = live && part_col<VEC>(k, t, team) < dim;
+      x[k] = in ? rx.get(k) : 0.0f;
+      f[k] = in && has_f ? rf.get(k) : 0.0f;
+      g[k] = gate_elem ? (in ? activate(rg.get(k), a.act) : 0.0f)
+             : a.gate_kind == EMB_GATE_ROW ? activate(grow, a.act)
+             : gate_col ? activate(gc.get(k), a.act) : 1.0f;
+    }
+    if (r + stride < a.rows) load(r + stride);
+    float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (has_f) {
+      const float2 s = norm(f);
+      st.x = s.x;
+      st.y = s.y;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = x[k] * a.res_scale + g[k] * (LAYER ? f[k] * wp.get(k) + bp.get(k) : f[k] * wp.get(k));
+      if (live) RowPart<ST, VEC>::store((ST*)a.y + r * dim, x, t, team, dim);
+    }
+    if (has_h) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = part_col<VEC>(k, t, team) < dim ? to_f32<ST>(from_f32<ST>(x[k])) : 0.0f;
+      const float2 s = norm(x);
+      st.z = s.x;
+      st.w = s.y;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = LAYER ? x[k] * wq.get(k) + bq.get(k) : x[k] * wq.get(k);
+      if (live) RowPart<BT, VEC>::store((BT*)a.h + r * dim, x, t, team, dim);
+    }
+    if (a.stats && t == 0 && live) a.stats[r] = st;
+  }
+}
+
+template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
+cudaError_t launch_as(const FwdArgs& a, cudaStream_t st) {
+  const int threads = std::max(kNormBlock, a.team);
+  const int teams = threads / a.team;
+  int per_sm = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, norm_gate_fwd_kernel<ST, BT, VEC, LAYER, MAXT>, threads, 0);
+  if (e != cudaSuccess) return e;
+  const long long blocks = std::min((a.rows + teams - 1) / teams, (long long)std::max(1, per_sm) * sm_count());
+  norm_gate_fwd_kernel<ST, BT, VEC, LAYER, MAXT><<<(int)blocks, threads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+template <typename ST, typename BT, bool VEC>
+cudaError_t launch(const FwdArgs& a, bool layer, cudaStream_t st) {
+  if (a.team <= kNormBlock)
+    return layer ? launch_as<ST, BT, VEC, true, kNormBlock>(a, st) : launch_as<ST, BT, VEC, false, kNormBlock>(a, st);
+  if (a.team <= 512) return layer ? launch_as<ST, BT, VEC, true, 512>(a, st) : launch_as<ST, BT, VEC, false, 512>(a, st);
+  return layer ? launch_as<ST, BT, VEC, true, 1024>(a, st) : launch_as<ST, BT, VEC, false, 1024>(a, st);
+}
+
+}  // namespace
+
+emb_status check_norm(const emb_norm_gate_desc* d) {
+  if (!d) return fail(EMB_ERR_INVALID_ARG, "desc is NULL");
+  if (d->rows < 0 || d->dim < 1) return fail(EMB_ERR_INVALID_ARG, "need rows >= 0 and dim >= 1");
+  if (d->dim > EMB_NORM_MAX_DIM) return fail(EMB_ERR_UNSUPPORTED, "dim above EMB_NORM_MAX_DIM");
+  if (d->rows > (1LL << 46)) return fail(EMB_ERR_UNSUPPORTED, "too many rows");
+  if (!good_ftype(d->stream_t) || !good_ftype(d->block_t) ||
+      (d->stream_t != d->block_t && d->stream_t != EMB_T_F32))
+    return fail(EMB_ERR_INVALID_ARG, "stream_t must be block_t or EMB_T_F32");
+  if (d->norm != EMB_NORM_RMS && d->norm != EMB_NORM_LAYER) return fail(EMB_ERR_INVALID_ARG, "bad norm");
+  if (d->gate < EMB_GATE_NONE || d->gate > EMB_GATE_COL) return fail(EMB_ERR_INVALID_ARG, "bad gate");
+  if (d->act != EMB_ACT_IDENTITY && d->act != EMB_ACT_SIGMOID) return fail(EMB_ERR_INVALID_ARG, "bad act");
+  if (!(d->eps > 0) || !std::isfinite(d->eps) || !std::isfinite(d->res_scale))
+    return fail(EMB_ERR_INVALID_ARG, "need eps > 0 and a finite res_scale");
+  return EMB_OK;
+}
+
+}  // namespace emb
+
+using namespace emb;
+
+extern "C" emb_status emb_norm_gate_fwd(const emb_norm_gate_desc* desc, const void* x_d, const void* f_d,
+                                        const void* gate_d, const float* w_post_d, const float* b_post_d,
+                                        const float* w_pre_d, const float* b_pre_d, void* y_d, void* h_d,
+                                        float* stats_d, void* stream) {
+  const emb_status rc = check_norm(desc);
+  if (rc != EMB_OK) return rc;
+  const emb_norm_gate_desc& d = *desc;
+  if (d.rows == 0) return EMB_OK;
+  if (!f_d && (y_d || gate_d || w_post_d || b_post_d || d.gate != EMB_GATE_NONE))
+    return fail(EMB_ERR_INVALID_ARG, "without f there is no y, gate or post vector");
+  if (!h_d && (w_pre_d || b_pre_d)) return fail(EMB_ERR_INVALID_ARG, "without h there is no pre vector");
+  if (d.norm == EMB_NORM_RMS && (b_post_d || b_pre_d)) return fail(EMB_ERR_INVALID_ARG, "biases need EMB_NORM_LAYER");
+  if ((d.gate != EMB_GATE_NONE) != (gate_d != nullptr)) return fail(EMB_ERR_INVALID_ARG, "gate does not match desc->gate");
+  if (!x_d || (f_d && !y_d) || (!f_d && !h_d)) return fail(EMB_ERR_INVALID_ARG, "x, y or h is NULL");
+  const size_t sb = ftype_bytes(d.stream_t), bb = ftype_bytes(d.block_t);
+  const size_t gb = d.gate == EMB_GATE_COL ? 4 : bb;
+  if (!aligned_to(x_d, sb) || !aligned_to(y_d, sb) || !aligned_to(f_d, bb) || !aligned_to(h_d, bb) ||
+      !aligned_to(gate_d, gb) || !aligned_to(w_post_d, 4) || !aligned_to(b_post_d, 4) || !aligned_to(w_pre_d, 4) ||
+      !aligned_to(b_pre_d, 4))
+    return fail(EMB_ERR_INVALID_ARG, "an array is not aligned to its elements");
+  if (!aligned_to(stats_d, 16)) return fail(EMB_ERR_INVALID_ARG, "stats must be 16-byte aligned");
+  const bool vec = d.dim % 8 == 0 && aligned_to(x_d, 8 * sb) && aligned_to(y_d, 8 * sb) && aligned_to(f_d, 8 * bb) &&
+                   aligned_to(h_d, 8 * bb) && (d.gate != EMB_GATE_ELEM || aligned_to(gate_d, 8 * bb));
+  const FwdArgs a{x_d, f_d, gate_d, w_post_d, b_post_d, w_pre_d, b_pre_d, y_d, h_d, (float4*)stats_d, d.rows, d.dim,
+                  norm_team(d.dim), d.gate, d.act, d.eps, d.res_scale, 1.0f / (float)d.dim};
+  const bool layer = d.norm == EMB_NORM_LAYER;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e;
+#define EMB_NORM_FWD(S, B) e = vec ? launch<S, B, true>(a, layer, st) : launch<S, B, false>(a, layer, st)
+  if (d.block_t == EMB_T_F32) EMB_NORM_FWD(float, float);
+  else if (d.block_t == EMB_T_BF16 && d.stream_t == EMB_T_F32) EMB_NORM_FWD(float, __nv_bfloat16);
+  else if (d.block_t == EMB_T_BF16) EMB_NORM_FWD(__nv_bfloat16, __nv_bfloat16);
+  else if (d.stream_t == EMB_T_F32) EMB_NORM_FWD(float, __half);
+  else EMB_NORM_FWD(__half, __half);
+#undef EMB_NORM_FWD
+  if (e != cudaSuccess) return cuda_fail(e, "norm_gate_fwd_kernel launch");
+  return EMB_OK;
+}
