@@ -549,15 +549,16 @@ EMB_API emb_status emb_fp8_quantize(const void* x_d, emb_ftype x_t, int64_t rows
  *   its input grad   dx[B, I] : a = dy, b = W transposed (128)
  *   its weight grad  dW[O, I] : a = dy transposed, b = x transposed (both 1)
  *   a_d, b_d      uint8[m, k] and uint8[n, k], rows lda / ldb bytes apart,
- *                 16-byte aligned, lda and ldb multiples of 16 and >= k.
+ *                 16-byte aligned, lda and ldb multiples of 16 and >= k.  Codes
+ *                 past k are not used, but a row is read in whole 16 bytes.
  *   sa_d, sb_d    float32[ceil(k/128), m or ceil(m/128)], likewise for n.
  *   bias_d        float32[n] or NULL.
  *   out_d         out_t[m, n], rows ldo elements apart, ldo >= n.
  *   workspace_d   emb_fp8_matmul_workspace_size() bytes (may be 0: NULL),
- *                 16-byte aligned; calls that share it must be ordered.
- * The order of the sums depends on the sizes alone, so results repeat
- * bitwise.  k = 0 gives the bias (or zeros).  Errors: INVALID_ARG, WORKSPACE,
- * UNSUPPORTED (m, n or k above 2^31 - 1), CUDA.
+ *                 32-byte aligned; calls that share it must be ordered.
+ * The order of the sums depends on the sizes and the GPU's SM count alone, so
+ * results repeat bitwise.  k = 0 gives the bias (or zeros).  Errors: INVALID_ARG, WORKSPACE,
+ * UNSUPPORTED (m, n or k above 2^31 - 65536), CUDA.
  */
 EMB_API emb_status emb_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
 EMB_API emb_status emb_fp8_matmul(const void* a_d, int64_t lda, const float* sa_d, int32_t a_block_rows,

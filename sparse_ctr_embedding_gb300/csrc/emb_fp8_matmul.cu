@@ -1,5 +1,30 @@
-// Product of two 8-bit block-scaled matrices.
+// Product of two 8-bit block-scaled matrices:
+//   out[i, j] = bias[j] + sum_b sa[b, i] sb[b, j] sum_{k in b} a[i, k] b[j, k]
+// over blocks b of 128 k's.
+//
+// Tile kernel (m > 8).  A persistent block per SM computes tiles of 128 x BN.
+// One warp brings 128-byte-wide slabs of both operands into a ring of shared
+// memory stages by TMA (128-byte swizzle; rows and columns past the edges
+// arrive as zeros); one thread issues four tcgen05.mma (e4m3, K = 32 each) a
+// slab, which sum one scale block in TMEM; eight warps read that sum from TMEM
+// and add it, times its scales, to float32 accumulators in registers.  Two
+// TMEM accumulators alternate, so the tensor cores work on the next block
+// while the last one is scaled.  The scaling costs one f32 multiply-add per
+// 128 products (a multiply more where b's scales differ by column), about half
+// the issue slots of the 512 cycles the block takes the tensor cores at BN 256.
+//
+// Work is cut into (tile, block) steps.  When the tiles fill the SMs several
+// times over, each is one unit; else all steps are split evenly over the SMs
+// (a tile's blocks then come from several SMs: their float32 partial tiles go
+// to the workspace and a second launch adds them in order).  The split depends
+// on the sizes and the SM count alone.
+//
+// Row kernel (m <= 8): bound by reading b once; plain CUDA cores, one or more
+// warps per row of b.
+#include <cuda.h>
+
 #include <algorithm>
+#include <cmath>
 
 #include "emb_dense.cuh"
 
@@ -8,44 +33,596 @@ namespace {
 
 __device__ unsigned g_op_flags;  // EMB_FLAG_OP_* bits since the last emb_check_op_flag
 
+constexpr int kBM = 128;             // rows of a tile
+constexpr int kBK = EMB_FP8_BLOCK;   // k's of a step: one scale block, 128 bytes of a row
+constexpr int kThreads = 320;        // 8 scaling warps, 1 TMA warp, 1 MMA warp
+constexpr int kScaleWarps = 8;
+constexpr unsigned kWaitLimit = 1u << 21;  // polls of one wait before the kernel gives up
+
 struct MatmulArgs {
   const unsigned char *a, *b;
   const float *sa, *sb, *bias;
   void* out;
+  float* partial;            // [slots][kBM][BN]
   long long lda, ldb, ldo;
   long long sa_row, sb_row;  // scales in a row of sa and sb
   int m, n, k;
   int a_shift, b_shift;      // row i's scale is at i >> shift
+  int m_tiles, n_tiles, k_blocks;
+  long long steps;           // m_tiles * n_tiles * k_blocks
+  long long per_cta;         // steps a block takes; 0: whole tiles, block-stride
+  int wide_out;              // rows of out take 32-byte stores
 };
 
-__device__ __forceinline__ float code_to_f32(unsigned char c) { return e4m3x2_to_f32((unsigned short)c).x; }
+// ------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ unsigned smem_u32(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(unsigned bar, unsigned count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(unsigned bar, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(unsigned bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(unsigned bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits for a barrier's phase; false when the limit ran out here or in another
+// warp of the block (`stop`), after which the caller leaves its loops.
+__device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity, volatile int* stop) {
+  if (mbar_try(bar, parity)) return true;
+  for (unsigned i = 0; i < kWaitLimit; ++i) {
+    if (mbar_try(bar, parity)) return true;
+    if (*stop) return false;
+  }
+  *stop = 1;
+  atomicOr(&g_op_flags, EMB_FLAG_OP_TIMEOUT);
+  return false;
+}
+__device__ __forceinline__ void tma_load(unsigned dst, const CUtensorMap* map, int x, int y, unsigned bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit(unsigned bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// D[128 x N] (+)= A B^T, 32 k's, e4m3 operands in shared memory.
+__device__ __forceinline__ void tc_mma(unsigned d, unsigned long long a, unsigned long long b, unsigned idesc, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((unsigned)add)
+      : "memory");
+}
+// 32 columns of this warp's 32 TMEM lanes, one lane a thread, waited for.
+__device__ __forceinline__ void tc_load32(unsigned addr, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
+      "[%32];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+        "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
+        "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(addr)
+      : "memory");
+}
+
+// Shared memory descriptor of a K-major operand: rows of 128 bytes, 128-byte
+// swizzle (layout 2), eight-row groups 1024 bytes apart, descriptor version 1.
+__device__ __forceinline__ unsigned long long smem_desc(unsigned addr) {
+  return (unsigned long long)((addr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// ------------------------------------------------------------------ tile kernel
+
+template <int BN>
+struct TileCfg {
+  static constexpr int kStageBytes = (kBM + BN) * kBK;
+  static constexpr int kStages = (196 * 1024) / kStageBytes;  // 4, 6 or 8
+  static constexpr int kHalf = BN / 2;                        // columns of a scaling warp
+  static constexpr int kScaleBytes = kScaleWarps * 2 * kHalf * 4;
+  static constexpr int kBytes = kStages * kStageBytes + kScaleBytes + 1024;  // + room to align
+};
+
+struct Unit {  // consecutive blocks of one tile
+  int tm, tn, kb0, kb1;
+  long long tile;
+};
+
+// Tiles in groups of 16 rows of tiles, column by column within a group: the
+// blocks at work at one time then share few slabs of a and b in L2.
+__device__ __forceinline__ void tile_at(const MatmulArgs& p, long long t, int* tm, int* tn) {
+  constexpr int kGroup = 16;
+  const long long per_group = (long long)kGroup * p.n_tiles;
+  const int g = (int)(t / per_group);
+  const int in = (int)(t - g * per_group);
+  const int rows = min(kGroup, p.m_tiles - g * kGroup);
+  *tm = g * kGroup + in % rows;
+  *tn = in / rows;
+}
+
+// The block's next unit from its position: a tile number, or a step.
+__device__ __forceinline__ bool next_unit(const MatmulArgs& p, long long* pos, long long end, Unit* u) {
+  if (*pos >= end) return false;
+  if (p.per_cta == 0) {
+    u->tile = *pos;
+    u->kb0 = 0;
+    u->kb1 = p.k_blocks;
+    *pos += gridDim.x;
+  } else {
+    u->tile = *pos / p.k_blocks;
+    u->kb0 = (int)(*pos - u->tile * p.k_blocks);
+    u->kb1 = (int)min((long long)p.k_blocks, u->kb0 + (end - *pos));
+    *pos += u->kb1 - u->kb0;
+  }
+  tile_at(p, u->tile, &u->tm, &u->tn);
+  return true;
+}
+__device__ __forceinline__ void my_range(const MatmulArgs& p, long long* pos, long long* end) {
+  if (p.per_cta == 0) {
+    *pos = blockIdx.x;
+    *end = (long long)p.m_tiles * p.n_tiles;
+  } else {
+    *pos = blockIdx.x * p.per_cta;
+    *end = min(p.steps, *pos + p.per_cta);
+  }
+}
 
 template <typename OT>
-__global__ void __launch_bounds__(256) matmul_kernel(const __grid_constant__ MatmulArgs p) {
-  __shared__ float as[32][129], bs[32][129];
-  const int i0 = blockIdx.y * 32, j0 = blockIdx.x * 32;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  float acc[4] = {};
-  for (int kb = 0; kb < (p.k + 127) / 128; ++kb) {
-    for (int e = threadIdx.x; e < 32 * 128; e += 256) {
-      const int r = e >> 7, c = e & 127, k = kb * 128 + c;
-      as[r][c] = i0 + r < p.m && k < p.k ? code_to_f32(p.a[(i0 + r) * p.lda + k]) : 0.0f;
-      bs[r][c] = j0 + r < p.n && k < p.k ? code_to_f32(p.b[(j0 + r) * p.ldb + k]) : 0.0f;
+__device__ __forceinline__ void store32(OT* dst, const float* v) {  // 32 bytes
+  if constexpr (sizeof(OT) == 4) {
+    Raw8<float> r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.set2(i, v[2 * i], v[2 * i + 1]);
+    r.store((float*)dst);
+  } else {
+    Raw8<OT> lo, hi;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo.set2(i, v[2 * i], v[2 * i + 1]);
+      hi.set2(i, v[8 + 2 * i], v[8 + 2 * i + 1]);
     }
-    __syncthreads();
-    for (int q = 0; q < 4; ++q) {
-      const int i = i0 + ty + 8 * q, j = j0 + tx;
-      float s = 0.0f;
-      for (int c = 0; c < 128; ++c) s += as[ty + 8 * q][c] * bs[tx][c];
-      if (i < p.m && j < p.n)
-        acc[q] += s * (p.sa[kb * p.sa_row + (i >> p.a_shift)] * p.sb[kb * p.sb_row + (j >> p.b_shift)]);
+    const unsigned* a = reinterpret_cast<const unsigned*>(lo.v);
+    const unsigned* b = reinterpret_cast<const unsigned*>(hi.v);
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]),
+                 "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3])
+                 : "memory");
+  }
+}
+
+// BCOL: b's scales differ by column (else one per 128 columns: one a warp).
+template <int BN, typename OT, bool BCOL>
+__global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap map_a,
+                                                           const __grid_constant__ CUtensorMap map_b,
+                                                           const __grid_constant__ MatmulArgs p) {
+  using C = TileCfg<BN>;
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) unsigned long long bars[2 * C::kStages + 4];
+  __shared__ unsigned tmem_slot;
+  __shared__ int stop_flag;
+  volatile int* stop = &stop_flag;
+  const unsigned smem = (smem_u32(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned full0 = smem_u32(bars), empty0 = full0 + 8 * C::kStages, tfull0 = empty0 + 8 * C::kStages, tempty0 = tfull0 + 16;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
     }
-    __syncthreads();
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(tfull0 + 8 * t, 1);
+      mbar_init(tempty0 + 8 * t, kScaleWarps);
+    }
+    stop_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int q = 0; q < 4; ++q) {
-    const int i = i0 + ty + 8 * q, j = j0 + tx;
-    if (i < p.m && j < p.n) ((OT*)p.out)[i * p.ldo + j] = from_f32<OT>(acc[q] + (p.bias ? p.bias[j] : 0.0f));
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(2 * BN) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const unsigned tmem = tmem_slot;
+
+  long long pos, end;
+  my_range(p, &pos, &end);
+  Unit u;
+
+  if (warp == 8) {
+    if (lane == 0) {  // TMA: both slabs of each step
+      unsigned it = 0;
+      bool go = true;
+      while (go && next_unit(p, &pos, end, &u)) {
+        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+          const unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
+          if (!mbar_wait(empty0 + 8 * s, ph ^ 1, stop)) {
+            go = false;
+            break;
+          }
+          const unsigned dst = smem + s * C::kStageBytes, bar = full0 + 8 * s;
+          mbar_expect_tx(bar, C::kStageBytes);
+          tma_load(dst, &map_a, kb * kBK, u.tm * kBM, bar);
+          tma_load(dst + kBM * kBK, &map_b, kb * kBK, u.tn * BN, bar);
+        }
+      }
+      if (!go) {  // gave up: the loads in flight must land before the block ends
+        const unsigned n = min(it, (unsigned)C::kStages);
+        for (unsigned j = it - n; j < it; ++j)
+          for (unsigned i = 0; i < kWaitLimit && !mbar_try(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1); ++i) {}
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0) {  // MMA
+      // f32 accumulator, e4m3 x e4m3, both K-major, N = BN, M = 128
+      constexpr unsigned idesc = (1u << 4) | ((BN >> 3) << 17) | ((kBM >> 4) << 24);
+      unsigned it = 0;
+      bool go = true;
+      while (go && next_unit(p, &pos, end, &u)) {
+        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+          const unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
+          const unsigned t = it & 1, tph = (it >> 1) & 1;
+          if (!mbar_wait(tempty0 + 8 * t, tph ^ 1, stop) || !mbar_wait(full0 + 8 * s, ph, stop)) {
+            go = false;
+            break;
+          }
+          tc_fence_after();
+          const unsigned at = smem + s * C::kStageBytes;
+          const unsigned long long da = smem_desc(at), db = smem_desc(at + kBM * kBK);
+#pragma unroll
+          for (int j = 0; j < kBK / 32; ++j) tc_mma(tmem + t * BN, da + 2 * j, db + 2 * j, idesc, j > 0);
+          tc_commit(empty0 + 8 * s);
+          tc_commit(tfull0 + 8 * t);
+        }
+      }
+      if (!go && it > 0) {  // gave up: wait for the products in flight before TMEM is freed
+        const unsigned j = it - 1;
+        for (unsigned i = 0; i < kWaitLimit && !mbar_try(tfull0 + 8 * (j & 1), (j >> 1) & 1); ++i) {}
+      }
+    }
+    __syncwarp();
+  } else {  // scaling warps: TMEM lanes 32 (warp % 4).., columns half (warp / 4)
+    const int half = warp >> 2, quarter = warp & 3;
+    float* sbuf = reinterpret_cast<float*>(raw + (smem - smem_u32(raw)) + C::kStages * C::kStageBytes) + warp * 2 * C::kHalf;
+    unsigned it = 0;
+    bool go = true;
+    while (go && next_unit(p, &pos, end, &u)) {
+      const int row = u.tm * kBM + quarter * 32 + lane;
+      const int col0 = u.tn * BN + half * C::kHalf;
+      const float* sa = p.sa + (min(row, p.m - 1) >> p.a_shift);
+      float acc[C::kHalf];
+#pragma unroll
+      for (int c = 0; c < C::kHalf; ++c) acc[c] = 0.0f;
+      constexpr int kPer = (C::kHalf + 31) / 32;  // b's scales a lane fetches
+      float sa_next = sa[u.kb0 * p.sa_row], sb_next[BCOL ? kPer : 1];
+      auto fetch_b = [&](int kb) {
+        if constexpr (BCOL) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int c = min(col0 + i * 32 + lane, p.n - 1);
+            sb_next[i] = __ldg(p.sb + kb * p.sb_row + (c >> p.b_shift));
+          }
+        } else {
+          sb_next[0] = __ldg(p.sb + kb * p.sb_row + (min(col0, p.n - 1) >> p.b_shift));
+        }
+      };
+      fetch_b(u.kb0);
+      for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+        const unsigned t = it & 1, tph = (it >> 1) & 1;
+        float s = sa_next;
+        float* sb = sbuf + t * C::kHalf;
+        if constexpr (BCOL) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) sb[i * 32 + lane] = sb_next[i];
+          __syncwarp();
+        } else {
+          s *= sb_next[0];
+        }
+        if (kb + 1 < u.kb1) {
+          sa_next = __ldg(sa + (kb + 1) * p.sa_row);
+          fetch_b(kb + 1);
+        }
+        go = mbar_wait(tfull0 + 8 * t, tph, stop);
+        go = __all_sync(0xffffffffu, go);
+        if (!go) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < C::kHalf; c += 32) {
+          float v[32];
+          tc_load32(tmem + ((unsigned)(quarter * 32) << 16) + t * BN + half * C::kHalf + c, v);
+          if (c + 32 == C::kHalf) {  // the last of this accumulator: the MMA may write it again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty0 + 8 * t);
+          }
+          if constexpr (BCOL) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 b = *reinterpret_cast<const float4*>(sb + c + j);
+              acc[c + j] = fmaf(v[j], s * b.x, acc[c + j]);
+              acc[c + j + 1] = fmaf(v[j + 1], s * b.y, acc[c + j + 1]);
+              acc[c + j + 2] = fmaf(v[j + 2], s * b.z, acc[c + j + 2]);
+              acc[c + j + 3] = fmaf(v[j + 3], s * b.w, acc[c + j + 3]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(v[j], s, acc[c + j]);
+          }
+        }
+      }
+      if (!go) break;
+      if (u.kb0 == 0 && u.kb1 == p.k_blocks) {
+        if (row < p.m) {
+          OT* dst = (OT*)p.out + row * p.ldo + col0;
+          constexpr int kVec = 32 / sizeof(OT);
+#pragma unroll
+          for (int c = 0; c < C::kHalf; c += kVec) {
+            if (p.bias) {
+#pragma unroll
+              for (int j = 0; j < kVec; ++j)
+                if (col0 + c + j < p.n) acc[c + j] += __ldg(p.bias + col0 + c + j);
+            }
+            if (p.wide_out && col0 + c + kVec <= p.n) {
+              store32<OT>(dst + c, acc + c);
+            } else {
+#pragma unroll
+              for (int j = 0; j < kVec; ++j)
+                if (col0 + c + j < p.n) dst[c + j] = from_f32<OT>(acc[c + j]);
+            }
+          }
+        }
+      } else if (row < p.m) {  // part of a tile: slot (block + tile) is this piece's alone
+        float* dst = p.partial + ((long long)(blockIdx.x + u.tile) * kBM + quarter * 32 + lane) * BN + half * C::kHalf;
+#pragma unroll
+        for (int c = 0; c < C::kHalf; c += 8) store32<float>(dst + c, acc + c);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN));
+  }
+}
+
+// Adds the pieces of each tile that several blocks computed, in k order.  One
+// block takes 16 rows of a tile.
+template <int BN, typename OT>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ MatmulArgs p) {
+  const long long tile = blockIdx.x / (kBM / 16);
+  const int r0 = (int)(blockIdx.x % (kBM / 16)) * 16;
+  const long long first = tile * p.k_blocks / p.per_cta, last = ((tile + 1) * p.k_blocks - 1) / p.per_cta;
+  if (first == last) return;  // one block had it whole
+  int tm, tn;
+  tile_at(p, tile, &tm, &tn);
+  for (int e = threadIdx.x; e < 16 * BN / 4; e += 256) {
+    const int r = r0 + e / (BN / 4), c = e % (BN / 4) * 4;
+    const int row = tm * kBM + r, col = tn * BN + c;
+    if (row >= p.m || col >= p.n) continue;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float* src = p.partial + ((first + tile) * kBM + r) * BN + c;
+#pragma unroll 4
+    for (long long b = first; b <= last; ++b, src += (long long)kBM * BN) {
+      const float4 w = *reinterpret_cast<const float4*>(src);
+      v.x += w.x;
+      v.y += w.y;
+      v.z += w.z;
+      v.w += w.w;
+    }
+    const float o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col + j < p.n) ((OT*)p.out)[row * p.ldo + col + j] = from_f32<OT>(o[j] + (p.bias ? __ldg(p.bias + col + j) : 0.0f));
+  }
+}
+
+// ------------------------------------------------------------------ row kernel
+
+constexpr int kRowMax = 8;
+
+// 16 codes as floats.
+__device__ __forceinline__ void codes16(const uint4& q, float* o) {
+  const unsigned w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = e4m3x2_to_f32((unsigned short)(w[i] & 0xffffu)), b = e4m3x2_to_f32((unsigned short)(w[i] >> 16));
+    o[4 * i] = a.x;
+    o[4 * i + 1] = a.y;
+    o[4 * i + 2] = b.x;
+    o[4 * i + 3] = b.y;
+  }
+}
+// Clears the codes from `keep` on (keep < 16).
+__device__ __forceinline__ uint4 head16(uint4 q, int keep) {
+  unsigned w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int left = keep - 4 * i;
+    w[i] = left >= 4 ? w[i] : left <= 0 ? 0u : w[i] & ((1u << (8 * left)) - 1u);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A block's eight warps take 8 / S rows of b, S warps to a row; a lane takes 16
+// neighbouring k's (one scale block for eight lanes) every 512 S.
+template <int M, int S, typename OT>
+__global__ void __launch_bounds__(256) row_kernel(const __grid_constant__ MatmulArgs p) {
+  constexpr int kRows = 8 / S;
+  __shared__ float part[8][M];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j = blockIdx.x * kRows + warp / S;
+  float acc[M];
+#pragma unroll
+  for (int i = 0; i < M; ++i) acc[i] = 0.0f;
+  if (j < p.n) {
+    const unsigned char* b = p.b + j * p.ldb;
+    const float* sb = p.sb + (j >> p.b_shift);
+#pragma unroll 4
+    for (int k = ((warp % S) * 32 + lane) * 16; k < p.k; k += S * 512) {
+      const int kb = k / kBK;
+      uint4 q = __ldg(reinterpret_cast<const uint4*>(b + k));  // rows are multiples of 16 bytes: in bounds
+      if (k + 16 > p.k) q = head16(q, p.k - k);
+      float w[16];
+      codes16(q, w);
+      const float s = __ldg(sb + kb * p.sb_row);
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        if (i < p.m) {
+          uint4 qa = __ldg(reinterpret_cast<const uint4*>(p.a + i * p.lda + k));
+          if (k + 16 > p.k) qa = head16(qa, p.k - k);
+          float x[16], d = 0.0f;
+          codes16(qa, x);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) d = fmaf(x[c], w[c], d);
+          acc[i] = fmaf(d, s * __ldg(p.sa + kb * p.sa_row + (i >> p.a_shift)), acc[i]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    for (int o = 16; o; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    if (lane == 0) part[warp][i] = acc[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < kRows * M) {
+    const int r = threadIdx.x / M, i = threadIdx.x % M, col = blockIdx.x * kRows + r;
+    if (col < p.n && i < p.m) {
+      float v = 0.0f;
+#pragma unroll
+      for (int s = 0; s < S; ++s) v += part[r * S + s][i];
+      ((OT*)p.out)[i * p.ldo + col] = from_f32<OT>(v + (p.bias ? __ldg(p.bias + col) : 0.0f));
+    }
+  }
+}
+
+// out = bias: a product over no k's.
+template <typename OT>
+__global__ void __launch_bounds__(256) bias_kernel(const __grid_constant__ MatmulArgs p) {
+  for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < (long long)p.m * p.n; e += (long long)gridDim.x * 256) {
+    const long long i = e / p.n, j = e - i * p.n;
+    ((OT*)p.out)[i * p.ldo + j] = from_f32<OT>(p.bias ? p.bias[j] : 0.0f);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+struct Plan {
+  int bn = 0;             // 0: row kernel
+  int m_tiles = 0, n_tiles = 0, k_blocks = 0;
+  long long per_cta = 0;  // steps a block, 0: whole tiles
+  int grid = 0;
+  size_t ws_bytes = 0;
+};
+
+Plan make_plan(long long m, long long n, long long k) {
+  Plan pl;
+  if (m == 0 || n == 0 || k == 0) return pl;
+  pl.k_blocks = (int)((k + kBK - 1) / kBK);
+  if (m <= kRowMax) return pl;
+  const int sms = sm_count();
+  const long long mt = (m + kBM - 1) / kBM;
+  // The widest tile that the work fills: with less than eight steps of it for
+  // each SM, narrower ones keep the pieces and their joining small.
+  pl.bn = 256;
+  while (pl.bn > 64 && (n <= pl.bn / 2 || mt * ((n + pl.bn - 1) / pl.bn) * pl.k_blocks < 8LL * sms)) pl.bn /= 2;
+  pl.m_tiles = (int)mt;
+  pl.n_tiles = (int)((n + pl.bn - 1) / pl.bn);
+  const long long tiles = mt * pl.n_tiles, steps = tiles * pl.k_blocks;
+  // Whole tiles when the last round of them leaves less than a tenth of the time idle, or a tile is one block long.
+  const long long rounds = (tiles + sms - 1) / sms;
+  if (pl.k_blocks == 1 || tiles * 10 >= rounds * sms * 9) {
+    pl.grid = (int)std::min<long long>(tiles, sms);
+  } else {
+    pl.per_cta = std::max<long long>((steps + sms - 1) / sms, std::min(2, pl.k_blocks));
+    pl.grid = (int)((steps + pl.per_cta - 1) / pl.per_cta);
+    pl.ws_bytes = (size_t)(pl.grid + tiles) * kBM * pl.bn * sizeof(float);
+  }
+  return pl;
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (EncodeTiled)f;
+  }();
+  return fn;
+}
+
+// Slabs of 128 k's by `box_rows` rows of a code matrix; what lies outside is read as zeros.
+bool make_map(CUtensorMap* map, const void* base, long long rows, long long k, long long ld, int box_rows) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
+  const cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)box_rows}, step[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, typename OT>
+cudaError_t launch_tiles(const MatmulArgs& p, const Plan& pl, const CUtensorMap& ma, const CUtensorMap& mb, cudaStream_t st) {
+  auto* k = p.b_shift ? tile_kernel<BN, OT, false> : tile_kernel<BN, OT, true>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<BN>::kBytes);
+  if (e != cudaSuccess) return e;
+  k<<<pl.grid, kThreads, TileCfg<BN>::kBytes, st>>>(ma, mb, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || pl.per_cta == 0) return e;
+  join_kernel<BN, OT><<<pl.m_tiles * pl.n_tiles * (kBM / 16), 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int M, typename OT>
+cudaError_t launch_rows(const MatmulArgs& p, cudaStream_t st) {
+  // four warps to a row of b when there are too few rows to fill the SMs with one each
+  if (p.k > 1024 && p.n < 32 * sm_count()) row_kernel<M, 4, OT><<<(p.n + 1) / 2, 256, 0, st>>>(p);
+  else row_kernel<M, 1, OT><<<(p.n + 7) / 8, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename OT>
+cudaError_t launch(const MatmulArgs& p, const Plan& pl, const CUtensorMap& ma, const CUtensorMap& mb, cudaStream_t st) {
+  if (p.k == 0) {
+    bias_kernel<OT><<<(int)std::min<long long>(((long long)p.m * p.n + 255) / 256, 8LL * sm_count()), 256, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  if (pl.bn == 0) {
+    if (p.m == 1) return launch_rows<1, OT>(p, st);
+    if (p.m == 2) return launch_rows<2, OT>(p, st);
+    if (p.m <= 4) return launch_rows<4, OT>(p, st);
+    return launch_rows<8, OT>(p, st);
+  }
+  if (pl.bn == 64) return launch_tiles<64, OT>(p, pl, ma, mb, st);
+  if (pl.bn == 128) return launch_tiles<128, OT>(p, pl, ma, mb, st);
+  return launch_tiles<256, OT>(p, pl, ma, mb, st);
 }
 
 }  // namespace
@@ -56,8 +633,11 @@ using namespace emb;
 extern "C" emb_status emb_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes) {
   if (!bytes) return fail(EMB_ERR_INVALID_ARG, "bytes is NULL");
   if (m < 0 || n < 0 || k < 0) return fail(EMB_ERR_INVALID_ARG, "negative m, n or k");
-  if (m > 0x7fffffffLL || n > 0x7fffffffLL || k > 0x7fffffffLL) return fail(EMB_ERR_UNSUPPORTED, "m, n or k above 2^31 - 1");
-  *bytes = 0;
+  if (m > 0x7fff0000LL || n > 0x7fff0000LL || k > 0x7fff0000LL) return fail(EMB_ERR_UNSUPPORTED, "m, n or k above 2^31 - 65536");
+  const Plan pl = make_plan(m, n, k);
+  if (pl.bn && (long long)pl.m_tiles * pl.n_tiles > 0x7fffffffLL / (kBM / 16))
+    return fail(EMB_ERR_UNSUPPORTED, "m * n too large");
+  *bytes = pl.ws_bytes;
   return EMB_OK;
 }
 
@@ -72,6 +652,7 @@ extern "C" emb_status emb_fp8_matmul(const void* a_d, int64_t lda, const float* 
   if ((a_block_rows != 1 && a_block_rows != EMB_FP8_BLOCK) || (b_block_rows != 1 && b_block_rows != EMB_FP8_BLOCK))
     return fail(EMB_ERR_INVALID_ARG, "block_rows must be 1 or 128");
   if (lda < k || ldb < k || lda % 16 || ldb % 16) return fail(EMB_ERR_INVALID_ARG, "a row of codes must be a multiple of 16 bytes and hold k");
+  if (lda >= (1LL << 39) || ldb >= (1LL << 39)) return fail(EMB_ERR_UNSUPPORTED, "rows of codes over 2^39 bytes apart");
   if (ldo < n) return fail(EMB_ERR_INVALID_ARG, "ldo below n");
   if (m == 0 || n == 0) return EMB_OK;
   if (!out_d || (k > 0 && (!a_d || !b_d || !sa_d || !sb_d))) return fail(EMB_ERR_INVALID_ARG, "a, b, a scale or out is NULL");
@@ -80,18 +661,23 @@ extern "C" emb_status emb_fp8_matmul(const void* a_d, int64_t lda, const float* 
     return fail(EMB_ERR_INVALID_ARG, "an array is not aligned to its elements");
   if (need && (!workspace_d || ws_bytes < need))
     return fail(EMB_ERR_WORKSPACE, "workspace missing or smaller than emb_fp8_matmul_workspace_size()");
-  if (need && !aligned_to(workspace_d, 16)) return fail(EMB_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+  if (need && !aligned_to(workspace_d, 32)) return fail(EMB_ERR_WORKSPACE, "workspace must be 32-byte aligned");
+  const Plan pl = make_plan(m, n, k);
   const int as = a_block_rows == 1 ? 0 : 7, bs = b_block_rows == 1 ? 0 : 7;
-  const MatmulArgs p{(const unsigned char*)a_d, (const unsigned char*)b_d, sa_d, sb_d, bias_d, out_d, lda, ldb, ldo,
-                     as ? (m + 127) / 128 : m, bs ? (n + 127) / 128 : n, (int)m, (int)n, (int)k, as, bs};
-  const dim3 grid((unsigned)((n + 31) / 32), (unsigned)((m + 31) / 32));
-  if (grid.y > 65535u) return fail(EMB_ERR_UNSUPPORTED, "m too large");
+  const size_t ob = ftype_bytes(out_t);
+  const MatmulArgs p{(const unsigned char*)a_d, (const unsigned char*)b_d, sa_d, sb_d, bias_d, out_d, (float*)workspace_d,
+                     lda, ldb, ldo, as ? (m + 127) / 128 : m, bs ? (n + 127) / 128 : n, (int)m, (int)n, (int)k, as, bs,
+                     pl.m_tiles, pl.n_tiles, pl.k_blocks, (long long)pl.m_tiles * pl.n_tiles * pl.k_blocks, pl.per_cta,
+                     aligned_to(out_d, 32) && (ldo * ob) % 32 == 0};
+  CUtensorMap ma{}, mb{};
+  if (pl.bn && (!make_map(&ma, a_d, m, k, lda, kBM) || !make_map(&mb, b_d, n, k, ldb, pl.bn)))
+    return fail(EMB_ERR_CUDA, "cuTensorMapEncodeTiled failed or is not available");
   cudaStream_t st = (cudaStream_t)stream;
-  if (out_t == EMB_T_F32) matmul_kernel<float><<<grid, 256, 0, st>>>(p);
-  else if (out_t == EMB_T_BF16) matmul_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
-  else matmul_kernel<__half><<<grid, 256, 0, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "matmul_kernel launch");
+  cudaError_t e;
+  if (out_t == EMB_T_F32) e = launch<float>(p, pl, ma, mb, st);
+  else if (out_t == EMB_T_BF16) e = launch<__nv_bfloat16>(p, pl, ma, mb, st);
+  else e = launch<__half>(p, pl, ma, mb, st);
+  if (e != cudaSuccess) return cuda_fail(e, "emb_fp8_matmul launch");
   return EMB_OK;
 }
 
