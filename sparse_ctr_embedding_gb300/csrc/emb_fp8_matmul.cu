@@ -35,8 +35,12 @@ __device__ unsigned g_op_flags;  // EMB_FLAG_OP_* bits since the last emb_check_
 
 constexpr int kBM = 128;             // rows of a tile
 constexpr int kBK = EMB_FP8_BLOCK;   // k's of a step: one scale block, 128 bytes of a row
-constexpr int kThreads = 320;        // 8 scaling warps, 1 TMA warp, 1 MMA warp
 constexpr int kScaleWarps = 8;
+constexpr int kThreads = 384;        // 8 scaling warps; then 1 TMA warp, 1 MMA warp, 2 idle
+// Registers: 384 x 168 at launch; the scaling warps' accumulators need more and
+// the other four warps little: 256 x 224 + 128 x 56 = 384 x 168.
+constexpr int kScaleRegs = 224, kOtherRegs = 56;
+static_assert(256 * kScaleRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
 constexpr unsigned kWaitLimit = 1u << 21;  // polls of one wait before the kernel gives up
 
 struct MatmulArgs {
@@ -109,19 +113,48 @@ __device__ __forceinline__ void tc_mma(unsigned d, unsigned long long a, unsigne
       "l"(a), "l"(b), "r"(idesc), "r"((unsigned)add)
       : "memory");
 }
-// 32 columns of this warp's 32 TMEM lanes, one lane a thread, waited for.
-__device__ __forceinline__ void tc_load32(unsigned addr, float* v) {
+// Starts reading 32 columns of this warp's 32 TMEM lanes, one lane a thread.
+__device__ __forceinline__ void tc_load32(unsigned addr, unsigned* v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
-      "[%32];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
-        "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]),
-        "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
-        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      "[%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+        "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(addr)
       : "memory");
+}
+// Waits for the loads above; the registers pass through so that no use of them moves before it.
+__device__ __forceinline__ void tc_wait32(unsigned* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
+                 "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                 "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
+}
+// Two floats in a 64-bit register, and their multiply-add (one issue slot for two).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(unsigned lo, unsigned hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  unsigned lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
 }
 
 // Shared memory descriptor of a K-major operand: rows of 128 bytes, 128-byte
@@ -247,8 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   my_range(p, &pos, &end);
   Unit u;
 
-  if (warp == 8) {
-    if (lane == 0) {  // TMA: both slabs of each step
+  if (warp >= kScaleWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8 && lane == 0) {  // TMA: both slabs of each step
       unsigned it = 0;
       bool go = true;
       while (go && next_unit(p, &pos, end, &u)) {
@@ -270,9 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           for (unsigned i = 0; i < kWaitLimit && !mbar_try(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1); ++i) {}
       }
     }
-    __syncwarp();
-  } else if (warp == 9) {
-    if (lane == 0) {  // MMA
+    if (warp == 9 && lane == 0) {  // MMA
       // f32 accumulator, e4m3 x e4m3, both K-major, N = BN, M = 128
       constexpr unsigned idesc = (1u << 4) | ((BN >> 3) << 17) | ((kBM >> 4) << 24);
       unsigned it = 0;
@@ -301,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     }
     __syncwarp();
   } else {  // scaling warps: TMEM lanes 32 (warp % 4).., columns half (warp / 4)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kScaleRegs));
     const int half = warp >> 2, quarter = warp & 3;
     float* sbuf = reinterpret_cast<float*>(raw + (smem - smem_u32(raw)) + C::kStages * C::kStageBytes) + warp * 2 * C::kHalf;
     unsigned it = 0;
@@ -309,9 +342,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       const int row = u.tm * kBM + quarter * 32 + lane;
       const int col0 = u.tn * BN + half * C::kHalf;
       const float* sa = p.sa + (min(row, p.m - 1) >> p.a_shift);
-      float acc[C::kHalf];
+      f32x2 acc2[C::kHalf / 2];
 #pragma unroll
-      for (int c = 0; c < C::kHalf; ++c) acc[c] = 0.0f;
+      for (int c = 0; c < C::kHalf / 2; ++c) acc2[c] = 0;
       constexpr int kPer = (C::kHalf + 31) / 32;  // b's scales a lane fetches
       float sa_next = sa[u.kb0 * p.sa_row], sb_next[BCOL ? kPer : 1];
       auto fetch_b = [&](int kb) {
@@ -345,31 +378,44 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         go = __all_sync(0xffffffffu, go);
         if (!go) break;
         tc_fence_after();
+        const f32x2 s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+        const unsigned taddr = tmem + ((unsigned)(quarter * 32) << 16) + t * BN + half * C::kHalf;
+        constexpr int kChunks = C::kHalf / 32;
+        unsigned v[2][32];
+        tc_load32(taddr, v[0]);
 #pragma unroll
-        for (int c = 0; c < C::kHalf; c += 32) {
-          float v[32];
-          tc_load32(tmem + ((unsigned)(quarter * 32) << 16) + t * BN + half * C::kHalf + c, v);
-          if (c + 32 == C::kHalf) {  // the last of this accumulator: the MMA may write it again
+        for (int c = 0; c < kChunks; ++c) {  // the next 32 columns are on their way while these are added
+          tc_wait32(v[c & 1]);
+          if (c + 1 < kChunks) {
+            tc_load32(taddr + (c + 1) * 32, v[(c + 1) & 1]);
+          } else {  // all of this accumulator is in registers: the MMA may write it again
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty0 + 8 * t);
           }
-          if constexpr (BCOL) {
+          const unsigned* w = v[c & 1];
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 b = *reinterpret_cast<const float4*>(sb + c + j);
-              acc[c + j] = fmaf(v[j], s * b.x, acc[c + j]);
-              acc[c + j + 1] = fmaf(v[j + 1], s * b.y, acc[c + j + 1]);
-              acc[c + j + 2] = fmaf(v[j + 2], s * b.z, acc[c + j + 2]);
-              acc[c + j + 3] = fmaf(v[j + 3], s * b.w, acc[c + j + 3]);
+          for (int j = 0; j < 32; j += 4) {
+            f32x2* a2 = acc2 + (c * 32 + j) / 2;
+            if constexpr (BCOL) {
+              const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(sb + c * 32 + j);
+              a2[0] = fma2(pack2(w[j], w[j + 1]), mul2(s2, b.x), a2[0]);
+              a2[1] = fma2(pack2(w[j + 2], w[j + 3]), mul2(s2, b.y), a2[1]);
+            } else {
+              a2[0] = fma2(pack2(w[j], w[j + 1]), s2, a2[0]);
+              a2[1] = fma2(pack2(w[j + 2], w[j + 3]), s2, a2[1]);
             }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(v[j], s, acc[c + j]);
           }
         }
       }
       if (!go) break;
+      float acc[C::kHalf];
+#pragma unroll
+      for (int c = 0; c < C::kHalf / 2; ++c) {
+        const float2 x = unpack2(acc2[c]);
+        acc[2 * c] = x.x;
+        acc[2 * c + 1] = x.y;
+      }
       if (u.kb0 == 0 && u.kb1 == p.k_blocks) {
         if (row < p.m) {
           OT* dst = (OT*)p.out + row * p.ldo + col0;
