@@ -41,6 +41,7 @@ constexpr int kThreads = 384;        // 8 scaling warps; then 1 TMA warp, 1 MMA 
 // the other four warps little: 256 x 224 + 128 x 56 = 384 x 168.
 constexpr int kScaleRegs = 224, kOtherRegs = 56;
 static_assert(256 * kScaleRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
+constexpr int kAhead = 4;            // steps whose scales are held or on their way
 constexpr unsigned kWaitLimit = 1u << 21;  // polls of one wait before the kernel gives up
 
 struct MatmulArgs {
@@ -170,7 +171,7 @@ struct TileCfg {
   static constexpr int kStageBytes = (kBM + BN) * kBK;
   static constexpr int kStages = (196 * 1024) / kStageBytes;  // 4, 6 or 8
   static constexpr int kHalf = BN / 2;                        // columns of a scaling warp
-  static constexpr int kScaleBytes = kScaleWarps * 2 * kHalf * 4;
+  static constexpr int kScaleBytes = kScaleWarps * kAhead * (32 + kHalf) * 4;
   static constexpr int kBytes = kStages * kStageBytes + kScaleBytes + 1024;  // + room to align
 };
 
@@ -335,50 +336,68 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   } else {  // scaling warps: TMEM lanes 32 (warp % 4).., columns half (warp / 4)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kScaleRegs));
     const int half = warp >> 2, quarter = warp & 3;
-    float* sbuf = reinterpret_cast<float*>(raw + (smem - smem_u32(raw)) + C::kStages * C::kStageBytes) + warp * 2 * C::kHalf;
+    // The scales of this warp's rows and columns come by 4-byte asynchronous
+    // copies (their rows have no alignment) into a ring of its own, kAhead - 1
+    // steps ahead and on into its next tiles: each is a new cache line, and a
+    // load of the step before was the longest wait of the loop.
+    float* const ring = reinterpret_cast<float*>(raw + (smem - smem_u32(raw)) + C::kStages * C::kStageBytes) +
+                        warp * kAhead * (32 + C::kHalf);
+    const unsigned ring_at = smem_u32(ring);
+    long long f_pos = pos;
+    Unit f;
+    int f_kb = 0;
+    const float *f_sa = nullptr, *f_sb = nullptr;
+    bool f_go = true;
+    f.kb1 = 0;
+    unsigned f_it = 0;
+    auto fetch = [&] {
+      if (f_go && f_kb == f.kb1) {
+        f_go = next_unit(p, &f_pos, end, &f);
+        f_kb = f.kb0;
+        if (f_go) {
+          f_sa = p.sa + f_kb * p.sa_row + (min(f.tm * kBM + quarter * 32 + lane, p.m - 1) >> p.a_shift);
+          f_sb = p.sb + f_kb * p.sb_row;
+        }
+      }
+      if (f_go) {
+        const unsigned at = ring_at + (f_it % kAhead) * (32 + C::kHalf) * 4 + lane * 4;
+        const int c0 = f.tn * BN + half * C::kHalf;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(f_sa) : "memory");
+#pragma unroll
+        for (int i = 0; i < (BCOL ? C::kHalf / 32 : 1); ++i)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + 128 + i * 128),
+                       "l"(f_sb + (min(c0 + (BCOL ? i * 32 + lane : 0), p.n - 1) >> p.b_shift))
+                       : "memory");
+        ++f_kb;
+        ++f_it;
+        f_sa += p.sa_row;
+        f_sb += p.sb_row;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) fetch();
     unsigned it = 0;
     bool go = true;
     while (go && next_unit(p, &pos, end, &u)) {
       const int row = u.tm * kBM + quarter * 32 + lane;
       const int col0 = u.tn * BN + half * C::kHalf;
-      const float* sa = p.sa + (min(row, p.m - 1) >> p.a_shift);
       f32x2 acc2[C::kHalf / 2];
 #pragma unroll
       for (int c = 0; c < C::kHalf / 2; ++c) acc2[c] = 0;
-      constexpr int kPer = (C::kHalf + 31) / 32;  // b's scales a lane fetches
-      float sa_next = sa[u.kb0 * p.sa_row], sb_next[BCOL ? kPer : 1];
-      auto fetch_b = [&](int kb) {
-        if constexpr (BCOL) {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int c = min(col0 + i * 32 + lane, p.n - 1);
-            sb_next[i] = __ldg(p.sb + kb * p.sb_row + (c >> p.b_shift));
-          }
-        } else {
-          sb_next[0] = __ldg(p.sb + kb * p.sb_row + (min(col0, p.n - 1) >> p.b_shift));
-        }
-      };
-      fetch_b(u.kb0);
       for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
         const unsigned t = it & 1, tph = (it >> 1) & 1;
-        float s = sa_next;
-        float* sb = sbuf + t * C::kHalf;
-        if constexpr (BCOL) {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) sb[i * 32 + lane] = sb_next[i];
-          __syncwarp();
-        } else {
-          s *= sb_next[0];
-        }
-        if (kb + 1 < u.kb1) {
-          sa_next = __ldg(sa + (kb + 1) * p.sa_row);
-          fetch_b(kb + 1);
-        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+        __syncwarp();  // every lane's copies of this step are there, and all lanes are done with the slot that is filled next
+        const float* sl = ring + (it % kAhead) * (32 + C::kHalf);
+        const float* sb = sl + 32;
+        const float s = BCOL ? sl[lane] : sl[lane] * sb[lane];
+        fetch();
         go = mbar_wait(tfull0 + 8 * t, tph, stop);
         go = __all_sync(0xffffffffu, go);
         if (!go) break;
         tc_fence_after();
-        const f32x2 s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+        [[maybe_unused]] const f32x2 s2 = pack2(__float_as_uint(s), __float_as_uint(s));
         const unsigned taddr = tmem + ((unsigned)(quarter * 32) << 16) + t * BN + half * C::kHalf;
         constexpr int kChunks = C::kHalf / 32;
         unsigned v[2][32];
@@ -402,8 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
               a2[0] = fma2(pack2(w[j], w[j + 1]), mul2(s2, b.x), a2[0]);
               a2[1] = fma2(pack2(w[j + 2], w[j + 3]), mul2(s2, b.y), a2[1]);
             } else {
-              a2[0] = fma2(pack2(w[j], w[j + 1]), s2, a2[0]);
-              a2[1] = fma2(pack2(w[j + 2], w[j + 3]), s2, a2[1]);
+              float* a1 = reinterpret_cast<float*>(a2);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) a1[q] = fmaf(__uint_as_float(w[j + q]), s, a1[q]);
             }
           }
         }
@@ -442,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         for (int c = 0; c < C::kHalf; c += 8) store32<float>(dst + c, acc + c);
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
