@@ -35,13 +35,17 @@ __device__ unsigned g_op_flags;  // EMB_FLAG_OP_* bits since the last emb_check_
 
 constexpr int kBM = 128;             // rows of a tile
 constexpr int kBK = EMB_FP8_BLOCK;   // k's of a step: one scale block, 128 bytes of a row
-constexpr int kScaleWarps = 8;
-constexpr int kThreads = 384;        // 8 scaling warps; then 1 TMA warp, 1 MMA warp, 2 idle
-// Registers: 384 x 168 at launch; the scaling warps' accumulators need more and
-// the other four warps little: 256 x 224 + 128 x 56 = 384 x 168.
-constexpr int kScaleRegs = 224, kOtherRegs = 56;
-static_assert(256 * kScaleRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
-constexpr int kAhead = 4;            // steps whose scales are held or on their way
+#ifndef SW
+#define SW 8
+#endif
+constexpr int kScaleWarps = SW;
+constexpr int kThreads = (kScaleWarps + 4) * 32;  // then a TMA warp, an MMA warp, a warp for the scales, an idle one
+// Registers: the scaling warps' accumulators need more than an even share, the other four warps little.
+constexpr int kLaunchRegs = SW == 8 ? 168 : 96;
+constexpr int kScaleRegs = SW == 8 ? 224 : 112, kOtherRegs = SW == 8 ? 56 : 32;
+static_assert(kScaleWarps * 32 * kScaleRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kTmaWarp = kScaleWarps, kMmaWarp = kScaleWarps + 1, kFetchWarp = kScaleWarps + 2;
+constexpr int kAhead = 8;            // steps whose scales are held or on their way
 constexpr unsigned kWaitLimit = 1u << 21;  // polls of one wait before the kernel gives up
 
 struct MatmulArgs {
@@ -170,8 +174,9 @@ template <int BN>
 struct TileCfg {
   static constexpr int kStageBytes = (kBM + BN) * kBK;
   static constexpr int kStages = (196 * 1024) / kStageBytes;  // 4, 6 or 8
-  static constexpr int kHalf = BN / 2;                        // columns of a scaling warp
-  static constexpr int kScaleBytes = kScaleWarps * kAhead * (32 + kHalf) * 4;
+  static constexpr int kHalf = BN * 4 / kScaleWarps;          // columns of a scaling warp
+  static constexpr int kSlot = kBM + BN;                      // scales of a step: rows, columns
+  static constexpr int kScaleBytes = kAhead * kSlot * 4;
   static constexpr int kBytes = kStages * kStageBytes + kScaleBytes + 1024;  // + room to align
 };
 
@@ -248,13 +253,15 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                                                            const __grid_constant__ MatmulArgs p) {
   using C = TileCfg<BN>;
   extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) unsigned long long bars[2 * C::kStages + 4];
+  __shared__ __align__(8) unsigned long long bars[2 * C::kStages + 4 + 2 * kAhead];
   __shared__ unsigned tmem_slot;
   __shared__ int stop_flag;
   volatile int* stop = &stop_flag;
   const unsigned smem = (smem_u32(raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned full0 = smem_u32(bars), empty0 = full0 + 8 * C::kStages, tfull0 = empty0 + 8 * C::kStages, tempty0 = tfull0 + 16;
+  const unsigned sfull0 = tempty0 + 16, sempty0 = sfull0 + 8 * kAhead;
+  float* const ring = reinterpret_cast<float*>(raw + (smem - smem_u32(raw)) + C::kStages * C::kStageBytes);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -265,10 +272,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       mbar_init(tfull0 + 8 * t, 1);
       mbar_init(tempty0 + 8 * t, kScaleWarps);
     }
+    for (int s = 0; s < kAhead; ++s) {
+      mbar_init(sfull0 + 8 * s, 32);
+      mbar_init(sempty0 + 8 * s, kScaleWarps);
+    }
     stop_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(2 * BN) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -283,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 
   if (warp >= kScaleWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8 && lane == 0) {  // TMA: both slabs of each step
+    if (warp == kTmaWarp && lane == 0) {  // TMA: both slabs of each step
       unsigned it = 0;
       bool go = true;
       while (go && next_unit(p, &pos, end, &u)) {
@@ -305,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           for (unsigned i = 0; i < kWaitLimit && !mbar_try(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1); ++i) {}
       }
     }
-    if (warp == 9 && lane == 0) {  // MMA
+    if (warp == kMmaWarp && lane == 0) {  // MMA
       // f32 accumulator, e4m3 x e4m3, both K-major, N = BN, M = 128
       constexpr unsigned idesc = (1u << 4) | ((BN >> 3) << 17) | ((kBM >> 4) << 24);
       unsigned it = 0;
@@ -332,51 +343,41 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         for (unsigned i = 0; i < kWaitLimit && !mbar_try(tfull0 + 8 * (j & 1), (j >> 1) & 1); ++i) {}
       }
     }
-    __syncwarp();
-  } else {  // scaling warps: TMEM lanes 32 (warp % 4).., columns half (warp / 4)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kScaleRegs));
-    const int half = warp >> 2, quarter = warp & 3;
-    // The scales of this warp's rows and columns come by 4-byte asynchronous
-    // copies (their rows have no alignment) into a ring of its own, kAhead - 1
-    // steps ahead and on into its next tiles: each is a new cache line, and a
-    // load of the step before was the longest wait of the loop.
-    float* const ring = reinterpret_cast<float*>(raw + (smem - smem_u32(raw)) + C::kStages * C::kStageBytes) +
-                        warp * kAhead * (32 + C::kHalf);
-    const unsigned ring_at = smem_u32(ring);
-    long long f_pos = pos;
-    Unit f;
-    int f_kb = 0;
-    const float *f_sa = nullptr, *f_sb = nullptr;
-    bool f_go = true;
-    f.kb1 = 0;
-    unsigned f_it = 0;
-    auto fetch = [&] {
-      if (f_go && f_kb == f.kb1) {
-        f_go = next_unit(p, &f_pos, end, &f);
-        f_kb = f.kb0;
-        if (f_go) {
-          f_sa = p.sa + f_kb * p.sa_row + (min(f.tm * kBM + quarter * 32 + lane, p.m - 1) >> p.a_shift);
-          f_sb = p.sb + f_kb * p.sb_row;
+    if (warp == kFetchWarp) {
+      // The steps' scales, by 4-byte asynchronous copies (rows of scales have no
+      // alignment), up to kAhead steps early: each is a new cache line.
+      unsigned it = 0;
+      bool go = true;
+      while (go && next_unit(p, &pos, end, &u)) {
+        const float *sa[kBM / 32], *sb[BCOL ? BN / 32 : 1];
+#pragma unroll
+        for (int i = 0; i < kBM / 32; ++i)
+          sa[i] = p.sa + u.kb0 * p.sa_row + (min(u.tm * kBM + i * 32 + lane, p.m - 1) >> p.a_shift);
+#pragma unroll
+        for (int i = 0; i < (BCOL ? BN / 32 : 1); ++i)
+          sb[i] = p.sb + u.kb0 * p.sb_row + (min(u.tn * BN + (BCOL ? i * 32 + lane : lane * kBK), p.n - 1) >> p.b_shift);
+        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+          const unsigned slot = it % kAhead;
+          go = __all_sync(0xffffffffu, mbar_wait(sempty0 + 8 * slot, ((it / kAhead) & 1) ^ 1, stop));
+          if (!go) break;
+          const unsigned at = smem_u32(ring + slot * C::kSlot + lane);
+#pragma unroll
+          for (int i = 0; i < kBM / 32; ++i, sa[i - 1] += p.sa_row)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + 128 * i), "l"(sa[i]) : "memory");
+          if (BCOL || lane < (BN + kBK - 1) / kBK) {
+#pragma unroll
+            for (int i = 0; i < (BCOL ? BN / 32 : 1); ++i, sb[i - 1] += p.sb_row)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + 4 * kBM + 128 * i), "l"(sb[i]) : "memory");
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sfull0 + 8 * slot) : "memory");
         }
       }
-      if (f_go) {
-        const unsigned at = ring_at + (f_it % kAhead) * (32 + C::kHalf) * 4 + lane * 4;
-        const int c0 = f.tn * BN + half * C::kHalf;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at), "l"(f_sa) : "memory");
-#pragma unroll
-        for (int i = 0; i < (BCOL ? C::kHalf / 32 : 1); ++i)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(at + 128 + i * 128),
-                       "l"(f_sb + (min(c0 + (BCOL ? i * 32 + lane : 0), p.n - 1) >> p.b_shift))
-                       : "memory");
-        ++f_kb;
-        ++f_it;
-        f_sa += p.sa_row;
-        f_sb += p.sb_row;
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll
-    for (int i = 0; i < kAhead - 1; ++i) fetch();
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    __syncwarp();
+  } else {  // scaling warps: TMEM lanes 32 (warp % 4).., columns group (warp / 4)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kScaleRegs));
+    const int half = warp >> 2, quarter = warp & 3;
     unsigned it = 0;
     bool go = true;
     while (go && next_unit(p, &pos, end, &u)) {
@@ -386,18 +387,19 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 #pragma unroll
       for (int c = 0; c < C::kHalf / 2; ++c) acc2[c] = 0;
       for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
-        const unsigned t = it & 1, tph = (it >> 1) & 1;
-        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
-        __syncwarp();  // every lane's copies of this step are there, and all lanes are done with the slot that is filled next
-        const float* sl = ring + (it % kAhead) * (32 + C::kHalf);
-        const float* sb = sl + 32;
-        const float s = BCOL ? sl[lane] : sl[lane] * sb[lane];
-        fetch();
-        go = mbar_wait(tfull0 + 8 * t, tph, stop);
+        const unsigned t = it & 1, tph = (it >> 1) & 1, slot = it % kAhead;
+        const float* sl = ring + slot * C::kSlot + quarter * 32 + lane;
+        const float* sb = ring + slot * C::kSlot + kBM + (BCOL ? half * C::kHalf : half * C::kHalf / kBK);
+        go = mbar_wait(sfull0 + 8 * slot, (it / kAhead) & 1, stop);
+        float s = 0.0f;
+        if (go) s = BCOL ? *sl : *sl * *sb;
+        go = go && mbar_wait(tfull0 + 8 * t, tph, stop);
         go = __all_sync(0xffffffffu, go);
         if (!go) break;
+        if (!BCOL && lane == 0) mbar_arrive(sempty0 + 8 * slot);
         tc_fence_after();
         [[maybe_unused]] const f32x2 s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+        constexpr int kChunk = C::kHalf < 32 ? C::kHalf : 32;
         const unsigned taddr = tmem + ((unsigned)(quarter * 32) << 16) + t * BN + half * C::kHalf;
         constexpr int kChunks = C::kHalf / 32;
         unsigned v[2][32];
@@ -426,6 +428,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
               for (int q = 0; q < 4; ++q) a1[q] = fmaf(__uint_as_float(w[j + q]), s, a1[q]);
             }
           }
+        }
+        if constexpr (BCOL) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sempty0 + 8 * slot);
         }
       }
       if (!go) break;
@@ -462,11 +468,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         for (int c = 0; c < C::kHalf; c += 8) store32<float>(dst + c, acc + c);
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN));
   }
