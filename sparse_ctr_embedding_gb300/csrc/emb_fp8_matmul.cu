@@ -35,14 +35,10 @@ __device__ unsigned g_op_flags;  // EMB_FLAG_OP_* bits since the last emb_check_
 
 constexpr int kBM = 128;             // rows of a tile
 constexpr int kBK = EMB_FP8_BLOCK;   // k's of a step: one scale block, 128 bytes of a row
-#ifndef SW
-#define SW 8
-#endif
-constexpr int kScaleWarps = SW;
+constexpr int kScaleWarps = 8;
 constexpr int kThreads = (kScaleWarps + 4) * 32;  // then a TMA warp, an MMA warp, a warp for the scales, an idle one
 // Registers: the scaling warps' accumulators need more than an even share, the other four warps little.
-constexpr int kLaunchRegs = SW == 8 ? 168 : 96;
-constexpr int kScaleRegs = SW == 8 ? 224 : 112, kOtherRegs = SW == 8 ? 56 : 32;
+constexpr int kLaunchRegs = 168, kScaleRegs = 224, kOtherRegs = 56;
 static_assert(kScaleWarps * 32 * kScaleRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kTmaWarp = kScaleWarps, kMmaWarp = kScaleWarps + 1, kFetchWarp = kScaleWarps + 2;
 constexpr int kAhead = 8;            // steps whose scales are held or on their way
@@ -98,6 +94,18 @@ __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity, volatil
   atomicOr(&g_op_flags, EMB_FLAG_OP_TIMEOUT);
   return false;
 }
+// One lane of a converged warp.  A branch on it (and not on a lane number) lets
+// the compiler keep what the lane issues in uniform registers: with the latter
+// each tcgen05.mma took about 100 cycles to issue.
+__device__ __forceinline__ bool elect_one() {
+  unsigned one;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(one));
+  return one != 0;
+}
 __device__ __forceinline__ void tma_load(unsigned dst, const CUtensorMap* map, int x, int y, unsigned bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
@@ -139,29 +147,6 @@ __device__ __forceinline__ void tc_wait32(unsigned* v) {
                  "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
                  "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
 }
-// Two floats in a 64-bit register, and their multiply-add (one issue slot for two).
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack2(unsigned lo, unsigned hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(f32x2 v) {
-  unsigned lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
-}
-
 // Shared memory descriptor of a K-major operand: rows of 128 bytes, 128-byte
 // swizzle (layout 2), eight-row groups 1024 bytes apart, descriptor version 1.
 __device__ __forceinline__ unsigned long long smem_desc(unsigned addr) {
@@ -253,25 +238,25 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
                                                            const __grid_constant__ MatmulArgs p) {
   using C = TileCfg<BN>;
   extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) unsigned long long bars[2 * C::kStages + 4 + 2 * kAhead];
+  __shared__ __align__(8) unsigned long long bars[2 * C::kStages + 2 + 2 * kAhead];
   __shared__ unsigned tmem_slot;
   __shared__ int stop_flag;
   volatile int* stop = &stop_flag;
   const unsigned smem = (smem_u32(raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned full0 = smem_u32(bars), empty0 = full0 + 8 * C::kStages, tfull0 = empty0 + 8 * C::kStages, tempty0 = tfull0 + 16;
+  // full: a stage's slabs are there.  done: its products are, so the stage may be
+  // filled again and its sums be read.  tempty: a TMEM accumulator has been read.
+  // sfull, sempty: the scales of a step.
+  const unsigned full0 = smem_u32(bars), done0 = full0 + 8 * C::kStages, tempty0 = done0 + 8 * C::kStages;
   const unsigned sfull0 = tempty0 + 16, sempty0 = sfull0 + 8 * kAhead;
   float* const ring = reinterpret_cast<float*>(raw + (smem - smem_u32(raw)) + C::kStages * C::kStageBytes);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, 1);
+      mbar_init(done0 + 8 * s, 1);
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(tfull0 + 8 * t, 1);
-      mbar_init(tempty0 + 8 * t, kScaleWarps);
-    }
+    for (int t = 0; t < 2; ++t) mbar_init(tempty0 + 8 * t, kScaleWarps);
     for (int s = 0; s < kAhead; ++s) {
       mbar_init(sfull0 + 8 * s, 32);
       mbar_init(sempty0 + 8 * s, kScaleWarps);
@@ -294,20 +279,21 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 
   if (warp >= kScaleWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kTmaWarp && lane == 0) {  // TMA: both slabs of each step
+    if (warp == kTmaWarp) {  // TMA: both slabs of each step
       unsigned it = 0;
       bool go = true;
       while (go && next_unit(p, &pos, end, &u)) {
         for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
           const unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
-          if (!mbar_wait(empty0 + 8 * s, ph ^ 1, stop)) {
-            go = false;
-            break;
+          go = __all_sync(0xffffffffu, mbar_wait(done0 + 8 * s, ph ^ 1, stop));
+          if (!go) break;
+          if (elect_one()) {
+            const unsigned dst = smem + s * C::kStageBytes, bar = full0 + 8 * s;
+            mbar_expect_tx(bar, C::kStageBytes);
+            tma_load(dst, &map_a, kb * kBK, u.tm * kBM, bar);
+            tma_load(dst + kBM * kBK, &map_b, kb * kBK, u.tn * BN, bar);
           }
-          const unsigned dst = smem + s * C::kStageBytes, bar = full0 + 8 * s;
-          mbar_expect_tx(bar, C::kStageBytes);
-          tma_load(dst, &map_a, kb * kBK, u.tm * kBM, bar);
-          tma_load(dst + kBM * kBK, &map_b, kb * kBK, u.tn * BN, bar);
+          __syncwarp();
         }
       }
       if (!go) {  // gave up: the loads in flight must land before the block ends
@@ -316,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           for (unsigned i = 0; i < kWaitLimit && !mbar_try(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1); ++i) {}
       }
     }
-    if (warp == kMmaWarp && lane == 0) {  // MMA
+    if (warp == kMmaWarp) {
       // f32 accumulator, e4m3 x e4m3, both K-major, N = BN, M = 128
       constexpr unsigned idesc = (1u << 4) | ((BN >> 3) << 17) | ((kBM >> 4) << 24);
       unsigned it = 0;
@@ -325,22 +311,24 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
           const unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
           const unsigned t = it & 1, tph = (it >> 1) & 1;
-          if (!mbar_wait(tempty0 + 8 * t, tph ^ 1, stop) || !mbar_wait(full0 + 8 * s, ph, stop)) {
-            go = false;
-            break;
-          }
+          const bool ready_t = mbar_try(tempty0 + 8 * t, tph ^ 1), ready_f = mbar_try(full0 + 8 * s, ph);
+          go = (ready_t || mbar_wait(tempty0 + 8 * t, tph ^ 1, stop)) && (ready_f || mbar_wait(full0 + 8 * s, ph, stop));
+          go = __all_sync(0xffffffffu, go);
+          if (!go) break;
           tc_fence_after();
           const unsigned at = smem + s * C::kStageBytes;
           const unsigned long long da = smem_desc(at), db = smem_desc(at + kBM * kBK);
+          if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < kBK / 32; ++j) tc_mma(tmem + t * BN, da + 2 * j, db + 2 * j, idesc, j > 0);
-          tc_commit(empty0 + 8 * s);
-          tc_commit(tfull0 + 8 * t);
+            for (int j = 0; j < kBK / 32; ++j) tc_mma(tmem + t * BN, da + 2 * j, db + 2 * j, idesc, j > 0);
+            tc_commit(done0 + 8 * s);
+          }
+          __syncwarp();
         }
       }
       if (!go && it > 0) {  // gave up: wait for the products in flight before TMEM is freed
         const unsigned j = it - 1;
-        for (unsigned i = 0; i < kWaitLimit && !mbar_try(tfull0 + 8 * (j & 1), (j >> 1) & 1); ++i) {}
+        for (unsigned i = 0; i < kWaitLimit && !mbar_try(done0 + 8 * (j % C::kStages), (j / C::kStages) & 1); ++i) {}
       }
     }
     if (warp == kFetchWarp) {
@@ -383,23 +371,21 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     while (go && next_unit(p, &pos, end, &u)) {
       const int row = u.tm * kBM + quarter * 32 + lane;
       const int col0 = u.tn * BN + half * C::kHalf;
-      f32x2 acc2[C::kHalf / 2];
+      float acc[C::kHalf];
 #pragma unroll
-      for (int c = 0; c < C::kHalf / 2; ++c) acc2[c] = 0;
+      for (int c = 0; c < C::kHalf; ++c) acc[c] = 0.0f;
       for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
-        const unsigned t = it & 1, tph = (it >> 1) & 1, slot = it % kAhead;
+        const unsigned t = it & 1, slot = it % kAhead, stage = it % C::kStages, ph = (it / C::kStages) & 1;
         const float* sl = ring + slot * C::kSlot + quarter * 32 + lane;
         const float* sb = ring + slot * C::kSlot + kBM + (BCOL ? half * C::kHalf : half * C::kHalf / kBK);
         go = mbar_wait(sfull0 + 8 * slot, (it / kAhead) & 1, stop);
         float s = 0.0f;
         if (go) s = BCOL ? *sl : *sl * *sb;
-        go = go && mbar_wait(tfull0 + 8 * t, tph, stop);
+        go = go && mbar_wait(done0 + 8 * stage, ph, stop);
         go = __all_sync(0xffffffffu, go);
         if (!go) break;
         if (!BCOL && lane == 0) mbar_arrive(sempty0 + 8 * slot);
         tc_fence_after();
-        [[maybe_unused]] const f32x2 s2 = pack2(__float_as_uint(s), __float_as_uint(s));
-        constexpr int kChunk = C::kHalf < 32 ? C::kHalf : 32;
         const unsigned taddr = tmem + ((unsigned)(quarter * 32) << 16) + t * BN + half * C::kHalf;
         constexpr int kChunks = C::kHalf / 32;
         unsigned v[2][32];
@@ -417,15 +403,16 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           const unsigned* w = v[c & 1];
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            f32x2* a2 = acc2 + (c * 32 + j) / 2;
             if constexpr (BCOL) {
-              const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(sb + c * 32 + j);
-              a2[0] = fma2(pack2(w[j], w[j + 1]), mul2(s2, b.x), a2[0]);
-              a2[1] = fma2(pack2(w[j + 2], w[j + 3]), mul2(s2, b.y), a2[1]);
+              float* a1 = acc + c * 32 + j;
+              const float4 b = *reinterpret_cast<const float4*>(sb + c * 32 + j);
+              a1[0] = fmaf(__uint_as_float(w[j]), s * b.x, a1[0]);
+              a1[1] = fmaf(__uint_as_float(w[j + 1]), s * b.y, a1[1]);
+              a1[2] = fmaf(__uint_as_float(w[j + 2]), s * b.z, a1[2]);
+              a1[3] = fmaf(__uint_as_float(w[j + 3]), s * b.w, a1[3]);
             } else {
-              float* a1 = reinterpret_cast<float*>(a2);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) a1[q] = fmaf(__uint_as_float(w[j + q]), s, a1[q]);
+              for (int q = 0; q < 4; ++q) acc[c * 32 + j + q] = fmaf(__uint_as_float(w[j + q]), s, acc[c * 32 + j + q]);
             }
           }
         }
@@ -435,13 +422,6 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
       }
       if (!go) break;
-      float acc[C::kHalf];
-#pragma unroll
-      for (int c = 0; c < C::kHalf / 2; ++c) {
-        const float2 x = unpack2(acc2[c]);
-        acc[2 * c] = x.x;
-        acc[2 * c + 1] = x.y;
-      }
       if (u.kb0 == 0 && u.kb1 == p.k_blocks) {
         if (row < p.m) {
           OT* dst = (OT*)p.out + row * p.ldo + col0;
