@@ -139,6 +139,14 @@ __device__ __forceinline__ void tc_load32(unsigned addr, unsigned* v) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tc_load16(unsigned addr, unsigned* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(addr)
+      : "memory");
+}
 // Waits for the loads above; the registers pass through so that no use of them moves before it.
 __device__ __forceinline__ void tc_wait32(unsigned* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -147,6 +155,22 @@ __device__ __forceinline__ void tc_wait32(unsigned* v) {
                  "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
                  "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
 }
+__device__ __forceinline__ void tc_wait16(unsigned* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
+}
+template <int N>
+__device__ __forceinline__ void tc_load(unsigned addr, unsigned* v) {
+  if constexpr (N == 16) tc_load16(addr, v);
+  else tc_load32(addr, v);
+}
+template <int N>
+__device__ __forceinline__ void tc_wait(unsigned* v) {
+  if constexpr (N == 16) tc_wait16(v);
+  else tc_wait32(v);
+}
+
 // Shared memory descriptor of a K-major operand: rows of 128 bytes, 128-byte
 // swizzle (layout 2), eight-row groups 1024 bytes apart, descriptor version 1.
 __device__ __forceinline__ unsigned long long smem_desc(unsigned addr) {
@@ -387,32 +411,37 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         if (!BCOL && lane == 0) mbar_arrive(sempty0 + 8 * slot);
         tc_fence_after();
         const unsigned taddr = tmem + ((unsigned)(quarter * 32) << 16) + t * BN + half * C::kHalf;
-        constexpr int kChunks = C::kHalf / 32;
-        unsigned v[2][32];
-        tc_load32(taddr, v[0]);
+        // Columns in chunks: the next one, and its scales, are on their way while one is added.
+        constexpr int kChunk = BCOL ? 16 : 32, kChunks = C::kHalf / kChunk;
+        unsigned v[2][kChunk];
+        float4 b[2][BCOL ? kChunk / 4 : 1];
+        auto start = [&](int c) {
+          if constexpr (BCOL) {
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {  // the next 32 columns are on their way while these are added
-          tc_wait32(v[c & 1]);
+            for (int j = 0; j < kChunk / 4; ++j) b[c & 1][j] = *reinterpret_cast<const float4*>(sb + c * kChunk + 4 * j);
+          }
+          tc_load<kChunk>(taddr + c * kChunk, v[c & 1]);
+        };
+        start(0);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          tc_wait<kChunk>(v[c & 1]);
           if (c + 1 < kChunks) {
-            tc_load32(taddr + (c + 1) * 32, v[(c + 1) & 1]);
+            start(c + 1);
           } else {  // all of this accumulator is in registers: the MMA may write it again
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty0 + 8 * t);
           }
           const unsigned* w = v[c & 1];
+          float* o = acc + c * kChunk;
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
+          for (int j = 0; j < kChunk; ++j) {
             if constexpr (BCOL) {
-              float* a1 = acc + c * 32 + j;
-              const float4 b = *reinterpret_cast<const float4*>(sb + c * 32 + j);
-              a1[0] = fmaf(__uint_as_float(w[j]), s * b.x, a1[0]);
-              a1[1] = fmaf(__uint_as_float(w[j + 1]), s * b.y, a1[1]);
-              a1[2] = fmaf(__uint_as_float(w[j + 2]), s * b.z, a1[2]);
-              a1[3] = fmaf(__uint_as_float(w[j + 3]), s * b.w, a1[3]);
+              const float4& q = b[c & 1][j / 4];
+              o[j] = fmaf(__uint_as_float(w[j]), s * (j % 4 == 0 ? q.x : j % 4 == 1 ? q.y : j % 4 == 2 ? q.z : q.w), o[j]);
             } else {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) acc[c * 32 + j + q] = fmaf(__uint_as_float(w[j + q]), s, acc[c * 32 + j + q]);
+              o[j] = fmaf(__uint_as_float(w[j]), s, o[j]);
             }
           }
         }
@@ -601,9 +630,9 @@ Plan make_plan(long long m, long long n, long long k) {
   pl.m_tiles = (int)mt;
   pl.n_tiles = (int)((n + pl.bn - 1) / pl.bn);
   const long long tiles = mt * pl.n_tiles, steps = tiles * pl.k_blocks;
-  // Whole tiles when the last round of them leaves less than a tenth of the time idle, or a tile is one block long.
+  // Whole tiles when the last round of them leaves at most a fifth of the SMs idle, or a tile is one block long.
   const long long rounds = (tiles + sms - 1) / sms;
-  if (pl.k_blocks == 1 || tiles * 10 >= rounds * sms * 9) {
+  if (pl.k_blocks == 1 || tiles * 5 >= rounds * sms * 4) {
     pl.grid = (int)std::min<long long>(tiles, sms);
   } else {
     pl.per_cta = std::max<long long>((steps + sms - 1) / sms, std::min(2, pl.k_blocks));
