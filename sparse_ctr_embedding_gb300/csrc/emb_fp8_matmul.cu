@@ -171,6 +171,24 @@ __device__ __forceinline__ void tc_wait(unsigned* v) {
   else tc_wait32(v);
 }
 
+// Two floats side by side, and their products and multiply-adds (one issue slot for two).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void fma2(f32x2 a, f32x2 b, float* c) {
+  f32x2 r = pack2(c[0], c[1]);
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(r) : "l"(a), "l"(b));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(c[0]), "=f"(c[1]) : "l"(r));
+}
+
 // Shared memory descriptor of a K-major operand: rows of 128 bytes, 128-byte
 // swizzle (layout 2), eight-row groups 1024 bytes apart, descriptor version 1.
 __device__ __forceinline__ unsigned long long smem_desc(unsigned addr) {
@@ -413,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         const unsigned taddr = tmem + ((unsigned)(quarter * 32) << 16) + t * BN + half * C::kHalf;
         // Columns in chunks: the next one, and its scales, are on their way while one is added.
         constexpr int kChunk = BCOL ? 16 : 32, kChunks = C::kHalf / kChunk;
+        const f32x2 s2 = pack2(s, s);
         unsigned v[2][kChunk];
         float4 b[2][BCOL ? kChunk / 4 : 1];
         auto start = [&](int c) {
@@ -436,12 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           const unsigned* w = v[c & 1];
           float* o = acc + c * kChunk;
 #pragma unroll
-          for (int j = 0; j < kChunk; ++j) {
+          for (int j = 0; j < kChunk; j += 2) {
+            const f32x2 x = pack2(__uint_as_float(w[j]), __uint_as_float(w[j + 1]));
             if constexpr (BCOL) {
               const float4& q = b[c & 1][j / 4];
-              o[j] = fmaf(__uint_as_float(w[j]), s * (j % 4 == 0 ? q.x : j % 4 == 1 ? q.y : j % 4 == 2 ? q.z : q.w), o[j]);
+              fma2(x, mul2(s2, j % 4 == 0 ? pack2(q.x, q.y) : pack2(q.z, q.w)), o + j);
             } else {
-              o[j] = fmaf(__uint_as_float(w[j]), s, o[j]);
+              fma2(x, s2, o + j);
             }
           }
         }
