@@ -8,7 +8,9 @@ built, importing succeeds but the first call raises ``LibraryNotBuilt``.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 import re
 from typing import Optional, Sequence, Tuple
@@ -575,41 +577,61 @@ class Pipeline:
 
 
 # ------------------------------------------------------------------ the dense tower's operators
+#
+# These run as often as a layer does, some for microseconds: the checks here
+# are few and flat, and the current stream is read as its raw handle.
 
 
-def _alloc(stream, shape, dtype, device) -> torch.Tensor:
+def _raw_stream(stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _empty(stream, like: torch.Tensor, shape, dtype) -> torch.Tensor:
     """A tensor for use on `stream`: torch's allocator then reuses its memory in that stream's order."""
-    if not isinstance(stream, torch.cuda.Stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _ftype(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _FTYPE:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    return _FTYPE[t.dtype]
+def _dense(t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
+    """The address of a contiguous CUDA tensor of this type."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
 
 
-def _matrix(t: torch.Tensor, dtype, name: str) -> int:
-    """Checks a CUDA matrix with neighbouring columns; returns its row stride."""
+def _ftype(dtype, name: str) -> int:
+    code = _FTYPE.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Checks a CUDA matrix with neighbouring columns; returns the distance of its rows."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a matrix with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return ld if rows > 1 else max(ld, cols)
 
 
-def _codes(rows: int, cols: int, device, stream) -> torch.Tensor:
-    """An empty code matrix whose rows lie a multiple of 16 bytes apart."""
-    return _alloc(stream, (rows, -(-cols // 16) * 16), torch.float8_e4m3fn, device)[:, :cols]
-
-
-def _code_ld(t: torch.Tensor, name: str) -> int:
-    ld = _matrix(t, torch.float8_e4m3fn, name)
-    return -(-max(ld, t.shape[1]) // 16) * 16 if t.shape[0] <= 1 or t.shape[1] == 0 else ld
+def _code_stride(t: torch.Tensor, name: str) -> int:
+    if t.dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"{name} must be {torch.float8_e4m3fn}, got {t.dtype}")
+    ld = _row_stride(t, name)
+    return -(-ld // 16) * 16 if ld % 16 and (t.shape[0] <= 1 or t.shape[1] == 0) else ld
 
 
 def emb_fp8_quantize(x: torch.Tensor, block_rows: int = 1, transpose: bool = False, stream=None):
@@ -617,19 +639,23 @@ def emb_fp8_quantize(x: torch.Tensor, block_rows: int = 1, transpose: bool = Fal
     may be strided): (q, s), with q[rows, cols] and s[ceil(cols/128),
     ceil(rows/block_rows)]; with transpose=True (q, s, qt, st), the codes of
     x.T in blocks along x's rows as well, from the same pass."""
-    ldx = _matrix(x, None, "x")
+    ldx = _row_stride(x, "x")
+    if block_rows not in (1, EMB_FP8_BLOCK):
+        raise ValueError("block_rows must be 1 or 128")
     r, c = x.shape
-    q = _codes(r, c, x.device, stream)
-    s = _alloc(stream, (-(-c // EMB_FP8_BLOCK), -(-r // block_rows) if block_rows > 0 else 0), torch.float32, x.device)
+    f8 = torch.float8_e4m3fn
+    ldq, ldqt = (c + 15) & ~15, (r + 15) & ~15
+    q = _empty(stream, x, (r, ldq), f8)
+    s = _empty(stream, x, ((c + 127) >> 7, r if block_rows == 1 else (r + 127) >> 7), torch.float32)
     qt = st = None
     if transpose:
-        qt = _codes(c, r, x.device, stream)
-        st = _alloc(stream, (-(-r // EMB_FP8_BLOCK), -(-c // block_rows) if block_rows > 0 else 0), torch.float32, x.device)
-    _check(lib().emb_fp8_quantize(x.data_ptr(), _ftype(x, "x"), r, c, ldx, block_rows, q.data_ptr(), _code_ld(q, "q"),
-                                  s.data_ptr(), None if qt is None else qt.data_ptr(),
-                                  0 if qt is None else _code_ld(qt, "qt"), None if st is None else st.data_ptr(),
-                                  _stream(stream)))
-    return (q, s, qt, st) if transpose else (q, s)
+        qt = _empty(stream, x, (c, ldqt), f8)
+        st = _empty(stream, x, ((r + 127) >> 7, c if block_rows == 1 else (c + 127) >> 7), torch.float32)
+    _check(lib().emb_fp8_quantize(x.data_ptr(), _ftype(x.dtype, "x"), r, c, ldx, block_rows, q.data_ptr(), ldq, s.data_ptr(),
+                                  qt.data_ptr() if transpose else None, ldqt, st.data_ptr() if transpose else None,
+                                  _raw_stream(stream)))
+    q = q if ldq == c else q[:, :c]
+    return (q, s, qt if ldqt == r else qt[:, :r], st) if transpose else (q, s)
 
 
 def emb_fp8_matmul_workspace_size(m: int, n: int, k: int) -> int:
@@ -638,10 +664,14 @@ def emb_fp8_matmul_workspace_size(m: int, n: int, k: int) -> int:
     return b.value
 
 
-def _block_rows(s: torch.Tensor, rows: int, k: int, name: str) -> int:
-    if s.dim() != 2 or s.shape[0] != -(-k // EMB_FP8_BLOCK) or s.shape[1] not in (rows, -(-rows // EMB_FP8_BLOCK)):
-        raise ValueError(f"{name} must be [ceil(k/128), rows] or [ceil(k/128), ceil(rows/128)], got {tuple(s.shape)}")
-    return 1 if s.shape[1] == rows else EMB_FP8_BLOCK
+def _block_rows(s: torch.Tensor, rows: int, k_blocks: int, name: str) -> int:
+    shape = s.shape
+    if len(shape) == 2 and shape[0] == k_blocks:
+        if shape[1] == rows:
+            return 1
+        if shape[1] == (rows + 127) >> 7:
+            return EMB_FP8_BLOCK
+    raise ValueError(f"{name} must be [ceil(k/128), rows] or [ceil(k/128), ceil(rows/128)], got {tuple(shape)}")
 
 
 def emb_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor,
@@ -651,56 +681,62 @@ def emb_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
     """a[m, k] @ b[n, k].T of codes and scales from emb_fp8_quantize (+ bias[n]).
     workspace: emb_fp8_matmul_workspace_size bytes that the caller keeps; made
     for the call if None."""
-    lda, ldb = _code_ld(a, "a"), _code_ld(b, "b")
-    (m, k), n = a.shape, b.shape[0]
-    if b.shape[1] != k:
-        raise ValueError(f"a and b must have the same columns, got {k} and {b.shape[1]}")
+    lda, ldb = _code_stride(a, "a"), _code_stride(b, "b")
+    (m, k), (n, kb) = a.shape, b.shape
+    if kb != k:
+        raise ValueError(f"a and b must have the same columns, got {k} and {kb}")
     if bias is not None and bias.numel() != n:
         raise ValueError(f"bias must have {n} elements")
+    blocks = (k + 127) >> 7
+    a_rows, b_rows = _block_rows(sa, m, blocks, "sa"), _block_rows(sb, n, blocks, "sb")
     if out is None:
-        out = _alloc(stream, (m, n), out_dtype, a.device)
-    elif tuple(out.shape) != (m, n):
-        raise ValueError(f"out must be [{m}, {n}]")
-    ldo = _matrix(out, None, "out")
+        out, ldo = _empty(stream, a, (m, n), out_dtype), n
+    else:
+        if tuple(out.shape) != (m, n):
+            raise ValueError(f"out must be [{m}, {n}]")
+        ldo = _row_stride(out, "out")
     if workspace is None:
-        workspace = _alloc(stream, (emb_fp8_matmul_workspace_size(m, n, k),), torch.uint8, a.device)
-    _check(lib().emb_fp8_matmul(a.data_ptr(), lda, _cuda(sa, torch.float32, "sa"), _block_rows(sa, m, k, "sa"),
-                                b.data_ptr(), ldb, _cuda(sb, torch.float32, "sb"), _block_rows(sb, n, k, "sb"), m, n, k,
-                                None if bias is None else _cuda(bias, torch.float32, "bias"), out.data_ptr(),
-                                _ftype(out, "out"), ldo, _cuda(workspace, None, "workspace"),
-                                workspace.numel() * workspace.element_size(), _stream(stream)))
+        workspace = _empty(stream, a, emb_fp8_matmul_workspace_size(m, n, k), torch.uint8)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    f32 = torch.float32
+    _check(lib().emb_fp8_matmul(a.data_ptr(), lda, _dense(sa, f32, "sa"), a_rows, b.data_ptr(), ldb, _dense(sb, f32, "sb"),
+                                b_rows, m, n, k, _dense(bias, f32, "bias"), out.data_ptr(), _ftype(out.dtype, "out"), ldo,
+                                workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream)))
     return out
 
 
 def _norm_gate(x: torch.Tensor, block_dtype: torch.dtype, gate, norm: str, act: str, eps: float,
                res_scale: float) -> _NormGate:
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x, f, y, h and their gradients must be matrices of one shape")
-    r, d = x.shape
+    r, d = shape
     kind = 0
     if gate is not None:
-        kind = {(r, d): 1, (r, 1): 2, (d,): 3}.get(tuple(gate.shape), 0)
+        gs = gate.shape
+        kind = 1 if gs == shape else 2 if gs == (r, 1) else 3 if gs == (d,) else 0
         if kind == 0:
-            raise ValueError(f"gate must be [{r}, {d}], [{r}, 1] or [{d}], got {tuple(gate.shape)}")
-        if gate.dtype != (torch.float32 if kind == 3 else block_dtype):
+            raise ValueError(f"gate must be [{r}, {d}], [{r}, 1] or [{d}], got {tuple(gs)}")
+        if gate.dtype is not (torch.float32 if kind == 3 else block_dtype):
             raise TypeError("a gate per element or row has f's type, a gate per channel is float32")
-    if block_dtype not in _FTYPE:
-        raise TypeError(f"f and h must be float32, bfloat16 or float16, got {block_dtype}")
-    return _NormGate(r, d, _ftype(x, "x"), _FTYPE[block_dtype], _NORM[norm], kind, _ACT[act], eps, res_scale)
+    return _NormGate(r, d, _ftype(x.dtype, "x"), _ftype(block_dtype, "f"), _NORM[norm], kind, _ACT[act], eps, res_scale)
 
 
 def _vector(t: Optional[torch.Tensor], dim: int, name: str):
-    if t is not None and t.numel() != dim:
-        raise ValueError(f"{name} must have {dim} elements")
-    return None if t is None else _cuda(t, torch.float32, name)
-
-
-def _same(t: Optional[torch.Tensor], like: torch.Tensor, name: str):
     if t is None:
         return None
-    if t.shape != like.shape:
-        raise ValueError(f"{name} must be {tuple(like.shape)}, got {tuple(t.shape)}")
-    return _cuda(t, like.dtype, name)
+    if t.numel() != dim:
+        raise ValueError(f"{name} must have {dim} elements")
+    return _dense(t, torch.float32, name)
+
+
+def _same(t: Optional[torch.Tensor], shape, dtype, name: str):
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return _dense(t, dtype, name)
 
 
 def emb_norm_gate_fwd(x: torch.Tensor, f: Optional[torch.Tensor], gate: Optional[torch.Tensor] = None, *,
@@ -713,18 +749,18 @@ def emb_norm_gate_fwd(x: torch.Tensor, f: Optional[torch.Tensor], gate: Optional
     pre=False: no norm follows (h is None).  gate: [rows, dim] or [rows, 1] in f's
     type, or float32 [dim].  stats: float32 [rows, 4] for the backward, or None
     with stats=False.  block_dtype: h's type where f is None (default x's)."""
-    block_dtype = f.dtype if f is not None else block_dtype or x.dtype
+    shape, st_type = x.shape, x.dtype
+    block_dtype = f.dtype if f is not None else block_dtype or st_type
     d = _norm_gate(x, block_dtype, gate, norm, act, eps, res_scale)
-    if f is not None and f.shape != x.shape:
-        raise ValueError(f"f must be {tuple(x.shape)}, got {tuple(f.shape)}")
-    y = None if f is None else _alloc(stream, x.shape, x.dtype, x.device)
-    h = _alloc(stream, x.shape, block_dtype, x.device) if pre else None
-    st = _alloc(stream, (x.shape[0], 4), torch.float32, x.device) if stats else None
-    _check(lib().emb_norm_gate_fwd(ctypes.byref(d), _cuda(x, None, "x"), None if f is None else _cuda(f, None, "f"),
-                                   None if gate is None else _cuda(gate, None, "gate"),
-                                   _vector(w_post, d.dim, "w_post"), _vector(b_post, d.dim, "b_post"),
-                                   _vector(w_pre, d.dim, "w_pre"), _vector(b_pre, d.dim, "b_pre"), _ptr(y), _ptr(h),
-                                   _ptr(st), _stream(stream)))
+    dim = d.dim
+    xp, fp, gp = _dense(x, st_type, "x"), _same(f, shape, block_dtype, "f"), None if gate is None else _dense(gate, gate.dtype, "gate")
+    wp, bp = _vector(w_post, dim, "w_post"), _vector(b_post, dim, "b_post")
+    wq, bq = _vector(w_pre, dim, "w_pre"), _vector(b_pre, dim, "b_pre")
+    y = None if f is None else _empty(stream, x, shape, st_type)
+    h = _empty(stream, x, shape, block_dtype) if pre else None
+    st = _empty(stream, x, (shape[0], 4), torch.float32) if stats else None
+    _check(lib().emb_norm_gate_fwd(ctypes.byref(d), xp, fp, gp, wp, bp, wq, bq, None if y is None else y.data_ptr(),
+                                   h.data_ptr() if pre else None, st.data_ptr() if stats else None, _raw_stream(stream)))
     return y, h, st
 
 
@@ -745,55 +781,47 @@ def emb_norm_gate_bwd(dy: Optional[torch.Tensor], dh: Optional[torch.Tensor], y:
     dh (of h), either None if absent: {"dx", "df", "dgate", "dw_post", "db_post",
     "dw_pre", "db_pre"}, None for those of an input that is absent.  y: the
     forward's y (its x where f is None)."""
-    like = f if f is not None else dh
-    if like is None:
+    if f is None and dh is None:
         raise ValueError("f and dh are both None")
-    d = _norm_gate(y, like.dtype, gate, norm, act, eps, res_scale)
-    if like.shape != y.shape:
-        raise ValueError(f"f must be {tuple(y.shape)}, got {tuple(like.shape)}")
-    r, dim, dev = d.rows, d.dim, y.device
-    if tuple(stats.shape) != (r, 4):
-        raise ValueError(f"stats must be [{r}, 4]")
-
-    def vec(like):
-        return None if like is None else _alloc(stream, (dim,), torch.float32, dev)
-
-    dy_p, dh_p = _same(dy, y, "dy"), None
-    if dh is not None:
-        if dh.shape != y.shape:
-            raise ValueError(f"dh must be {tuple(y.shape)}, got {tuple(dh.shape)}")
-        dh_p = _cuda(dh, like.dtype, "dh")
-    out = {"dx": _alloc(stream, y.shape, y.dtype, dev), "df": None if f is None else _alloc(stream, f.shape, f.dtype, dev),
-           "dgate": None if gate is None else _alloc(stream, gate.shape, gate.dtype, dev),
-           "dw_post": vec(w_post), "db_post": vec(b_post), "dw_pre": vec(w_pre), "db_pre": vec(b_pre)}
-    if workspace is None:
-        workspace = _alloc(stream, (emb_norm_gate_bwd_workspace_size(r, dim),), torch.uint8, dev)
+    shape, st_type = y.shape, y.dtype
+    bt = f.dtype if f is not None else dh.dtype
+    d = _norm_gate(y, bt, gate, norm, act, eps, res_scale)
+    r, dim = shape
+    f32 = torch.float32
+    ins = (_same(dy, shape, st_type, "dy"), _same(dh, shape, bt, "dh"), _dense(y, st_type, "y"), _same(f, shape, bt, "f"),
+           None if gate is None else _dense(gate, gate.dtype, "gate"), _same(stats, (r, 4), f32, "stats"),
+           _vector(w_post, dim, "w_post"), _vector(b_post, dim, "b_post"), _vector(w_pre, dim, "w_pre"))
     _vector(b_pre, dim, "b_pre")
-    _check(lib().emb_norm_gate_bwd(ctypes.byref(d), dy_p, dh_p, _cuda(y, None, "y"),
-                                   None if f is None else _cuda(f, None, "f"),
-                                   None if gate is None else _cuda(gate, None, "gate"), _cuda(stats, torch.float32, "stats"),
-                                   _vector(w_post, dim, "w_post"), _vector(b_post, dim, "b_post"),
-                                   _vector(w_pre, dim, "w_pre"), _ptr(out["dx"]), _ptr(out["df"]), _ptr(out["dgate"]),
-                                   _ptr(out["dw_post"]), _ptr(out["db_post"]), _ptr(out["dw_pre"]), _ptr(out["db_pre"]),
-                                   _cuda(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
-                                   _stream(stream)))
+    out = {"dx": _empty(stream, y, shape, st_type), "df": None if f is None else _empty(stream, y, shape, bt),
+           "dgate": None if gate is None else _empty(stream, y, gate.shape, gate.dtype)}
+    for name, v in (("dw_post", w_post), ("db_post", b_post), ("dw_pre", w_pre), ("db_pre", b_pre)):
+        out[name] = None if v is None else _empty(stream, y, (dim,), f32)
+    if workspace is None:
+        workspace = _empty(stream, y, emb_norm_gate_bwd_workspace_size(r, dim), torch.uint8)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    _check(lib().emb_norm_gate_bwd(ctypes.byref(d), *ins, *[None if v is None else v.data_ptr() for v in out.values()],
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream)))
     return out
 
 
 def emb_adamw_step(tensors, grads, params: _AdamwParams, stream=None) -> None:
-    """One step over a ctypes array of _AdamwTensor and one of gradient pointers (AdamW builds both)."""
-    _check(lib().emb_adamw_step(tensors, grads, len(tensors), ctypes.byref(params), _stream(stream)))
+    """One step over a ctypes array of _AdamwTensor and the address of an array of gradient pointers (AdamW makes both)."""
+    _check(lib().emb_adamw_step(tensors, grads, len(tensors), ctypes.byref(params), _raw_stream(stream)))
+
+
+_dtype_of, _on_cuda = operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
 
 
 class AdamW:
-    """AdamW over a list of tensors, one launch a step.  params: contiguous CUDA
-    tensors (float32, bfloat16 or float16), updated in place.  copies: for each
-    float32 parameter a bfloat16 or float16 tensor (or None) that receives the
-    updated weights, as the "f16m" tables keep them.  state "f32", or "q8": m and
-    sqrt(v) as e4m3 codes with a scale per 256 elements, stochastically rounded
-    from `seed`.  The states live in `arena` (m, v, m_scale, v_scale: all
-    tensors one after another, each from a multiple of 256 elements), which
-    with `step_count` is the checkpoint; load_state takes per-tensor lists."""
+    """AdamW over a list of tensors, one launch a step (per 380 tensors).  params:
+    contiguous CUDA tensors (float32, bfloat16 or float16), updated in place.
+    copies: for each float32 parameter a bfloat16 or float16 tensor (or None) that
+    receives the updated weights, as the "f16m" tables keep them.  state "f32", or
+    "q8": m and sqrt(v) as e4m3 codes with a scale per 256 elements,
+    stochastically rounded from `seed`.  The states live in `arena` (m, v, m_scale,
+    v_scale: all tensors one after another, each from a multiple of 256 elements),
+    which with `step_count` is the checkpoint; load_state takes per-tensor lists."""
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999),
                  eps: float = 1e-8, weight_decay: float = 0.01, state: str = "f32", seed: int = 0,
@@ -806,7 +834,8 @@ class AdamW:
         self._copies = list(copies) if copies is not None else [None] * len(self.params)
         if len(self._copies) != len(self.params):
             raise ValueError("copies must have one entry per parameter")
-        q8 = _ADAM_STATE[state] == 1
+        self._state = _ADAM_STATE[state]
+        q8 = self._state == 1
         block = EMB_ADAM_BLOCK
         self._n = [p.numel() for p in self.params]
         self._at = [0]
@@ -825,28 +854,33 @@ class AdamW:
                 raise ValueError("parameters must be on one device")
             if c is not None and c.numel() != p.numel():
                 raise ValueError("a copy must have its parameter's size")
-            at = self._at[i]
-            self._tensors[i] = _AdamwTensor(_cuda(p, None, "param"), None if c is None else _cuda(c, None, "copy"),
+            at, kind = self._at[i], _ftype(p.dtype, "param")
+            self._tensors[i] = _AdamwTensor(_dense(p, p.dtype, "param"), None if c is None else _dense(c, c.dtype, "copy"),
                                             base["m"] + at * st.itemsize, base["v"] + at * st.itemsize,
                                             base["m_scale"] + at // block * 4 if q8 else None,
                                             base["v_scale"] + at // block * 4 if q8 else None, self._n[i], at,
-                                            _ftype(p, "param"), _ftype(p, "param"), 0 if c is None else _ftype(c, "copy"))
+                                            kind, kind, 0 if c is None else _ftype(c.dtype, "copy"))
         self._grad_dtypes = [p.dtype for p in self.params]
 
     def load_state(self, step: int, m, v, m_scale=None, v_scale=None) -> None:
         """Sets the states from one tensor per parameter (the layout of `arena`, without its padding)."""
         for key, parts in (("m", m), ("v", v), ("m_scale", m_scale), ("v_scale", v_scale)):
-            if (parts is None) != (self.arena[key] is None):
+            whole = self.arena[key]
+            if (parts is None) != (whole is None):
                 raise ValueError(f"{key} does not match the state kind {self.state}")
             if parts is None:
                 continue
-            whole = self.arena[key]
+            to, of = [], []
             for part, at, n in zip(parts, self._at, self._n):
                 if key.endswith("scale"):
                     at, n = at // EMB_ADAM_BLOCK, -(-n // EMB_ADAM_BLOCK)
                 if part.numel() != n or part.dtype != whole.dtype:
                     raise ValueError(f"{key}: expected {n} elements of {whole.dtype}")
-                whole[at:at + n].view(torch.uint8).copy_(part.reshape(-1).view(torch.uint8))
+                to.append(whole[at:at + n].view(torch.uint8))
+                of.append(part.reshape(-1).view(torch.uint8))
+            if len(to) != len(self.params):
+                raise ValueError(f"{key}: expected {len(self.params)} tensors")
+            torch._foreach_copy_(to, of)
         self.step_count = int(step)
 
     def step(self, grads: Sequence[torch.Tensor], grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -854,25 +888,26 @@ class AdamW:
         float16); grad_scale: device float32 scalar that multiplies them."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients are needed, got {len(grads)}")
-        if [g.numel() for g in grads] != self._n or not all([g.is_cuda and g.is_contiguous() for g in grads]):
+        T = torch.Tensor
+        if list(map(T.numel, grads)) != self._n or not all(map(T.is_contiguous, grads)) or not all(map(_on_cuda, grads)):
             raise ValueError("each gradient must be a contiguous CUDA tensor of its parameter's size")
-        dtypes = [g.dtype for g in grads]
+        dtypes = list(map(_dtype_of, grads))
         if dtypes != self._grad_dtypes:
-            for t, g in zip(self._tensors, grads):
-                t.grad_t = _ftype(g, "grad")
+            kinds = [_ftype(g, "grad") for g in dtypes]
+            for t, kind in zip(self._tensors, kinds):
+                t.grad_t = kind
             self._grad_dtypes = dtypes
-        ptrs = (ctypes.c_void_p * len(grads))(*[g.data_ptr() for g in grads])
+        ptrs = array.array("Q", map(T.data_ptr, grads))
         p = _AdamwParams(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, self.step_count + 1,
-                         _ADAM_STATE[self.state], self.seed & 0xFFFFFFFF,
-                         None if grad_scale is None else _cuda(grad_scale, torch.float32, "grad_scale"))
-        emb_adamw_step(self._tensors, ptrs, p, stream)
+                         self._state, self.seed & 0xFFFFFFFF, _dense(grad_scale, torch.float32, "grad_scale"))
+        emb_adamw_step(self._tensors, ptrs.buffer_info()[0], p, stream)
         self.step_count += 1
 
 
 def emb_check_op_flag(stream=None) -> int:
     """Synchronise, read and clear the dense operators' flag word (0 = clean)."""
     f = ctypes.c_uint32()
-    rc = lib().emb_check_op_flag(_stream(stream), ctypes.byref(f))
+    rc = lib().emb_check_op_flag(_raw_stream(stream), ctypes.byref(f))
     if rc not in (EMB_OK, 8):
         raise EmbError(rc, emb_last_error())
     return f.value

@@ -32,7 +32,7 @@ struct TensorArg {
   unsigned char pt, gt, ct, vec;
 };
 
-// Launches of up to 40 tensors pass 4 KB of parameters, larger ones up to 32 KB.
+// Launches of up to 40 tensors pass 4 KB of parameters, of up to 120 12 KB, larger ones 32 KB.
 template <int N>
 struct StepArgs {
   TensorArg t[N];
@@ -266,21 +266,20 @@ __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ S
   }
 }
 
-emb_status check_tensor(const emb_adamw_tensor& t, const void* g, bool q8, int i) {
-  const std::string at = "tensor " + std::to_string(i) + ": ";
-  if (t.n < 0 || t.first < 0) return fail(EMB_ERR_INVALID_ARG, at + "negative n or first");
-  if (!good_ftype(t.param_t) || !good_ftype(t.grad_t)) return fail(EMB_ERR_INVALID_ARG, at + "bad element type");
+const char* bad_tensor(const emb_adamw_tensor& t, const void* g, bool q8) {
+  if (t.n < 0 || t.first < 0) return "negative n or first";
+  if (!good_ftype(t.param_t) || !good_ftype(t.grad_t)) return "bad element type";
   if (t.copy_d && (t.param_t != EMB_T_F32 || (t.copy_t != EMB_T_BF16 && t.copy_t != EMB_T_F16)))
-    return fail(EMB_ERR_INVALID_ARG, at + "a copy is bf16 or f16 of float32 weights");
-  if (t.n == 0) return EMB_OK;
-  if (!t.param_d || !g || !t.m_d || !t.v_d) return fail(EMB_ERR_INVALID_ARG, at + "param, grad, m or v is NULL");
-  if (q8 && (!t.m_scale_d || !t.v_scale_d)) return fail(EMB_ERR_INVALID_ARG, at + "8-bit states need their scales");
+    return "a copy is bf16 or f16 of float32 weights";
+  if (t.n == 0) return nullptr;
+  if (!t.param_d || !g || !t.m_d || !t.v_d) return "param, grad, m or v is NULL";
+  if (q8 && (!t.m_scale_d || !t.v_scale_d)) return "8-bit states need their scales";
   const size_t st = q8 ? 1 : 4;
   if (!aligned_to(t.param_d, ftype_bytes(t.param_t)) || !aligned_to(g, ftype_bytes(t.grad_t)) ||
       !aligned_to(t.m_d, st) || !aligned_to(t.v_d, st) || !aligned_to(t.copy_d, 2) || !aligned_to(t.m_scale_d, 4) ||
       !aligned_to(t.v_scale_d, 4))
-    return fail(EMB_ERR_INVALID_ARG, at + "an array is not aligned to its elements");
-  return EMB_OK;
+    return "an array is not aligned to its elements";
+  return nullptr;
 }
 
 template <bool kQ8, int N>
@@ -339,11 +338,11 @@ extern "C" emb_status emb_adamw_step(const emb_adamw_tensor* tensors, const void
   if (p.state != EMB_ADAM_F32 && p.state != EMB_ADAM_Q8) return fail(EMB_ERR_INVALID_ARG, "bad state kind");
   const bool q8 = p.state == EMB_ADAM_Q8;
   for (int i = 0; i < n_tensors; ++i) {
-    const emb_status rc = check_tensor(tensors[i], grads[i], q8, i);
-    if (rc != EMB_OK) return rc;
+    if (const char* why = bad_tensor(tensors[i], grads[i], q8))
+      return fail(EMB_ERR_INVALID_ARG, "tensor " + std::to_string(i) + ": " + why);
     if (tensors[i].n / EMB_ADAM_BLOCK >= 0x7fffff00LL) return fail(EMB_ERR_UNSUPPORTED, "a tensor has over 2^39 elements");
   }
-  constexpr int kFew = 40, kMany = 380;
+  constexpr int kFew = 40, kSome = 120, kMany = 380;
   static_assert(sizeof(StepArgs<kFew>) <= 4096 && sizeof(StepArgs<kMany>) <= 32764, "kernel parameters");
   int done = 0;
   while (done < n_tensors) {
@@ -362,6 +361,9 @@ extern "C" emb_status emb_adamw_step(const emb_adamw_tensor* tensors, const void
     if (k - done <= kFew)
       e = q8 ? launch<true, kFew>(t, g, k - done, params, (unsigned)units, (cudaStream_t)stream)
              : launch<false, kFew>(t, g, k - done, params, (unsigned)units, (cudaStream_t)stream);
+    else if (k - done <= kSome)
+      e = q8 ? launch<true, kSome>(t, g, k - done, params, (unsigned)units, (cudaStream_t)stream)
+             : launch<false, kSome>(t, g, k - done, params, (unsigned)units, (cudaStream_t)stream);
     else
       e = q8 ? launch<true, kMany>(t, g, k - done, params, (unsigned)units, (cudaStream_t)stream)
              : launch<false, kMany>(t, g, k - done, params, (unsigned)units, (cudaStream_t)stream);

@@ -2,7 +2,7 @@
 //   out[i, j] = bias[j] + sum_b sa[b, i] sb[b, j] sum_{k in b} a[i, k] b[j, k]
 // over blocks b of 128 k's.
 //
-// Tile kernel (m > 8).  A persistent block per SM computes tiles of 128 x BN.
+// Tile kernel (m > 2).  A persistent block per SM computes tiles of 128 x BN.
 // One warp brings 128-byte-wide slabs of both operands into a ring of shared
 // memory stages by TMA (128-byte swizzle; rows and columns past the edges
 // arrive as zeros); one thread issues four tcgen05.mma (e4m3, K = 32 each) a
@@ -19,8 +19,9 @@
 // to the workspace and a second launch adds them in order).  The split depends
 // on the sizes and the SM count alone.
 //
-// Row kernel (m <= 8): bound by reading b once; plain CUDA cores, one or more
-// warps per row of b.
+// Row kernel (m <= 2): bound by reading b once; plain CUDA cores, one or more
+// warps per row of b.  From three rows on the tile kernel is faster (4 x 1024 x
+// 8192: 15 us against 18).
 #include <cuda.h>
 
 #include <algorithm>
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Matmu
 
 // ------------------------------------------------------------------ row kernel
 
-constexpr int kRowMax = 8;
+constexpr int kRowMax = 2;
 
 // 16 codes as floats.
 __device__ __forceinline__ void codes16(const uint4& q, float* o) {
@@ -565,10 +566,11 @@ __device__ __forceinline__ uint4 head16(uint4 q, int keep) {
 }
 
 // A block's eight warps take 8 / S rows of b, S warps to a row; a lane takes 16
-// neighbouring k's (one scale block for eight lanes) every 512 S.
+// neighbouring k's (one scale block for eight lanes) every 512 S, four such
+// pieces of both operands on their way at a time.
 template <int M, int S, typename OT>
 __global__ void __launch_bounds__(256) row_kernel(const __grid_constant__ MatmulArgs p) {
-  constexpr int kRows = 8 / S;
+  constexpr int kRows = 8 / S, kBatch = 4;
   __shared__ float part[8][M];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int j = blockIdx.x * kRows + warp / S;
@@ -578,24 +580,39 @@ __global__ void __launch_bounds__(256) row_kernel(const __grid_constant__ Matmul
   if (j < p.n) {
     const unsigned char* b = p.b + j * p.ldb;
     const float* sb = p.sb + (j >> p.b_shift);
-#pragma unroll 4
-    for (int k = ((warp % S) * 32 + lane) * 16; k < p.k; k += S * 512) {
-      const int kb = k / kBK;
-      uint4 q = __ldg(reinterpret_cast<const uint4*>(b + k));  // rows are multiples of 16 bytes: in bounds
-      if (k + 16 > p.k) q = head16(q, p.k - k);
-      float w[16];
-      codes16(q, w);
-      const float s = __ldg(sb + kb * p.sb_row);
+    for (int k0 = ((warp % S) * 32 + lane) * 16; k0 < p.k; k0 += kBatch * S * 512) {
+      uint4 qb[kBatch], qa[kBatch][M];
+      float s[kBatch][M];
 #pragma unroll
-      for (int i = 0; i < M; ++i) {
-        if (i < p.m) {
-          uint4 qa = __ldg(reinterpret_cast<const uint4*>(p.a + i * p.lda + k));
-          if (k + 16 > p.k) qa = head16(qa, p.k - k);
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = k0 + u * S * 512;
+        const bool in = k < p.k;
+        const int kb = k / kBK;
+        qb[u] = in ? __ldg(reinterpret_cast<const uint4*>(b + k)) : make_uint4(0, 0, 0, 0);  // rows are multiples of 16 bytes
+        const float t = in ? __ldg(sb + kb * p.sb_row) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+          qa[u][i] = in && i < p.m ? __ldg(reinterpret_cast<const uint4*>(p.a + i * p.lda + k)) : make_uint4(0, 0, 0, 0);
+          s[u][i] = in && i < p.m ? t * __ldg(p.sa + kb * p.sa_row + (i >> p.a_shift)) : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int left = p.k - (k0 + u * S * 512);
+        if (left < 16) {  // the row's last piece: what lies past k does not count
+          qb[u] = head16(qb[u], max(left, 0));
+#pragma unroll
+          for (int i = 0; i < M; ++i) qa[u][i] = head16(qa[u][i], max(left, 0));
+        }
+        float w[16];
+        codes16(qb[u], w);
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
           float x[16], d = 0.0f;
-          codes16(qa, x);
+          codes16(qa[u][i], x);
 #pragma unroll
           for (int c = 0; c < 16; ++c) d = fmaf(x[c], w[c], d);
-          acc[i] = fmaf(d, s * __ldg(p.sa + kb * p.sa_row + (i >> p.a_shift)), acc[i]);
+          acc[i] = fmaf(d, s[u][i], acc[i]);
         }
       }
     }
@@ -716,10 +733,7 @@ cudaError_t launch(const MatmulArgs& p, const Plan& pl, const CUtensorMap& ma, c
     return cudaGetLastError();
   }
   if (pl.bn == 0) {
-    if (p.m == 1) return launch_rows<1, OT>(p, st);
-    if (p.m == 2) return launch_rows<2, OT>(p, st);
-    if (p.m <= 4) return launch_rows<4, OT>(p, st);
-    return launch_rows<8, OT>(p, st);
+    return p.m == 1 ? launch_rows<1, OT>(p, st) : launch_rows<2, OT>(p, st);
   }
   if (pl.bn == 64) return launch_tiles<64, OT>(p, pl, ma, mb, st);
   if (pl.bn == 128) return launch_tiles<128, OT>(p, pl, ma, mb, st);
