@@ -653,7 +653,7 @@ typedef struct {
   float* m_scale_d; /* Q8: float32[ceil(n/256)] */
   float* v_scale_d;
   int64_t n;        /* elements; 0 is allowed */
-  int64_t first;    /* Q8: number of this tensor's first element among all, for the random numbers */
+  int64_t first;    /* Q8: number of this tensor's first element among all, for the random numbers; a multiple of 256 */
   emb_ftype param_t, grad_t, copy_t;
 } emb_adamw_tensor;
 typedef struct {

@@ -100,24 +100,28 @@ __device__ __forceinline__ unsigned fmix32(unsigned h) {
   return h ^ (h >> 16);
 }
 
-// A magnitude in code units (at most 448 after the clamp) to one of the two
-// codes around it, upwards with the probability of its distance from the lower
-// one.  Codes from 2^-6 on have 3 mantissa bits: adding 20 random bits below
-// them and cutting rounds to one of them.  Below 2^-6 codes are 2^-9 apart;
-// adding 2^-6 first puts that spacing at the same bit.  mag is finite.
+// A magnitude in code units to one of the two codes around it, upwards with the
+// probability of its distance from the lower one.  Codes from 2^-6 on have 3
+// mantissa bits: adding 20 random bits below them and cutting rounds to one of
+// them.  Below 2^-6 codes are 2^-9 apart; adding 2^-6 first puts that spacing at
+// the same bit.  The block's largest value is 448 up to three units in its last
+// place, and r20 leaves seven, so it is never carried past 448.  mag is finite.
 __device__ __forceinline__ float round_random(float mag, unsigned r20) {
-  mag = fminf(mag, kE4m3Max);
   const float base = mag < 0.015625f ? 0.015625f : 0.0f;
   const unsigned cut = (__float_as_uint(__fadd_rn(mag, base)) + r20) & ~0xFFFFFu;
   return __fsub_rn(__uint_as_float(cut), base);
 }
 
-__device__ __forceinline__ float warp_amax(float a) {  // a >= 0: the bits order as the values
-  return fmaxf(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a))), kAmaxFloor);
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN where either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
-
+__device__ __forceinline__ unsigned warp_max(float a) {  // a >= 0 or NaN: the bits order as the values, NaN last
+  return __reduce_max_sync(0xffffffffu, __float_as_uint(a));
+}
 template <bool kQ8, int N>
-__global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ StepArgs<N> a) {
+__global__ void __launch_bounds__(256, 4) adamw_kernel(const __grid_constant__ StepArgs<N> a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
   const unsigned end = min(a.n_units, (blockIdx.x + 1) * a.span);
@@ -204,30 +208,43 @@ __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ S
         }
     }
     if constexpr (kQ8) {
-      float am = 0.0f, au = 0.0f;  // elements past the end are zeros here and do not count
+      float am = 0.0f, au = 0.0f;  // elements past the end are zeros, and so are their moments
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        if (k < cnt) {
+        am = max_nan(am, fabsf(m[k]));
+        au = max_nan(au, u[k]);
+      }
+      unsigned bm = warp_max(am), bu = warp_max(au);
+      const bool finite = max(bm, bu) < 0x7f800000u;  // the same in all lanes
+      if (!finite) {
+        am = au = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
           am = fmaxf(am, finite_abs(m[k]));
           au = fmaxf(au, finite_abs(u[k]));
         }
+        bm = warp_max(am);
+        bu = warp_max(au);
       }
-      am = warp_amax(am);
-      au = warp_amax(au);
+      am = fmaxf(__uint_as_float(bm), kAmaxFloor);
+      au = fmaxf(__uint_as_float(bu), kAmaxFloor);
       const float im = inv_of(am), iu = inv_of(au);
-      const unsigned long long e0 = (unsigned long long)(t.first + i0);
+      const unsigned long long e0 = (unsigned long long)(t.first + i0);  // a multiple of eight: the upper half is the same for all eight
+      const unsigned mix = ((unsigned)(e0 >> 32) * 0x9e3779b9u) ^ a.key;
       float qm[8], qu[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const unsigned long long e = e0 + k;
-        const unsigned r = fmix32((unsigned)e ^ ((unsigned)(e >> 32) * 0x9e3779b9u) ^ a.key);
-        // a value that is not finite would carry out of its bits above: it becomes the code NaN here
+        const unsigned r = fmix32(((unsigned)e0 + k) ^ mix);
         const float xm = __fmul_rn(m[k], im);
-        const float a_m = round_random(fabsf(xm), ((r & 0xffffu) << 4) + 8u);
-        qm[k] = finite_f32(m[k]) ? (xm < 0.0f ? -a_m : a_m) : __uint_as_float(0x7fc00000u);
-        float a_u = round_random(__fmul_rn(u[k], iu), ((r >> 16) << 4) + 8u);
-        if (u[k] > 0.0f && a_u == 0.0f) a_u = 0.001953125f;
-        qu[k] = finite_f32(u[k]) ? a_u : __uint_as_float(0x7fc00000u);
+        qm[k] = copysignf(round_random(fabsf(xm), ((r & 0xffffu) << 4) + 8u), xm);
+        qu[k] = fmaxf(round_random(__fmul_rn(u[k], iu), ((r >> 16) << 4) + 8u), u[k] > 0.0f ? 0.001953125f : 0.0f);
+      }
+      if (!finite) {  // such a value would have carried out of its bits: it becomes the code NaN
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (!finite_f32(m[k])) qm[k] = __uint_as_float(0x7fc00000u);
+          if (!finite_f32(u[k])) qu[k] = __uint_as_float(0x7fc00000u);
+        }
       }
       unsigned wm[2], wu[2];
 #pragma unroll
@@ -267,7 +284,7 @@ __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ S
 }
 
 const char* bad_tensor(const emb_adamw_tensor& t, const void* g, bool q8) {
-  if (t.n < 0 || t.first < 0) return "negative n or first";
+  if (t.n < 0 || t.first < 0 || t.first % EMB_ADAM_BLOCK) return "n is negative, or first no multiple of 256";
   if (!good_ftype(t.param_t) || !good_ftype(t.grad_t)) return "bad element type";
   if (t.copy_d && (t.param_t != EMB_T_F32 || (t.copy_t != EMB_T_BF16 && t.copy_t != EMB_T_F16)))
     return "a copy is bf16 or f16 of float32 weights";

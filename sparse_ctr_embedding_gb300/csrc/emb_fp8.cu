@@ -28,11 +28,6 @@ struct QuantArgs {
 
 __device__ __forceinline__ unsigned amax_bits(float a) { return __reduce_max_sync(0xffffffffu, __float_as_uint(a)); }
 
-// One code; values that are not finite become NaN (the conversion would saturate an infinity).
-__device__ __forceinline__ float scaled(float x, float inv) {
-  return finite_f32(x) ? __fmul_rn(x, inv) : __uint_as_float(0x7fc00000u);
-}
-
 template <typename T>
 __device__ __forceinline__ void load4(const T* p, float* o);
 template <>
@@ -81,13 +76,30 @@ __global__ void __launch_bounds__(256, 2) quantize_kernel(const __grid_constant_
       for (int k = 0; k < 4; ++k) v[i][k] = r < a.rows && c0 + k < a.cols ? to_f32<T>(x[r * a.ldx + c0 + k]) : 0.0f;
     }
   }
-  float tile_amax = 0.0f;
-  if (SQUARE) {
+  // The largest magnitude of each row's four.  fmaxf passes NaN over, as it should;
+  // a thread that meets an infinity makes its infinities NaN first (e4m3 has none)
+  // and takes the maxima again.
+  float top[16];
+  auto maxima = [&] {
     float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      top[i] = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
+      m = fmaxf(m, top[i]);
+    }
+    return m;
+  };
+  float m = maxima();
+  if (m > kFltMax) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) m = fmaxf(m, finite_abs(v[i][k]));
+      for (int k = 0; k < 4; ++k)
+        if (!finite_f32(v[i][k])) v[i][k] = __uint_as_float(0x7fc00000u);
+    m = maxima();
+  }
+  float tile_amax = 0.0f;
+  if (SQUARE) {
     m = __uint_as_float(amax_bits(m));
     if (lane == 0) part[0][w] = m;
     __syncthreads();
@@ -105,13 +117,12 @@ __global__ void __launch_bounds__(256, 2) quantize_kernel(const __grid_constant_
       const long long r = r0 + i;
       float amax = tile_amax;
       if (!SQUARE) {
-        amax = fmaxf(fmaxf(finite_abs(v[i][0]), finite_abs(v[i][1])), fmaxf(finite_abs(v[i][2]), finite_abs(v[i][3])));
-        amax = fmaxf(__uint_as_float(amax_bits(amax)), kAmaxFloor);
+        amax = fmaxf(__uint_as_float(amax_bits(top[i])), kAmaxFloor);
         if (lane == 0 && r < a.rows) a.s[tc * a.srow + r] = scale_of(amax);
       }
       const float inv = inv_of(amax);
-      const unsigned c = e4m3x2(scaled(v[i][0], inv), scaled(v[i][1], inv)) |
-                         (e4m3x2(scaled(v[i][2], inv), scaled(v[i][3], inv)) << 16);
+      const unsigned c = e4m3x2(__fmul_rn(v[i][0], inv), __fmul_rn(v[i][1], inv)) |
+                         (e4m3x2(__fmul_rn(v[i][2], inv), __fmul_rn(v[i][3], inv)) << 16);
       // columns past the last one are zeros up to the row's next 16 bytes
       if (r < a.rows && c0 < ((a.cols + 15) & ~15LL)) *reinterpret_cast<unsigned*>(a.q + r * a.ldq + c0) = c;
     }
@@ -126,7 +137,7 @@ __global__ void __launch_bounds__(256, 2) quantize_kernel(const __grid_constant_
       for (int k = 0; k < 4; ++k) {
         float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m = fmaxf(m, finite_abs(v[i][k]));
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i][k]));
         part[w][lane * 4 + k] = m;
       }
       __syncthreads();
@@ -145,8 +156,8 @@ __global__ void __launch_bounds__(256, 2) quantize_kernel(const __grid_constant_
       unsigned c[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        c[j] = e4m3x2(scaled(v[4 * j][k], inv[k]), scaled(v[4 * j + 1][k], inv[k])) |
-               (e4m3x2(scaled(v[4 * j + 2][k], inv[k]), scaled(v[4 * j + 3][k], inv[k])) << 16);
+        c[j] = e4m3x2(__fmul_rn(v[4 * j][k], inv[k]), __fmul_rn(v[4 * j + 1][k], inv[k])) |
+               (e4m3x2(__fmul_rn(v[4 * j + 2][k], inv[k]), __fmul_rn(v[4 * j + 3][k], inv[k])) << 16);
       *reinterpret_cast<uint4*>(tile_t + (lane * 4 + k) * kTile + ((w ^ (lane & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
     }
     __syncthreads();

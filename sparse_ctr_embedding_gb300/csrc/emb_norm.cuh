@@ -1,23 +1,43 @@
 // Row access and row reductions shared by the norm kernels (emb_norm_fwd.cu,
 // emb_norm_bwd.cu).
 //
-// A row is worked on by a team of T threads, T a power of two from 8 to 1024
-// with 8 T >= dim, eight elements a thread: neighbouring ones read with one
-// 16- or 32-byte access where dim and the pointers allow it (VEC), else T
-// apart.  The whole row then sits in registers, every array is read once, and
-// the norm's mean and variance are taken in two exact steps from there.
+// A row is worked on by a team of T threads, T a power of two from 8 to 1024,
+// E elements a thread with E T >= dim.  Where dim and the pointers allow it
+// (VEC) a thread has eight neighbours, read with one 16- or 32-byte access;
+// else E (4, or 8 in teams of 1024) elements T apart.  The whole row then sits
+// in registers, every array is read once, and a norm's mean and variance are
+// taken in two exact steps from there.  Elements past the row's end are zeros
+// in registers.
 #pragma once
 
 #include "emb_dense.cuh"
 
 namespace emb {
 
-// This thread's eight elements of a row.
-template <typename T, bool VEC>
+constexpr int kNormBlock = 256;  // threads of a block, unless one team is larger
+
+// Elements a thread has.
+template <bool VEC, int MAXT>
+__host__ __device__ constexpr int norm_elems() {
+  return VEC || MAXT == 1024 ? 8 : 4;
+}
+inline int norm_team(int dim, bool vec) {
+  int t = 8;
+  while (t * (vec || t == 1024 ? 8 : 4) < dim) t *= 2;
+  return t;
+}
+
+// This thread's elements of a row.
+template <typename T, bool VEC, int E>
 struct RowPart;
-template <typename T>
-struct RowPart<T, true> {
+template <typename T, int E>
+struct RowPart<T, true, E> {
+  static_assert(E == 8, "one vector access");
   Raw8<T> r;
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.set2(k, 0.0f, 0.0f);
+  }
   __device__ __forceinline__ void load(const T* row, int t, int, int dim) {
     if (t * 8 < dim) r.load(row + t * 8);
   }
@@ -30,50 +50,69 @@ struct RowPart<T, true> {
     o.store(row + t * 8);
   }
 };
-template <typename T>
-struct RowPart<T, false> {
-  T v[8];
+template <typename T, int E>
+struct RowPart<T, false, E> {
+  T v[E];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < E; ++k) v[k] = from_f32<T>(0.0f);
+  }
   __device__ __forceinline__ void load(const T* row, int t, int team, int dim) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < E; ++k)
       if (t + k * team < dim) v[k] = row[t + k * team];
   }
   __device__ __forceinline__ float get(int k) const { return to_f32<T>(v[k]); }
   __device__ __forceinline__ static void store(T* row, const float* v, int t, int team, int dim) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < E; ++k)
       if (t + k * team < dim) row[t + k * team] = from_f32<T>(v[k]);
   }
 };
 
-// Column of this thread's k-th element, and whether the row has it.
+// Column of this thread's k-th element.
 template <bool VEC>
 __device__ __forceinline__ int part_col(int k, int t, int team) {
   return VEC ? t * 8 + k : t + k * team;
 }
 
-// This thread's eight elements of a float32 vector [dim] (NULL: all `absent`),
-// held in registers over the rows, or read again at each use.
-template <bool VEC, bool kHold>
+// This thread's elements of a float32 vector [dim] (NULL: all `absent`), held
+// in registers over the rows, or read again (from L1) for each row.
+template <bool VEC, bool kHold, int E>
 struct VecPart {
   const float* p;
   float absent;
-  int t, team, dim;
-  float v[kHold ? 8 : 1];
-  __device__ __forceinline__ float read(int k) const {
-    const int c = part_col<VEC>(k, t, team);
-    return p && c < dim ? __ldg(p + c) : absent;
-  }
-  __device__ __forceinline__ VecPart(const float* p_, float absent_, int t_, int team_, int dim_)
-      : p(p_), absent(absent_), t(t_), team(team_), dim(dim_) {
-    if constexpr (kHold) {
+  int t, team, dim, vec;
+  float v[kHold ? E : 1];
+  __device__ __forceinline__ void read(float* o) const {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = read(k);
+    for (int k = 0; k < E; ++k) o[k] = absent;
+    if (!p) return;
+    if (VEC && vec) {
+      if (t * 8 < dim) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p + t * 8)), b = __ldg(reinterpret_cast<const float4*>(p + t * 8 + 4));
+        o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
+        if constexpr (E == 8) o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const int c = part_col<VEC>(k, t, team);
+        if (c < dim) o[k] = __ldg(p + c);
+      }
     }
   }
-  __device__ __forceinline__ float get(int k) const {
-    if constexpr (kHold) return v[k];
-    else return read(k);
+  __device__ __forceinline__ VecPart(const float* p_, float absent_, int t_, int team_, int dim_)
+      : p(p_), absent(absent_), t(t_), team(team_), dim(dim_), vec((reinterpret_cast<uintptr_t>(p_) & 15) == 0) {
+    if constexpr (kHold) read(v);
+  }
+  __device__ __forceinline__ void get(float* o) const {
+    if constexpr (kHold) {
+#pragma unroll
+      for (int k = 0; k < E; ++k) o[k] = v[k];
+    } else {
+      read(o);
+    }
   }
 };
 
@@ -88,11 +127,14 @@ struct TeamSum {
   int bar;       // named barrier of the team
   float2* slots; // 2 x 32 of the team
   int set = 0;
-  __device__ __forceinline__ float2 operator()(float a, float b) {
-    for (int o = min(team, 32) >> 1; o; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
+  template <bool TWO>
+  __device__ __forceinline__ float2 sum(float a, float b) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      if (o < team) {  // the same in the whole block
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
+      }
     if (warps > 1) {
       float2* s = slots + set * 32;
       set ^= 1;
@@ -102,25 +144,21 @@ struct TeamSum {
       const float2 v = s[lane & (warps - 1)];
       a = v.x;
       b = v.y;
-      for (int o = warps >> 1; o; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1)
+        if (o < warps) {
+          a += __shfl_xor_sync(0xffffffffu, a, o);
+          if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
+        }
     }
     return make_float2(a, b);
   }
 };
 
-constexpr int kNormBlock = 256;  // threads of a block, unless one team is larger
-
-inline int norm_team(int dim) {
-  int t = 8;
-  while (t * 8 < dim) t *= 2;
-  return t;
-}
-
+// The reciprocal is the approximate one (2 units in the last place): the exact
+// one's ten instructions an element were a tenth of the kernels' time.
 __device__ __forceinline__ float activate(float g, int act) {
-  return act == EMB_ACT_SIGMOID ? 1.0f / (1.0f + expf(-g)) : g;
+  return act == EMB_ACT_SIGMOID ? __fdividef(1.0f, 1.0f + expf(-g)) : g;
 }
 
 emb_status check_norm(const emb_norm_gate_desc* d);

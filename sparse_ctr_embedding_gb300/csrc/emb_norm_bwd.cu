@@ -35,53 +35,64 @@ struct BwdArgs {
   float res_scale, inv_dim;
 };
 
-// Sums over a thread's rows for its eight columns.
-template <bool kHold>
+// Sums over a thread's rows for its columns: in registers, or for 1024-thread
+// teams (64 registers a thread) in shared memory, in words of the thread's own.
+template <bool kHold, int E>
 struct ColSums {
-  float v[kHold ? kSums : 1][8];
-  float* sh;  // !kHold: [kSums][8][blockDim] (a thread's own words, no sharing)
+  float v[kHold ? kSums : 1][E];
+  float* sh;  // !kHold: [kSums][E][blockDim]
   __device__ __forceinline__ explicit ColSums(float* shared) : sh(shared) {
 #pragma unroll
     for (int s = 0; s < kSums; ++s)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < E; ++k) {
         if constexpr (kHold) v[s][k] = 0.0f;
-        else sh[(s * 8 + k) * blockDim.x + threadIdx.x] = 0.0f;
+        else sh[(s * E + k) * blockDim.x + threadIdx.x] = 0.0f;
       }
   }
   __device__ __forceinline__ void add(int s, int k, float x) {
     if constexpr (kHold) v[s][k] += x;
-    else sh[(s * 8 + k) * blockDim.x + threadIdx.x] += x;
+    else sh[(s * E + k) * blockDim.x + threadIdx.x] += x;
   }
   __device__ __forceinline__ float get(int s, int k) const {
     if constexpr (kHold) return v[s][k];
-    else return sh[(s * 8 + k) * blockDim.x + threadIdx.x];
+    else return sh[(s * E + k) * blockDim.x + threadIdx.x];
   }
 };
 
 template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kernel(const __grid_constant__ BwdArgs a) {
-  constexpr bool kHold = MAXT < 1024;
+  constexpr bool kHold = MAXT < 1024;  // registers enough to keep vectors or sums, and to load a row ahead
+  constexpr int E = norm_elems<VEC, MAXT>();
   extern __shared__ float dyn[];
   __shared__ float2 slots[4][64];
   const int team = a.team, dim = a.dim;
   const int my_team = threadIdx.x / team;
-  TeamSum sum{team, (int)threadIdx.x % team, team >> 5, 1 + (my_team & 3), slots[my_team & 3]};
-  const int t = sum.t;
+  TeamSum sums{team, (int)threadIdx.x % team, team >> 5, 1 + (my_team & 3), slots[my_team & 3]};
+  const int t = sums.t;
   const int teams = blockDim.x / team;
   const long long stride = (long long)gridDim.x * teams;
   const bool has_f = a.f != nullptr, has_dh = a.dh != nullptr, has_dy = a.dy != nullptr;
   const bool gate_elem = a.gate_kind == EMB_GATE_ELEM;
   const float* const gate_col = a.gate_kind == EMB_GATE_COL ? (const float*)a.gate : nullptr;
 
-  VecPart<VEC, kHold> wp(a.w_post, 1.0f, t, team, dim), wq(a.w_pre, 1.0f, t, team, dim);
-  VecPart<VEC, kHold> bp(LAYER ? a.b_post : nullptr, 0.0f, t, team, dim), gc(gate_col, 0.0f, t, team, dim);
-  ColSums<kHold> cols(dyn);
+  // the vectors are read for each row: registers go to the rows on their way and the sums
+  VecPart<VEC, false, E> wp(a.w_post, 1.0f, t, team, dim), wq(a.w_pre, 1.0f, t, team, dim);
+  VecPart<VEC, false, E> bp(LAYER ? a.b_post : nullptr, 0.0f, t, team, dim), gc(gate_col, 0.0f, t, team, dim);
+  ColSums<kHold, E> cols(dyn);
 
-  RowPart<ST, VEC> rdy, ry;
-  RowPart<BT, VEC> rdh, rf, rg;
+  RowPart<ST, VEC, E> rdy, ry;
+  RowPart<BT, VEC, E> rdh, rf, rg;
   float grow = 0.0f;
   float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto clear = [&] {  // no row: zeros, which add nothing to any sum
+    rdy.clear();
+    ry.clear();
+    rdh.clear();
+    rf.clear();
+    rg.clear();
+    st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
   auto load = [&](long long r) {
     if (has_dy) rdy.load((const ST*)a.dy + r * dim, t, team, dim);
     if (has_dh) {
@@ -91,87 +102,110 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kerne
     if (has_f) rf.load((const BT*)a.f + r * dim, t, team, dim);
     if (gate_elem) rg.load((const BT*)a.gate + r * dim, t, team, dim);
     if (a.gate_kind == EMB_GATE_ROW) grow = to_f32<BT>(((const BT*)a.gate)[r]);
-    if (a.stats) st = a.stats[r];
+    st = a.stats[r];
   };
+  clear();
 
-  const long long r_first = (long long)blockIdx.x * teams + my_team;
-  const long long b_first = (long long)blockIdx.x * teams;
+  const long long b_first = (long long)blockIdx.x * teams, r_first = b_first + my_team;
   const long long rounds = a.rows > b_first ? (a.rows - b_first + stride - 1) / stride : 0;
-  if (r_first < a.rows) load(r_first);
+  if (kHold && r_first < a.rows) load(r_first);
   for (long long i = 0; i < rounds; ++i) {
     const long long r = r_first + i * stride;
     const bool live = r < a.rows;
-    float dt[8], hat[8], f[8], g[8];
+    if (!kHold && live) load(r);
+    float dt[E], dh[E], hat[E], f[E], g[E], w[E];
     const float4 s = st;
     const float gr = grow;
-    float dh[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const bool in = live && part_col<VEC>(k, t, team) < dim;
-      dt[k] = in && has_dy ? rdy.get(k) : 0.0f;
-      dh[k] = in && has_dh ? rdh.get(k) : 0.0f;
-      hat[k] = in && has_dh ? (ry.get(k) - s.z) * s.w : 0.0f;
-      f[k] = in && has_f ? (rf.get(k) - s.x) * s.y : 0.0f;
-      g[k] = in && gate_elem ? rg.get(k) : 0.0f;
+    for (int k = 0; k < E; ++k) {
+      // only a layer norm's mean makes something of the zeros past the row's end
+      const bool in = !LAYER || part_col<VEC>(k, t, team) < dim;
+      dt[k] = rdy.get(k);
+      dh[k] = rdh.get(k);
+      hat[k] = in ? (ry.get(k) - (LAYER ? s.z : 0.0f)) * s.w : 0.0f;
+      f[k] = in ? (rf.get(k) - (LAYER ? s.x : 0.0f)) * s.y : 0.0f;
+      g[k] = rg.get(k);
     }
-    if (r + stride < a.rows) load(r + stride);
+    if (kHold) {
+      if (r + stride < a.rows) load(r + stride);
+      else clear();
+    }
     if (has_dh) {
       float p = 0.0f, q = 0.0f;
+      wq.get(w);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < E; ++k) {
         cols.add(2, k, dh[k] * hat[k]);
         if (LAYER) cols.add(3, k, dh[k]);
-        dh[k] *= wq.get(k);
+        dh[k] *= w[k];
         p += dh[k] * hat[k];
         if (LAYER) q += dh[k];
       }
-      const float2 m = sum(p, q);
+      const float2 m = sums.sum<LAYER>(p, q);
       const float c1 = m.x * a.inv_dim, c2 = LAYER ? m.y * a.inv_dim : 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const bool in = live && part_col<VEC>(k, t, team) < dim;
+      for (int k = 0; k < E; ++k) {
+        const bool in = !LAYER || part_col<VEC>(k, t, team) < dim;
         dt[k] = in ? dt[k] + s.w * (dh[k] - hat[k] * c1 - c2) : 0.0f;
       }
     }
     if (!has_f) {
-      if (live && a.dx) RowPart<ST, VEC>::store((ST*)a.dx + r * dim, dt, t, team, dim);
+      if (live && a.dx) RowPart<ST, VEC, E>::store((ST*)a.dx + r * dim, dt, t, team, dim);
       continue;
     }
     if (live && a.dx) {
-      float dx[8];
+      float dx[E];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) dx[k] = dt[k] * a.res_scale;
-      RowPart<ST, VEC>::store((ST*)a.dx + r * dim, dx, t, team, dim);
+      for (int k = 0; k < E; ++k) dx[k] = dt[k] * a.res_scale;
+      RowPart<ST, VEC, E>::store((ST*)a.dx + r * dim, dx, t, team, dim);
     }
-    const float a_row = a.gate_kind == EMB_GATE_ROW ? activate(gr, a.act) : 1.0f;
-    float p = 0.0f, q = 0.0f, dg_row = 0.0f;
-    float dg[8];
+    if (gate_elem) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float act = gate_elem ? activate(g[k], a.act) : gate_col ? activate(gc.get(k), a.act) : a_row;
-      const float slope = a.act == EMB_ACT_SIGMOID ? act * (1.0f - act) : 1.0f;
-      const float n = LAYER ? f[k] * wp.get(k) + bp.get(k) : f[k] * wp.get(k);
-      dg[k] = dt[k] * n * slope;
-      dg_row += dg[k];
-      if (gate_col) cols.add(4, k, dg[k]);
-      const float dn = dt[k] * act;
+      for (int k = 0; k < E; ++k) g[k] = activate(g[k], a.act);
+    } else if (gate_col) {
+      gc.get(g);
+#pragma unroll
+      for (int k = 0; k < E; ++k) g[k] = activate(g[k], a.act);
+    } else {
+      const float v = a.gate_kind == EMB_GATE_ROW ? activate(gr, a.act) : 1.0f;
+#pragma unroll
+      for (int k = 0; k < E; ++k) g[k] = v;
+    }
+    float p = 0.0f, q = 0.0f;
+    wp.get(w);
+    if (a.gate_kind != EMB_GATE_NONE) {
+      float n[E], dg_row = 0.0f;
+#pragma unroll
+      for (int k = 0; k < E; ++k) n[k] = 0.0f;
+      if (LAYER) bp.get(n);
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        n[k] = (f[k] * w[k] + n[k]) * dt[k];
+        if (a.act == EMB_ACT_SIGMOID) n[k] *= g[k] * (1.0f - g[k]);
+        dg_row += n[k];
+        if (gate_col) cols.add(4, k, n[k]);
+      }
+      if (live && gate_elem && a.dgate) RowPart<BT, VEC, E>::store((BT*)a.dgate + r * dim, n, t, team, dim);
+      if (a.gate_kind == EMB_GATE_ROW) {
+        const float v = sums.sum<false>(dg_row, 0.0f).x;
+        if (live && t == 0 && a.dgate) ((BT*)a.dgate)[r] = from_f32<BT>(v);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const float dn = dt[k] * g[k];
       cols.add(0, k, dn * f[k]);
       if (LAYER) cols.add(1, k, dn);
-      dt[k] = dn * wp.get(k);
+      dt[k] = dn * w[k];
       p += dt[k] * f[k];
       if (LAYER) q += dt[k];
     }
-    if (live && gate_elem && a.dgate) RowPart<BT, VEC>::store((BT*)a.dgate + r * dim, dg, t, team, dim);
-    if (a.gate_kind == EMB_GATE_ROW) {
-      const float v = sum(dg_row, 0.0f).x;
-      if (live && t == 0 && a.dgate) ((BT*)a.dgate)[r] = from_f32<BT>(v);
-    }
     if (a.df) {
-      const float2 m = sum(p, q);
+      const float2 m = sums.sum<LAYER>(p, q);
       const float c1 = m.x * a.inv_dim, c2 = LAYER ? m.y * a.inv_dim : 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) dt[k] = s.y * (dt[k] - f[k] * c1 - c2);
-      if (live) RowPart<BT, VEC>::store((BT*)a.df + r * dim, dt, t, team, dim);
+      for (int k = 0; k < E; ++k) dt[k] = s.y * (dt[k] - f[k] * c1 - c2);
+      if (live) RowPart<BT, VEC, E>::store((BT*)a.df + r * dim, dt, t, team, dim);
     }
   }
 
@@ -182,18 +216,18 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kerne
     float* out = a.partial + ((long long)blockIdx.x * kSums + c) * dim;
     if (teams == 1) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < E; ++k) {
         const int col = part_col<VEC>(k, t, team);
         if (col < dim) out[col] = cols.get(c, k);
       }
     } else if constexpr (kHold) {
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < 8; ++k) dyn[my_team * team * 8 + part_col<VEC>(k, t, team)] = cols.get(c, k);
+      for (int k = 0; k < E; ++k) dyn[my_team * team * E + part_col<VEC>(k, t, team)] = cols.get(c, k);
       __syncthreads();
       for (int col = threadIdx.x; col < dim; col += blockDim.x) {
         float v = 0.0f;
-        for (int j = 0; j < teams; ++j) v += dyn[j * team * 8 + col];
+        for (int j = 0; j < teams; ++j) v += dyn[j * team * E + col];
         out[col] = v;
       }
     }
@@ -229,8 +263,9 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ 
   }
 }
 
+// Most blocks of a launch, whichever way its rows are read.
 long long bwd_blocks(long long rows, int dim) {
-  const int team = norm_team(dim);
+  const int team = norm_team(dim, false);  // never smaller than the vector form's
   const int teams = std::max(kNormBlock, team) / team;
   return std::min((rows + teams - 1) / teams, (long long)kMaxBlocksPerSm * sm_count());
 }
@@ -239,7 +274,7 @@ template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
 cudaError_t launch_as(const BwdArgs& a, cudaStream_t st, int* blocks_out) {
   const int threads = std::max(kNormBlock, a.team);
   const int teams = threads / a.team;
-  const size_t smem = MAXT == 1024 ? sizeof(float) * kSums * 8 * 1024 : teams > 1 ? sizeof(float) * 8 * threads : 0;
+  const size_t smem = sizeof(float) * threads * norm_elems<VEC, MAXT>() * (MAXT == 1024 ? kSums : teams > 1 ? 1 : 0);
   auto* k = norm_gate_bwd_kernel<ST, BT, VEC, LAYER, MAXT>;
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -323,7 +358,7 @@ extern "C" emb_status emb_norm_gate_bwd(const emb_norm_gate_desc* desc, const vo
                      aligned_to(f_d, 8 * bb) && aligned_to(dx_d, 8 * sb) && aligned_to(df_d, 8 * bb) &&
                      (!ge || (aligned_to(gate_d, 8 * bb) && aligned_to(dgate_d, 8 * bb)));
     const BwdArgs a{dy_d, dh_d, y_d, f_d, gate_d, (const float4*)stats_d, w_post_d, b_post_d, w_pre_d, dx_d, df_d,
-                    dgate_d, (float*)workspace_d, d.rows, d.dim, norm_team(d.dim), d.gate, d.act, want, d.res_scale,
+                    dgate_d, (float*)workspace_d, d.rows, d.dim, norm_team(d.dim, vec), d.gate, d.act, want, d.res_scale,
                     1.0f / (float)d.dim};
     const bool layer = d.norm == EMB_NORM_LAYER;
 #define EMB_NORM_BWD(S, B) e = vec ? launch<S, B, true>(a, layer, st, &j.blocks) : launch<S, B, false>(a, layer, st, &j.blocks)

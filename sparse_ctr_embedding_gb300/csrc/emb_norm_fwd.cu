@@ -31,24 +31,27 @@ struct FwdArgs {
 template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kernel(const __grid_constant__ FwdArgs a) {
   __shared__ float2 slots[4][64];  // teams that need them: 64 threads or more, so at most 4 a block
+  constexpr bool kHold = MAXT < 1024;  // registers enough to keep vectors or sums, and to load a row ahead
+  constexpr int E = norm_elems<VEC, MAXT>();
   const int team = a.team, dim = a.dim;
   const int my_team = threadIdx.x / team;
-  TeamSum sum{team, (int)threadIdx.x % team, team >> 5, 1 + (my_team & 3), slots[my_team & 3]};
-  const int t = sum.t;
+  TeamSum sums{team, (int)threadIdx.x % team, team >> 5, 1 + (my_team & 3), slots[my_team & 3]};
+  const int t = sums.t;
   const int teams = blockDim.x / team;
   const long long stride = (long long)gridDim.x * teams;
   const bool has_f = a.f != nullptr, has_h = a.h != nullptr;
   const bool gate_elem = a.gate_kind == EMB_GATE_ELEM;
-
-  constexpr bool kHold = MAXT < 1024;
   const float* const gate_col = a.gate_kind == EMB_GATE_COL ? (const float*)a.gate : nullptr;
-  VecPart<VEC, kHold> wp(a.w_post, 1.0f, t, team, dim), wq(a.w_pre, 1.0f, t, team, dim);
-  VecPart<VEC, kHold> bp(LAYER ? a.b_post : nullptr, 0.0f, t, team, dim), bq(LAYER ? a.b_pre : nullptr, 0.0f, t, team, dim);
-  VecPart<VEC, kHold> gc(gate_col, 0.0f, t, team, dim);
+  VecPart<VEC, kHold, E> wp(a.w_post, 1.0f, t, team, dim), wq(a.w_pre, 1.0f, t, team, dim);
+  VecPart<VEC, kHold, E> bp(LAYER ? a.b_post : nullptr, 0.0f, t, team, dim), bq(LAYER ? a.b_pre : nullptr, 0.0f, t, team, dim);
+  VecPart<VEC, kHold, E> gc(gate_col, 0.0f, t, team, dim);
 
-  RowPart<ST, VEC> rx;
-  RowPart<BT, VEC> rf, rg;
+  RowPart<ST, VEC, E> rx;
+  RowPart<BT, VEC, E> rf, rg;
   float grow = 0.0f;
+  rx.clear();
+  rf.clear();
+  rg.clear();
   auto load = [&](long long r) {
     rx.load((const ST*)a.x + r * dim, t, team, dim);
     if (has_f) rf.load((const BT*)a.f + r * dim, t, team, dim);
@@ -60,56 +63,71 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kerne
     float s = 0.0f, mean = 0.0f;
     if (LAYER) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s += v[k];
-      mean = sum(s, 0.0f).x * a.inv_dim;
+      for (int k = 0; k < E; ++k) s += v[k];
+      mean = sums.sum<false>(s, 0.0f).x * a.inv_dim;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = part_col<VEC>(k, t, team) < dim ? v[k] - mean : 0.0f;
+      for (int k = 0; k < E; ++k) v[k] = part_col<VEC>(k, t, team) < dim ? v[k] - mean : 0.0f;
     }
     s = 0.0f;  // of v^2 / dim: the sum itself could overflow where the mean does not
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += (v[k] * a.inv_dim) * v[k];
-    const float r = 1.0f / sqrtf(sum(s, 0.0f).x + a.eps);
+    for (int k = 0; k < E; ++k) s += (v[k] * a.inv_dim) * v[k];
+    const float r = 1.0f / sqrtf(sums.sum<false>(s, 0.0f).x + a.eps);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= r;
+    for (int k = 0; k < E; ++k) v[k] *= r;
     return make_float2(mean, r);
   };
 
-  // teams of one warp take rows next to one another, so the loop is uniform over a warp
-  const long long r_first = (long long)blockIdx.x * teams + my_team;
-  const long long rounds = a.rows > (long long)blockIdx.x * teams ? (a.rows - (long long)blockIdx.x * teams + stride - 1) / stride : 0;
-  if (r_first < a.rows) load(r_first);
+  // all teams of a block go through as many rounds, so that a warp's teams stay together
+  const long long b_first = (long long)blockIdx.x * teams, r_first = b_first + my_team;
+  const long long rounds = a.rows > b_first ? (a.rows - b_first + stride - 1) / stride : 0;
+  if (kHold && r_first < a.rows) load(r_first);
   for (long long i = 0; i < rounds; ++i) {
     const long long r = r_first + i * stride;
     const bool live = r < a.rows;
-    float x[8], f[8], g[8];
+    if (!kHold && live) load(r);
+    float x[E], f[E], g[E], w[E], b[E];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const bool in = live && part_col<VEC>(k, t, team) < dim;
-      x[k] = in ? rx.get(k) : 0.0f;
-      f[k] = in && has_f ? rf.get(k) : 0.0f;
-      g[k] = gate_elem ? (in ? activate(rg.get(k), a.act) : 0.0f)
-             : a.gate_kind == EMB_GATE_ROW ? activate(grow, a.act)
-             : gate_col ? activate(gc.get(k), a.act) : 1.0f;
+    for (int k = 0; k < E; ++k) {
+      x[k] = rx.get(k);
+      f[k] = rf.get(k);
+      g[k] = rg.get(k);
     }
-    if (r + stride < a.rows) load(r + stride);
+    const float gr = grow;
+    if (kHold && r + stride < a.rows) load(r + stride);
     float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (has_f) {
+      if (gate_elem) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) g[k] = activate(g[k], a.act);
+      } else if (gate_col) {
+        gc.get(g);
+#pragma unroll
+        for (int k = 0; k < E; ++k) g[k] = activate(g[k], a.act);
+      } else {
+        const float v = a.gate_kind == EMB_GATE_ROW ? activate(gr, a.act) : 1.0f;
+#pragma unroll
+        for (int k = 0; k < E; ++k) g[k] = v;
+      }
       const float2 s = norm(f);
       st.x = s.x;
       st.y = s.y;
+      wp.get(w);
+      if (LAYER) bp.get(b);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = x[k] * a.res_scale + g[k] * (LAYER ? f[k] * wp.get(k) + bp.get(k) : f[k] * wp.get(k));
-      if (live) RowPart<ST, VEC>::store((ST*)a.y + r * dim, x, t, team, dim);
+      for (int k = 0; k < E; ++k) x[k] = x[k] * a.res_scale + g[k] * (LAYER ? f[k] * w[k] + b[k] : f[k] * w[k]);
+      if (live) RowPart<ST, VEC, E>::store((ST*)a.y + r * dim, x, t, team, dim);
     }
     if (has_h) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = part_col<VEC>(k, t, team) < dim ? to_f32<ST>(from_f32<ST>(x[k])) : 0.0f;
+      for (int k = 0; k < E; ++k) x[k] = to_f32<ST>(from_f32<ST>(x[k]));  // the stored residual
       const float2 s = norm(x);
       st.z = s.x;
       st.w = s.y;
+      wq.get(w);
+      if (LAYER) bq.get(b);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = LAYER ? x[k] * wq.get(k) + bq.get(k) : x[k] * wq.get(k);
-      if (live) RowPart<BT, VEC>::store((BT*)a.h + r * dim, x, t, team, dim);
+      for (int k = 0; k < E; ++k) x[k] = LAYER ? x[k] * w[k] + b[k] : x[k] * w[k];
+      if (live) RowPart<BT, VEC, E>::store((BT*)a.h + r * dim, x, t, team, dim);
     }
     if (a.stats && t == 0 && live) a.stats[r] = st;
   }
@@ -180,7 +198,7 @@ extern "C" emb_status emb_norm_gate_fwd(const emb_norm_gate_desc* desc, const vo
   const bool vec = d.dim % 8 == 0 && aligned_to(x_d, 8 * sb) && aligned_to(y_d, 8 * sb) && aligned_to(f_d, 8 * bb) &&
                    aligned_to(h_d, 8 * bb) && (d.gate != EMB_GATE_ELEM || aligned_to(gate_d, 8 * bb));
   const FwdArgs a{x_d, f_d, gate_d, w_post_d, b_post_d, w_pre_d, b_pre_d, y_d, h_d, (float4*)stats_d, d.rows, d.dim,
-                  norm_team(d.dim), d.gate, d.act, d.eps, d.res_scale, 1.0f / (float)d.dim};
+                  norm_team(d.dim, vec), d.gate, d.act, d.eps, d.res_scale, 1.0f / (float)d.dim};
   const bool layer = d.norm == EMB_NORM_LAYER;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
