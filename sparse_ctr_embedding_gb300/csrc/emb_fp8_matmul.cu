@@ -508,34 +508,32 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
 }
 
 // Adds the pieces of each tile that several blocks computed, in k order.  One
-// block takes 16 rows of a tile.
+// block takes 1024 neighbouring elements (whole rows) of a tile, four a thread.
 template <int BN, typename OT>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ MatmulArgs p) {
-  const long long tile = blockIdx.x / (kBM / 16);
-  const int r0 = (int)(blockIdx.x % (kBM / 16)) * 16;
+  constexpr int kRows = 1024 / BN;
+  const long long tile = blockIdx.x / (kBM / kRows);
+  const int r = (int)(blockIdx.x % (kBM / kRows)) * kRows + threadIdx.x / (BN / 4), c = threadIdx.x % (BN / 4) * 4;
   const long long first = tile * p.k_blocks / p.per_cta, last = ((tile + 1) * p.k_blocks - 1) / p.per_cta;
   if (first == last) return;  // one block had it whole
   int tm, tn;
   tile_at(p, tile, &tm, &tn);
-  for (int e = threadIdx.x; e < 16 * BN / 4; e += 256) {
-    const int r = r0 + e / (BN / 4), c = e % (BN / 4) * 4;
-    const int row = tm * kBM + r, col = tn * BN + c;
-    if (row >= p.m || col >= p.n) continue;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float* src = p.partial + ((first + tile) * kBM + r) * BN + c;
-#pragma unroll 4
-    for (long long b = first; b <= last; ++b, src += (long long)kBM * BN) {
-      const float4 w = *reinterpret_cast<const float4*>(src);
-      v.x += w.x;
-      v.y += w.y;
-      v.z += w.z;
-      v.w += w.w;
-    }
-    const float o[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (col + j < p.n) ((OT*)p.out)[row * p.ldo + col + j] = from_f32<OT>(o[j] + (p.bias ? __ldg(p.bias + col + j) : 0.0f));
+  const int row = tm * kBM + r, col = tn * BN + c;
+  if (row >= p.m || col >= p.n) return;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float* src = p.partial + ((first + tile) * kBM + r) * BN + c;
+#pragma unroll 8
+  for (long long b = first; b <= last; ++b, src += (long long)kBM * BN) {
+    const float4 w = *reinterpret_cast<const float4*>(src);
+    v.x += w.x;
+    v.y += w.y;
+    v.z += w.z;
+    v.w += w.w;
   }
+  const float o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (col + j < p.n) ((OT*)p.out)[row * p.ldo + col + j] = from_f32<OT>(o[j] + (p.bias ? __ldg(p.bias + col + j) : 0.0f));
 }
 
 // ------------------------------------------------------------------ row kernel
@@ -714,7 +712,7 @@ cudaError_t launch_tiles(const MatmulArgs& p, const Plan& pl, const CUtensorMap&
   k<<<pl.grid, kThreads, TileCfg<BN>::kBytes, st>>>(ma, mb, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || pl.per_cta == 0) return e;
-  join_kernel<BN, OT><<<pl.m_tiles * pl.n_tiles * (kBM / 16), 256, 0, st>>>(p);
+  join_kernel<BN, OT><<<pl.m_tiles * pl.n_tiles * (kBM * BN / 1024), 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -750,7 +748,7 @@ extern "C" emb_status emb_fp8_matmul_workspace_size(int64_t m, int64_t n, int64_
   if (m < 0 || n < 0 || k < 0) return fail(EMB_ERR_INVALID_ARG, "negative m, n or k");
   if (m > 0x7fff0000LL || n > 0x7fff0000LL || k > 0x7fff0000LL) return fail(EMB_ERR_UNSUPPORTED, "m, n or k above 2^31 - 65536");
   const Plan pl = make_plan(m, n, k);
-  if (pl.bn && (long long)pl.m_tiles * pl.n_tiles > 0x7fffffffLL / (kBM / 16))
+  if (pl.bn && (long long)pl.m_tiles * pl.n_tiles > 0x7fffffffLL / 32)
     return fail(EMB_ERR_UNSUPPORTED, "m * n too large");
   *bytes = pl.ws_bytes;
   return EMB_OK;

@@ -21,7 +21,8 @@ namespace emb {
 namespace {
 
 constexpr int kSums = 5;  // dw_post, db_post, dw_pre, db_pre, per-channel dgate
-constexpr int kMaxBlocksPerSm = 4;
+// Most blocks an SM is given: as many as the workspace has partials for.
+constexpr int max_blocks_per_sm(int threads) { return 1024 / threads; }
 
 struct BwdArgs {
   const void *dy, *dh, *y, *f, *gate;
@@ -62,7 +63,11 @@ struct ColSums {
 
 template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kernel(const __grid_constant__ BwdArgs a) {
-  constexpr bool kHold = MAXT < 1024;  // registers enough to keep vectors or sums, and to load a row ahead
+  // A row is loaded while the one before it is reduced (131,072 x 1024 bf16: 519
+  // us, 628 without), where registers allow: a layer norm's vector form would
+  // spill (32,768 x 2048: 339 us without, 405 with).
+  constexpr bool kPre = MAXT < 1024 && !(VEC && LAYER);
+  constexpr bool kHold = MAXT < 1024;  // registers enough to keep the sums over the rows
   constexpr int E = norm_elems<VEC, MAXT>();
   extern __shared__ float dyn[];
   __shared__ float2 slots[4][64];
@@ -108,11 +113,14 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kerne
 
   const long long b_first = (long long)blockIdx.x * teams, r_first = b_first + my_team;
   const long long rounds = a.rows > b_first ? (a.rows - b_first + stride - 1) / stride : 0;
-  if (kHold && r_first < a.rows) load(r_first);
+  if (kPre && r_first < a.rows) load(r_first);
   for (long long i = 0; i < rounds; ++i) {
     const long long r = r_first + i * stride;
     const bool live = r < a.rows;
-    if (!kHold && live) load(r);
+    if (!kPre) {
+      if (live) load(r);
+      else clear();
+    }
     float dt[E], dh[E], hat[E], f[E], g[E], w[E];
     const float4 s = st;
     const float gr = grow;
@@ -126,7 +134,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kerne
       f[k] = in ? (rf.get(k) - (LAYER ? s.x : 0.0f)) * s.y : 0.0f;
       g[k] = rg.get(k);
     }
-    if (kHold) {
+    if (kPre) {
       if (r + stride < a.rows) load(r + stride);
       else clear();
     }
@@ -240,10 +248,11 @@ struct JoinArgs {
   int dim, blocks;
 };
 
-// Sums the blocks' partials: 32 columns a block, eight threads a column, each
-// adding every eighth partial, then the eight in order.
-__global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ JoinArgs a) {
-  __shared__ float part[8][33];
+// Sums the blocks' partials: 32 columns a block, 32 threads a column, each
+// adding every 32nd partial, then the 32 in order.
+constexpr int kJoin = 32;
+__global__ void __launch_bounds__(32 * kJoin) norm_join_kernel(const __grid_constant__ JoinArgs a) {
+  __shared__ float part[kJoin][33];
   float* out = a.out[blockIdx.y];
   if (!out) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -252,22 +261,26 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ 
   if (col < a.dim) {
     const float* p = a.partial + (long long)blockIdx.y * a.dim + col;
     const long long step = (long long)kSums * a.dim;
-#pragma unroll 4
-    for (int b = w; b < a.blocks; b += 8) v += p[b * step];
+#pragma unroll 8
+    for (int b = w; b < a.blocks; b += kJoin) v += p[b * step];
   }
   part[w][lane] = v;
   __syncthreads();
   if (w == 0 && col < a.dim) {
-    for (int j = 1; j < 8; ++j) v += part[j][lane];
+#pragma unroll
+    for (int j = 1; j < kJoin; ++j) v += part[j][lane];
     out[col] = v;
   }
 }
 
 // Most blocks of a launch, whichever way its rows are read.
 long long bwd_blocks(long long rows, int dim) {
-  const int team = norm_team(dim, false);  // never smaller than the vector form's
-  const int teams = std::max(kNormBlock, team) / team;
-  return std::min((rows + teams - 1) / teams, (long long)kMaxBlocksPerSm * sm_count());
+  long long most = 0;
+  for (const bool vec : {false, true}) {
+    const int team = norm_team(dim, vec), threads = std::max(kNormBlock, team), teams = threads / team;
+    most = std::max(most, std::min((rows + teams - 1) / teams, (long long)max_blocks_per_sm(threads) * sm_count()));
+  }
+  return most;
 }
 
 template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
@@ -282,7 +295,7 @@ cudaError_t launch_as(const BwdArgs& a, cudaStream_t st, int* blocks_out) {
   int per_sm = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, smem);
   if (e != cudaSuccess) return e;
-  per_sm = std::min(std::max(1, per_sm), kMaxBlocksPerSm);
+  per_sm = std::min(std::max(1, per_sm), max_blocks_per_sm(threads));
   const long long blocks = std::min((a.rows + teams - 1) / teams, (long long)per_sm * sm_count());
   k<<<(int)blocks, threads, smem, st>>>(a);
   *blocks_out = (int)blocks;
@@ -371,7 +384,7 @@ extern "C" emb_status emb_norm_gate_bwd(const emb_norm_gate_desc* desc, const vo
     if (e != cudaSuccess) return cuda_fail(e, "norm_gate_bwd_kernel launch");
   }
   if (want) {
-    norm_join_kernel<<<dim3((d.dim + 31) / 32, kSums), 256, 0, st>>>(j);
+    norm_join_kernel<<<dim3((d.dim + 31) / 32, kSums), 32 * kJoin, 0, st>>>(j);
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "norm_join_kernel launch");
   }

