@@ -578,8 +578,12 @@ class Pipeline:
 
 # ------------------------------------------------------------------ the dense tower's operators
 #
-# These run as often as a layer does, some for microseconds: the checks here
-# are few and flat, and the current stream is read as its raw handle.
+# These run as often as a layer does, some for microseconds: one condition per
+# tensor finds the usual case, and only a call that fails it is looked at again
+# for its message.  The current stream is read as its raw handle.
+
+_F8, _F32, _U8 = torch.float8_e4m3fn, torch.float32, torch.uint8
+_new = torch.empty
 
 
 def _raw_stream(stream) -> int:
@@ -591,21 +595,21 @@ def _raw_stream(stream) -> int:
 def _empty(stream, like: torch.Tensor, shape, dtype) -> torch.Tensor:
     """A tensor for use on `stream`: torch's allocator then reuses its memory in that stream's order."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _new(shape, dtype=dtype, device=like.device)
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _new(shape, dtype=dtype, device=like.device)
 
 
 def _dense(t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
     """The address of a contiguous CUDA tensor of this type."""
     if t is None:
         return None
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous CUDA tensor")
 
 
 def _ftype(dtype, name: str) -> int:
@@ -628,8 +632,8 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
 
 
 def _code_stride(t: torch.Tensor, name: str) -> int:
-    if t.dtype is not torch.float8_e4m3fn:
-        raise TypeError(f"{name} must be {torch.float8_e4m3fn}, got {t.dtype}")
+    if t.dtype is not _F8:
+        raise TypeError(f"{name} must be {_F8}, got {t.dtype}")
     ld = _row_stride(t, name)
     return -(-ld // 16) * 16 if ld % 16 and (t.shape[0] <= 1 or t.shape[1] == 0) else ld
 
@@ -643,19 +647,17 @@ def emb_fp8_quantize(x: torch.Tensor, block_rows: int = 1, transpose: bool = Fal
     if block_rows not in (1, EMB_FP8_BLOCK):
         raise ValueError("block_rows must be 1 or 128")
     r, c = x.shape
-    f8 = torch.float8_e4m3fn
-    ldq, ldqt = (c + 15) & ~15, (r + 15) & ~15
-    q = _empty(stream, x, (r, ldq), f8)
-    s = _empty(stream, x, ((c + 127) >> 7, r if block_rows == 1 else (r + 127) >> 7), torch.float32)
-    qt = st = None
-    if transpose:
-        qt = _empty(stream, x, (c, ldqt), f8)
-        st = _empty(stream, x, ((r + 127) >> 7, c if block_rows == 1 else (c + 127) >> 7), torch.float32)
+    rb, cb, ldq, ldqt = (r + 127) >> 7, (c + 127) >> 7, (c + 15) & ~15, (r + 15) & ~15
+    rows, cols = (r, c) if block_rows == 1 else (rb, cb)
+    q, s = _empty(stream, x, (r, ldq), _F8), _empty(stream, x, (cb, rows), _F32)
+    if not transpose:
+        _check(lib().emb_fp8_quantize(x.data_ptr(), _ftype(x.dtype, "x"), r, c, ldx, block_rows, q.data_ptr(), ldq, s.data_ptr(),
+                                      None, 0, None, _raw_stream(stream)))
+        return (q if ldq == c else q[:, :c]), s
+    qt, st = _empty(stream, x, (c, ldqt), _F8), _empty(stream, x, (rb, cols), _F32)
     _check(lib().emb_fp8_quantize(x.data_ptr(), _ftype(x.dtype, "x"), r, c, ldx, block_rows, q.data_ptr(), ldq, s.data_ptr(),
-                                  qt.data_ptr() if transpose else None, ldqt, st.data_ptr() if transpose else None,
-                                  _raw_stream(stream)))
-    q = q if ldq == c else q[:, :c]
-    return (q, s, qt if ldqt == r else qt[:, :r], st) if transpose else (q, s)
+                                  qt.data_ptr(), ldqt, st.data_ptr(), _raw_stream(stream)))
+    return (q if ldq == c else q[:, :c]), s, (qt if ldqt == r else qt[:, :r]), st
 
 
 def emb_fp8_matmul_workspace_size(m: int, n: int, k: int) -> int:
@@ -666,11 +668,10 @@ def emb_fp8_matmul_workspace_size(m: int, n: int, k: int) -> int:
 
 def _block_rows(s: torch.Tensor, rows: int, k_blocks: int, name: str) -> int:
     shape = s.shape
-    if len(shape) == 2 and shape[0] == k_blocks:
-        if shape[1] == rows:
-            return 1
-        if shape[1] == (rows + 127) >> 7:
-            return EMB_FP8_BLOCK
+    if shape == (k_blocks, rows):
+        return 1
+    if shape == (k_blocks, (rows + 127) >> 7):
+        return EMB_FP8_BLOCK
     raise ValueError(f"{name} must be [ceil(k/128), rows] or [ceil(k/128), ceil(rows/128)], got {tuple(shape)}")
 
 
@@ -692,17 +693,16 @@ def emb_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
     if out is None:
         out, ldo = _empty(stream, a, (m, n), out_dtype), n
     else:
-        if tuple(out.shape) != (m, n):
+        if out.shape != (m, n):
             raise ValueError(f"out must be [{m}, {n}]")
         ldo = _row_stride(out, "out")
     if workspace is None:
-        workspace = _empty(stream, a, emb_fp8_matmul_workspace_size(m, n, k), torch.uint8)
+        workspace = _empty(stream, a, emb_fp8_matmul_workspace_size(m, n, k), _U8)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    f32 = torch.float32
-    _check(lib().emb_fp8_matmul(a.data_ptr(), lda, _dense(sa, f32, "sa"), a_rows, b.data_ptr(), ldb, _dense(sb, f32, "sb"),
-                                b_rows, m, n, k, _dense(bias, f32, "bias"), out.data_ptr(), _ftype(out.dtype, "out"), ldo,
-                                workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream)))
+    _check(lib().emb_fp8_matmul(a.data_ptr(), lda, _dense(sa, _F32, "sa"), a_rows, b.data_ptr(), ldb, _dense(sb, _F32, "sb"),
+                                b_rows, m, n, k, None if bias is None else _dense(bias, _F32, "bias"), out.data_ptr(),
+                                _ftype(out.dtype, "out"), ldo, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream)))
     return out
 
 
@@ -718,7 +718,7 @@ def _norm_gate(x: torch.Tensor, block_dtype: torch.dtype, gate, norm: str, act: 
         kind = 1 if gs == shape else 2 if gs == (r, 1) else 3 if gs == (d,) else 0
         if kind == 0:
             raise ValueError(f"gate must be [{r}, {d}], [{r}, 1] or [{d}], got {tuple(gs)}")
-        if gate.dtype is not (torch.float32 if kind == 3 else block_dtype):
+        if gate.dtype is not (_F32 if kind == 3 else block_dtype):
             raise TypeError("a gate per element or row has f's type, a gate per channel is float32")
     return _NormGate(r, d, _ftype(x.dtype, "x"), _ftype(block_dtype, "f"), _NORM[norm], kind, _ACT[act], eps, res_scale)
 
@@ -728,7 +728,7 @@ def _vector(t: Optional[torch.Tensor], dim: int, name: str):
         return None
     if t.numel() != dim:
         raise ValueError(f"{name} must have {dim} elements")
-    return _dense(t, torch.float32, name)
+    return _dense(t, _F32, name)
 
 
 def _same(t: Optional[torch.Tensor], shape, dtype, name: str):
@@ -754,13 +754,21 @@ def emb_norm_gate_fwd(x: torch.Tensor, f: Optional[torch.Tensor], gate: Optional
     d = _norm_gate(x, block_dtype, gate, norm, act, eps, res_scale)
     dim = d.dim
     xp, fp, gp = _dense(x, st_type, "x"), _same(f, shape, block_dtype, "f"), None if gate is None else _dense(gate, gate.dtype, "gate")
-    wp, bp = _vector(w_post, dim, "w_post"), _vector(b_post, dim, "b_post")
-    wq, bq = _vector(w_pre, dim, "w_pre"), _vector(b_pre, dim, "b_pre")
-    y = None if f is None else _empty(stream, x, shape, st_type)
-    h = _empty(stream, x, shape, block_dtype) if pre else None
-    st = _empty(stream, x, (shape[0], 4), torch.float32) if stats else None
-    _check(lib().emb_norm_gate_fwd(ctypes.byref(d), xp, fp, gp, wp, bp, wq, bq, None if y is None else y.data_ptr(),
-                                   h.data_ptr() if pre else None, st.data_ptr() if stats else None, _raw_stream(stream)))
+    wp = None if w_post is None else _vector(w_post, dim, "w_post")
+    bp = None if b_post is None else _vector(b_post, dim, "b_post")
+    wq = None if w_pre is None else _vector(w_pre, dim, "w_pre")
+    bq = None if b_pre is None else _vector(b_pre, dim, "b_pre")
+    y = h = st = yp = hp = sp = None
+    if f is not None:
+        y = _empty(stream, x, shape, st_type)
+        yp = y.data_ptr()
+    if pre:
+        h = _empty(stream, x, shape, block_dtype)
+        hp = h.data_ptr()
+    if stats:
+        st = _empty(stream, x, (shape[0], 4), _F32)
+        sp = st.data_ptr()
+    _check(lib().emb_norm_gate_fwd(ctypes.byref(d), xp, fp, gp, wp, bp, wq, bq, yp, hp, sp, _raw_stream(stream)))
     return y, h, st
 
 
@@ -787,7 +795,7 @@ def emb_norm_gate_bwd(dy: Optional[torch.Tensor], dh: Optional[torch.Tensor], y:
     bt = f.dtype if f is not None else dh.dtype
     d = _norm_gate(y, bt, gate, norm, act, eps, res_scale)
     r, dim = shape
-    f32 = torch.float32
+    f32 = _F32
     ins = (_same(dy, shape, st_type, "dy"), _same(dh, shape, bt, "dh"), _dense(y, st_type, "y"), _same(f, shape, bt, "f"),
            None if gate is None else _dense(gate, gate.dtype, "gate"), _same(stats, (r, 4), f32, "stats"),
            _vector(w_post, dim, "w_post"), _vector(b_post, dim, "b_post"), _vector(w_pre, dim, "w_pre"))
@@ -801,7 +809,7 @@ def emb_norm_gate_bwd(dy: Optional[torch.Tensor], dh: Optional[torch.Tensor], y:
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     _check(lib().emb_norm_gate_bwd(ctypes.byref(d), *ins, *[None if v is None else v.data_ptr() for v in out.values()],
-                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream)))
+                                   workspace.data_ptr(), workspace.nbytes, _raw_stream(stream)))
     return out
 
 

@@ -44,24 +44,41 @@ struct StepArgs {
   const float* grad_scale;
 };
 
-__device__ __forceinline__ void load8(const void* base, int type, long long i, float* o) {
-  if (type == EMB_T_F32) {
-    Raw8<float> r;
-    r.load((const float*)base + i);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = r.get(k);
-  } else if (type == EMB_T_BF16) {
-    Raw8<__nv_bfloat16> r;
-    r.load((const __nv_bfloat16*)base + i);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = r.get(k);
-  } else {
-    Raw8<__half> r;
-    r.load((const __half*)base + i);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = r.get(k);
+// Eight elements of a float type as they lie in memory (f32 in all of w, the
+// others in its first half), loaded in one step and read in another.
+struct Raw {
+  unsigned w[8];
+  __device__ __forceinline__ void load(const void* base, int type, long long i) {
+    if (type == EMB_T_F32)
+      asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                   : "l"((const float*)base + i));
+    else
+      asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "l"((const unsigned short*)base + i));
   }
-}
+  __device__ __forceinline__ void get(int type, float* o) const {
+    if (type == EMB_T_F32) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = __uint_as_float(w[k]);
+    } else if (type == EMB_T_BF16) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[2 * k] = __uint_as_float(w[k] << 16);
+        o[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        o[2 * k] = v.x;
+        o[2 * k + 1] = v.y;
+      }
+    }
+  }
+};
+
 __device__ __forceinline__ void store8(void* base, int type, long long i, const float* o) {
   if (type == EMB_T_F32) {
     Raw8<float> r;
@@ -121,7 +138,7 @@ __device__ __forceinline__ unsigned warp_max(float a) {  // a >= 0 or NaN: the b
   return __reduce_max_sync(0xffffffffu, __float_as_uint(a));
 }
 template <bool kQ8, int N>
-__global__ void __launch_bounds__(256, 4) adamw_kernel(const __grid_constant__ StepArgs<N> a) {
+__global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ StepArgs<N> a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
   const unsigned end = min(a.n_units, (blockIdx.x + 1) * a.span);
@@ -132,8 +149,43 @@ __global__ void __launch_bounds__(256, 4) adamw_kernel(const __grid_constant__ S
     const int mid = (lo + hi + 1) >> 1;
     if (a.t[mid].unit0 <= unit) lo = mid; else hi = mid - 1;
   }
+  // What a unit reads; with 8-bit states the next unit's loads are under way
+  // while one is computed (see kAhead).
+  struct Loaded {
+    Raw p, g, m, v;  // m, v: float32 states
+    uint2 cm, cv;    // 8-bit ones
+    float ms, vs;
+  } in;
+  auto fetch = [&](unsigned u, int at) {
+    const TensorArg& t = a.t[at];
+    const unsigned blk = u - t.unit0;
+    const long long i0 = (long long)blk * EMB_ADAM_BLOCK + lane * 8;
+    if (kQ8) {
+      in.ms = t.ms[blk];
+      in.vs = t.vs[blk];
+    }
+    if (!t.vec || t.n - i0 < 8) return;
+    in.g.load(t.g, t.gt, i0);
+    in.p.load(t.p, t.pt, i0);
+    if (kQ8) {
+      in.cm = *reinterpret_cast<const uint2*>((const unsigned char*)t.m + i0);
+      in.cv = *reinterpret_cast<const uint2*>((const unsigned char*)t.v + i0);
+    } else {
+      in.m.load(t.m, EMB_T_F32, i0);
+      in.v.load(t.v, EMB_T_F32, i0);
+    }
+  };
+  auto tensor_of = [&](unsigned u, int at) {
+    while (at + 1 < a.n_tensors && a.t[at + 1].unit0 <= u) ++at;
+    return at;
+  };
+  constexpr bool kAhead = kQ8;
+  if (kAhead) fetch(unit, lo);
   for (; unit < end; unit += 8) {
-    while (lo + 1 < a.n_tensors && a.t[lo + 1].unit0 <= unit) ++lo;
+    if (!kAhead) {
+      lo = tensor_of(unit, lo);
+      fetch(unit, lo);
+    }
     const TensorArg& t = a.t[lo];
     const unsigned blk = unit - t.unit0;
     const long long i0 = (long long)blk * EMB_ADAM_BLOCK + lane * 8;
@@ -141,8 +193,8 @@ __global__ void __launch_bounds__(256, 4) adamw_kernel(const __grid_constant__ S
     const bool vec = t.vec && cnt == 8;
     float p[8], g[8], m[8], u[8];
     if (vec) {
-      load8(t.g, t.gt, i0, g);
-      load8(t.p, t.pt, i0, p);
+      in.g.get(t.gt, g);
+      in.p.get(t.pt, p);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -151,33 +203,32 @@ __global__ void __launch_bounds__(256, 4) adamw_kernel(const __grid_constant__ S
       }
     }
     if constexpr (kQ8) {
-      const float ms = t.ms[blk], vs = t.vs[blk];
-      unsigned char cm[8], cv[8];
-      if (vec) {
-        *reinterpret_cast<uint2*>(cm) = *reinterpret_cast<const uint2*>((const unsigned char*)t.m + i0);
-        *reinterpret_cast<uint2*>(cv) = *reinterpret_cast<const uint2*>((const unsigned char*)t.v + i0);
-      } else {
+      unsigned w[4] = {in.cm.x, in.cm.y, in.cv.x, in.cv.y};
+      if (!vec) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          cm[k] = k < cnt ? ((const unsigned char*)t.m)[i0 + k] : 0;
-          cv[k] = k < cnt ? ((const unsigned char*)t.v)[i0 + k] : 0;
-        }
+        for (int j = 0; j < 4; ++j) w[j] = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < cnt) {
+            w[k >> 2] |= (unsigned)((const unsigned char*)t.m)[i0 + k] << (8 * (k & 3));
+            w[2 + (k >> 2)] |= (unsigned)((const unsigned char*)t.v)[i0 + k] << (8 * (k & 3));
+          }
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 x = e4m3x2_to_f32(reinterpret_cast<unsigned short*>(cm)[k]);
-        const float2 y = e4m3x2_to_f32(reinterpret_cast<unsigned short*>(cv)[k]);
-        m[2 * k] = __fmul_rn(x.x, ms);
-        m[2 * k + 1] = __fmul_rn(x.y, ms);
-        u[2 * k] = __fmul_rn(y.x, vs);
-        u[2 * k + 1] = __fmul_rn(y.y, vs);
+        const float2 x = e4m3x2_to_f32((unsigned short)(w[k >> 1] >> (16 * (k & 1))));
+        const float2 y = e4m3x2_to_f32((unsigned short)(w[2 + (k >> 1)] >> (16 * (k & 1))));
+        m[2 * k] = __fmul_rn(x.x, in.ms);
+        m[2 * k + 1] = __fmul_rn(x.y, in.ms);
+        u[2 * k] = __fmul_rn(y.x, in.vs);
+        u[2 * k + 1] = __fmul_rn(y.y, in.vs);
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) u[k] = __fmul_rn(u[k], u[k]);
     } else {
       if (vec) {
-        load8(t.m, EMB_T_F32, i0, m);
-        load8(t.v, EMB_T_F32, i0, u);
+        in.m.get(EMB_T_F32, m);
+        in.v.get(EMB_T_F32, u);
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -185,6 +236,10 @@ __global__ void __launch_bounds__(256, 4) adamw_kernel(const __grid_constant__ S
           u[k] = k < cnt ? ((const float*)t.v)[i0 + k] : 0.0f;
         }
       }
+    }
+    if (kAhead && unit + 8 < end) {
+      lo = tensor_of(unit + 8, lo);
+      fetch(unit + 8, lo);
     }
     float v[8];
 #pragma unroll

@@ -1,7 +1,7 @@
 // 8-bit quantiser: codes and block scales of a matrix and of its transpose.
 //
 // Bound by memory: x in once, one byte an element out per orientation.  A block
-// of 256 threads takes one tile of 128 x 128: warp w holds rows 16w..16w+15, a
+// of 512 threads takes one tile of 128 x 128: warp w holds rows 8w..8w+7, a
 // lane four neighbouring columns of each, so a warp reads and writes whole
 // 128-element row pieces.  The tile stays in registers while the largest
 // magnitudes of its rows (warp reductions), its columns (in shared memory over
@@ -15,6 +15,7 @@ namespace emb {
 namespace {
 
 constexpr int kTile = EMB_FP8_BLOCK;
+constexpr int kWarps = 16, kRows = kTile / kWarps;  // rows of a warp
 
 struct QuantArgs {
   const void* x;
@@ -57,17 +58,17 @@ __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, flo
 }
 
 template <typename T, bool SQUARE>
-__global__ void __launch_bounds__(256, 2) quantize_kernel(const __grid_constant__ QuantArgs a) {
-  __shared__ __align__(16) unsigned char tile_t[kTile * kTile];  // transposed codes, 16-byte chunks swizzled
-  __shared__ float part[8][kTile];
+__global__ void __launch_bounds__(kWarps * 32, 2) quantize_kernel(const __grid_constant__ QuantArgs a) {
+  __shared__ __align__(16) unsigned char tile_t[kTile * kTile];  // transposed codes, swizzled
+  __shared__ __align__(16) float part[kWarps][kTile];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const long long tr = blockIdx.x / a.col_tiles, tc = blockIdx.x % a.col_tiles;
-  const long long r0 = tr * kTile + w * 16, c0 = tc * kTile + lane * 4;
+  const long long r0 = tr * kTile + w * kRows, c0 = tc * kTile + lane * 4;
   const T* x = (const T*)a.x;
-  float v[16][4];
+  float v[kRows][4];
   const bool whole = a.vec && c0 + 4 <= a.cols;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < kRows; ++i) {
     const long long r = r0 + i;
     if (r < a.rows && whole) {
       load4<T>(x + r * a.ldx + c0, v[i]);
@@ -79,11 +80,11 @@ __global__ void __launch_bounds__(256, 2) quantize_kernel(const __grid_constant_
   // The largest magnitude of each row's four.  fmaxf passes NaN over, as it should;
   // a thread that meets an infinity makes its infinities NaN first (e4m3 has none)
   // and takes the maxima again.
-  float top[16];
+  float top[kRows];
   auto maxima = [&] {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       top[i] = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
       m = fmaxf(m, top[i]);
     }
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(256, 2) quantize_kernel(const __grid_constant_
   float m = maxima();
   if (m > kFltMax) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < kRows; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (!finite_f32(v[i][k])) v[i][k] = __uint_as_float(0x7fc00000u);
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(256, 2) quantize_kernel(const __grid_constant_
     if (lane == 0) part[0][w] = m;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) tile_amax = fmaxf(tile_amax, part[0][j]);
+    for (int j = 0; j < kWarps; ++j) tile_amax = fmaxf(tile_amax, part[0][j]);
     tile_amax = fmaxf(tile_amax, kAmaxFloor);
     if (threadIdx.x == 0) {
       if (a.s) a.s[tc * a.srow + tr] = scale_of(tile_amax);
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(256, 2) quantize_kernel(const __grid_constant_
   }
   if (a.q) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       const long long r = r0 + i;
       float amax = tile_amax;
       if (!SQUARE) {
@@ -133,43 +134,50 @@ __global__ void __launch_bounds__(256, 2) quantize_kernel(const __grid_constant_
 #pragma unroll
       for (int k = 0; k < 4; ++k) inv[k] = inv_of(tile_amax);
     } else {
+      float top_c[4] = {};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float m = 0.0f;
+      for (int i = 0; i < kRows; ++i)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(v[i][k]));
-        part[w][lane * 4 + k] = m;
-      }
+        for (int k = 0; k < 4; ++k) top_c[k] = fmaxf(top_c[k], fabsf(v[i][k]));
+      *reinterpret_cast<float4*>(&part[w][lane * 4]) = make_float4(top_c[0], top_c[1], top_c[2], top_c[3]);
       __syncthreads();
+      float4 m4 = make_float4(kAmaxFloor, kAmaxFloor, kAmaxFloor, kAmaxFloor);
+#pragma unroll
+      for (int j = 0; j < kWarps; ++j) {
+        const float4 o = *reinterpret_cast<const float4*>(&part[j][lane * 4]);
+        m4 = make_float4(fmaxf(m4.x, o.x), fmaxf(m4.y, o.y), fmaxf(m4.z, o.z), fmaxf(m4.w, o.w));
+      }
+      const float m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float m = kAmaxFloor;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, part[j][lane * 4 + k]);
-        inv[k] = inv_of(m);
-        if (w == 0 && c0 + k < a.cols) a.st[tr * a.strow + c0 + k] = scale_of(m);
+        inv[k] = inv_of(m[k]);
+        if (w == 0 && c0 + k < a.cols) a.st[tr * a.strow + c0 + k] = scale_of(m[k]);
       }
     }
-    // a lane's column k holds 16 codes of the transposed row 4 lane + k, at chunk w
+    // A lane's column k holds eight codes of the transposed row 4 lane + k, at
+    // eight-byte piece w.  Piece p of row c lies at p ^ (c / 4 mod 16): a warp's
+    // stores meet no bank twice, and two pieces that make up sixteen bytes stay
+    // together, swapped where that number is odd.
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      unsigned c[4];
+      unsigned c[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 2; ++j)
         c[j] = e4m3x2(__fmul_rn(v[4 * j][k], inv[k]), __fmul_rn(v[4 * j + 1][k], inv[k])) |
                (e4m3x2(__fmul_rn(v[4 * j + 2][k], inv[k]), __fmul_rn(v[4 * j + 3][k], inv[k])) << 16);
-      *reinterpret_cast<uint4*>(tile_t + (lane * 4 + k) * kTile + ((w ^ (lane & 7)) << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<uint2*>(tile_t + (lane * 4 + k) * kTile + ((w ^ (lane & 15)) << 3)) = make_uint2(c[0], c[1]);
     }
     __syncthreads();
     const long long row_end = (a.rows + 15) & ~15LL;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int at = j * 256 + threadIdx.x;  // 16-byte chunk of the tile: 8 to a transposed row
-      const int c = at >> 3, chunk = at & 7;
+    for (int j = 0; j < kTile * 8 / (kWarps * 32); ++j) {
+      const int at = j * kWarps * 32 + threadIdx.x;  // 16-byte chunk of the tile: 8 to a transposed row
+      const int c = at >> 3, chunk = at & 7, x = (c >> 2) & 15;
       const long long col = tc * kTile + c, row = tr * kTile + chunk * 16;
-      if (col < a.cols && row < row_end)
-        *reinterpret_cast<uint4*>(a.qt + col * a.ldqt + row) =
-            *reinterpret_cast<const uint4*>(tile_t + c * kTile + ((chunk ^ ((c >> 2) & 7)) << 4));
+      if (col < a.cols && row < row_end) {
+        const uint4 o = *reinterpret_cast<const uint4*>(tile_t + c * kTile + ((chunk ^ (x >> 1)) << 4));
+        *reinterpret_cast<uint4*>(a.qt + col * a.ldqt + row) = x & 1 ? make_uint4(o.z, o.w, o.x, o.y) : o;
+      }
     }
   }
 }
@@ -205,8 +213,8 @@ extern "C" emb_status emb_fp8_quantize(const void* x_d, emb_ftype x_t, int64_t r
   cudaStream_t st = (cudaStream_t)stream;
 #define EMB_QUANT(T)                                                        \
   do {                                                                      \
-    if (square) quantize_kernel<T, true><<<grid, 256, 0, st>>>(a);          \
-    else quantize_kernel<T, false><<<grid, 256, 0, st>>>(a);                \
+    if (square) quantize_kernel<T, true><<<grid, kWarps * 32, 0, st>>>(a);          \
+    else quantize_kernel<T, false><<<grid, kWarps * 32, 0, st>>>(a);                \
   } while (0)
   if (x_t == EMB_T_F32) EMB_QUANT(float);
   else if (x_t == EMB_T_BF16) EMB_QUANT(__nv_bfloat16);
