@@ -57,7 +57,7 @@ struct MatmulArgs {
   int m_tiles, n_tiles, k_blocks;
   long long steps;           // m_tiles * n_tiles * k_blocks
   long long per_cta;         // steps a block takes; 0: whole tiles, block-stride
-  int wide_out;              // rows of out take 32-byte stores
+  int wide_out;              // rows of out are aligned to 32 bytes
 };
 
 // ------------------------------------------------------------------ PTX
@@ -205,7 +205,8 @@ struct TileCfg {
   static constexpr int kHalf = BN * 4 / kScaleWarps;          // columns of a scaling warp
   static constexpr int kSlot = kBM + BN;                      // scales of a step: rows, columns
   static constexpr int kScaleBytes = kAhead * kSlot * 4;
-  static constexpr int kBytes = kStages * kStageBytes + kScaleBytes + 1024;  // + room to align
+  static constexpr int kStoreBytes = kScaleWarps * 32 * 17 * 4;  // 32 rows x 16 columns a warp, for unaligned output
+  static constexpr int kBytes = kStages * kStageBytes + kScaleBytes + kStoreBytes + 1024;  // + room to align
 };
 
 struct Unit {  // consecutive blocks of one tile
@@ -275,7 +276,9 @@ __device__ __forceinline__ void store32(OT* dst, const float* v) {  // 32 bytes
 }
 
 // BCOL: b's scales differ by column (else one per 128 columns: one a warp).
-template <int BN, typename OT, bool BCOL>
+// WIDE: rows of out are aligned to 32 bytes.  (Both ways of storing in one kernel
+// cost the main loop its registers: 131,072 x 1024 x 8192 900 us instead of 790.)
+template <int BN, typename OT, bool BCOL, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap map_a,
                                                            const __grid_constant__ CUtensorMap map_b,
                                                            const __grid_constant__ MatmulArgs p) {
@@ -409,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   } else {  // scaling warps: TMEM lanes 32 (warp % 4).., columns group (warp / 4)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kScaleRegs));
     const int half = warp >> 2, quarter = warp & 3;
+    float* const stage = ring + kAhead * C::kSlot + warp * 32 * 17;
     unsigned it = 0;
     bool go = true;
     while (go && next_unit(p, &pos, end, &u)) {
@@ -473,23 +477,42 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       }
       if (!go) break;
       if (u.kb0 == 0 && u.kb1 == p.k_blocks) {
-        if (row < p.m) {
-          OT* dst = (OT*)p.out + row * p.ldo + col0;
-          constexpr int kVec = 32 / sizeof(OT);
+        if constexpr (WIDE) {
+          if (row < p.m) {
+            OT* dst = (OT*)p.out + row * p.ldo + col0;
+            constexpr int kVec = 32 / sizeof(OT);
 #pragma unroll
-          for (int c = 0; c < C::kHalf; c += kVec) {
-            if (p.bias) {
+            for (int c = 0; c < C::kHalf; c += kVec) {
+              if (p.bias) {
 #pragma unroll
-              for (int j = 0; j < kVec; ++j)
-                if (col0 + c + j < p.n) acc[c + j] += __ldg(p.bias + col0 + c + j);
+                for (int j = 0; j < kVec; ++j)
+                  if (col0 + c + j < p.n) acc[c + j] += __ldg(p.bias + col0 + c + j);
+              }
+              if (col0 + c + kVec <= p.n) {
+                store32<OT>(dst + c, acc + c);
+              } else {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                  if (col0 + c + j < p.n) dst[c + j] = from_f32<OT>(acc[c + j]);
+              }
             }
-            if (p.wide_out && col0 + c + kVec <= p.n) {
-              store32<OT>(dst + c, acc + c);
-            } else {
+          }
+        } else {
+          // through shared memory, so that a half warp stores 16 neighbours of a row
+          // (10,046 x 1293 x 475 to f16: 155 us with a row to a lane, 61 so)
 #pragma unroll
-              for (int j = 0; j < kVec; ++j)
-                if (col0 + c + j < p.n) dst[c + j] = from_f32<OT>(acc[c + j]);
-            }
+          for (int c = 0; c < C::kHalf; c += 16) {
+            if (col0 + c >= p.n) break;  // the same for the warp
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = acc[c + j];
+            __syncwarp();
+            const int col = col0 + c + (lane & 15);
+            const float bias = p.bias && col < p.n ? __ldg(p.bias + col) : 0.0f;
+            OT* dst = (OT*)p.out + (row - lane) * p.ldo + col;
+#pragma unroll 4
+            for (int r = lane >> 4; r < 32; r += 2)
+              if (row - lane + r < p.m && col < p.n) dst[r * p.ldo] = from_f32<OT>(stage[r * 17 + (lane & 15)] + bias);
           }
         }
       } else if (row < p.m) {  // part of a tile: slot (block + tile) is this piece's alone
@@ -658,22 +681,37 @@ Plan make_plan(long long m, long long n, long long k) {
   if (m <= kRowMax) return pl;
   const int sms = sm_count();
   const long long mt = (m + kBM - 1) / kBM;
-  // The widest tile that the work fills: with less than eight steps of it for
-  // each SM, narrower ones keep the pieces and their joining small.
-  pl.bn = 256;
-  while (pl.bn > 64 && (n <= pl.bn / 2 || mt * ((n + pl.bn - 1) / pl.bn) * pl.k_blocks < 8LL * sms)) pl.bn /= 2;
-  pl.m_tiles = (int)mt;
-  pl.n_tiles = (int)((n + pl.bn - 1) / pl.bn);
-  const long long tiles = mt * pl.n_tiles, steps = tiles * pl.k_blocks;
-  // Whole tiles when the last round of them leaves at most a fifth of the SMs idle, or a tile is one block long.
-  const long long rounds = (tiles + sms - 1) / sms;
-  if (pl.k_blocks == 1 || tiles * 5 >= rounds * sms * 4) {
-    pl.grid = (int)std::min<long long>(tiles, sms);
-  } else {
-    pl.per_cta = std::max<long long>((steps + sms - 1) / sms, std::min(2, pl.k_blocks));
-    pl.grid = (int)((steps + pl.per_cta - 1) / pl.per_cta);
-    pl.ws_bytes = (size_t)(pl.grid + tiles) * kBM * pl.bn * sizeof(float);
+  // The tile's width, and whole tiles or even shares of the steps: whichever a
+  // model of the time (us, fitted to 20 shapes from 64 x 1024 x 8192 to 30,584 x
+  // 452 x 692, within a fifth of each) puts first.  A step of 256, 128 or 64
+  // columns takes 0.48, 0.33 or 0.29, a tile's end 3.3, 2 or 2; sharing costs the
+  // second launch and 0.42 a megabyte of partial tiles.  Measured: 9853 x 448 x
+  // 2560 30 whole and 41 shared at 256; 1024 x 1664 x 16,384 64 and 46; 1024 x
+  // 8192 x 131,072 by rows 1250 and 1470.
+  double best = 0.0;
+  const double step_us[3] = {0.48, 0.33, 0.29}, end_us[3] = {3.3, 2.0, 2.0};
+  for (int w = 0; w < 3; ++w) {
+    const int bn = 256 >> w;
+    const long long nt = (n + bn - 1) / bn, tiles = mt * nt, steps = tiles * pl.k_blocks;
+    const long long rounds = (tiles + sms - 1) / sms;
+    const double whole = (double)rounds * (pl.k_blocks * step_us[w] + end_us[w]);
+    const long long per = std::max<long long>((steps + sms - 1) / sms, 2);
+    const long long grid = (steps + per - 1) / per;
+    const double mb = (double)(grid + tiles) * std::min<long long>(m, kBM) * bn * 4e-6;
+    // blocks at different k's share no slabs: from DRAM a step then takes half as long again
+    const double far = (double)(m + n) * k > 64e6 ? 1.5 : 1.0;
+    const double shared = per * step_us[w] * far + end_us[w] + 4.0 + 0.42 * mb;
+    const bool share = pl.k_blocks > 1 && shared < whole;
+    const double us = share ? shared : whole;
+    if (w > 0 && us >= best) continue;
+    best = us;
+    pl.bn = bn;
+    pl.n_tiles = (int)nt;
+    pl.per_cta = share ? per : 0;
+    pl.grid = (int)(share ? grid : std::min<long long>(tiles, sms));
+    pl.ws_bytes = share ? (size_t)(grid + tiles) * kBM * bn * sizeof(float) : 0;
   }
+  pl.m_tiles = (int)mt;
   return pl;
 }
 
@@ -706,7 +744,8 @@ bool make_map(CUtensorMap* map, const void* base, long long rows, long long k, l
 
 template <int BN, typename OT>
 cudaError_t launch_tiles(const MatmulArgs& p, const Plan& pl, const CUtensorMap& ma, const CUtensorMap& mb, cudaStream_t st) {
-  auto* k = p.b_shift ? tile_kernel<BN, OT, false> : tile_kernel<BN, OT, true>;
+  auto* k = p.wide_out ? (p.b_shift ? tile_kernel<BN, OT, false, true> : tile_kernel<BN, OT, true, true>)
+                       : (p.b_shift ? tile_kernel<BN, OT, false, false> : tile_kernel<BN, OT, true, false>);
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg<BN>::kBytes);
   if (e != cudaSuccess) return e;
   k<<<pl.grid, kThreads, TileCfg<BN>::kBytes, st>>>(ma, mb, p);
