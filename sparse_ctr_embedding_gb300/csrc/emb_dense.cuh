@@ -27,7 +27,7 @@ __device__ __forceinline__ float to_f32<__half>(__half v) {
 }
 template <>
 __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
-  return __bfloat162float(v);
+  return __uint_as_float((unsigned)__bfloat16_as_ushort(v) << 16);
 }
 template <typename T>
 __device__ __forceinline__ T from_f32(float v);
@@ -85,7 +85,10 @@ struct Raw8<__half> : Raw8Half<__half, __half2> {
 };
 template <>
 struct Raw8<__nv_bfloat16> : Raw8Half<__nv_bfloat16, __nv_bfloat162> {
-  __device__ __forceinline__ float get(int i) const { return __bfloat162float(i & 1 ? __high2bfloat16(v[i >> 1]) : __low2bfloat16(v[i >> 1])); }
+  __device__ __forceinline__ float get(int i) const {  // a bf16 is the upper half of its float
+    const unsigned u = *reinterpret_cast<const unsigned*>(&v[i >> 1]);
+    return __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
+  }
   __device__ __forceinline__ void set2(int i, float a, float b) { v[i] = __floats2bfloat162_rn(a, b); }
 };
 
