@@ -78,7 +78,8 @@ __device__ __forceinline__ int part_col(int k, int t, int team) {
 
 // This thread's elements of a float32 vector [dim] (NULL: all `absent`), held
 // in registers over the rows, or read again (from L1) for each row.
-template <bool VEC, bool kHold, int E>
+// SURE: it is there, and aligned to 16 bytes.
+template <bool VEC, bool kHold, int E, bool SURE>
 struct VecPart {
   const float* p;
   float absent;
@@ -87,8 +88,8 @@ struct VecPart {
   __device__ __forceinline__ void read(float* o) const {
 #pragma unroll
     for (int k = 0; k < E; ++k) o[k] = absent;
-    if (!p) return;
-    if (VEC && vec) {
+    if (!SURE && !p) return;
+    if (VEC && (SURE || vec)) {
       if (t * 8 < dim) {
         const float4 a = __ldg(reinterpret_cast<const float4*>(p + t * 8)), b = __ldg(reinterpret_cast<const float4*>(p + t * 8 + 4));
         o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;

@@ -61,7 +61,10 @@ struct ColSums {
   }
 };
 
-template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
+// FULL: the usual case (every array there, a sigmoid gate per element), known when
+// compiling: half the instructions of the other cases are their branches and
+// what the branches' ends move between registers.
+template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT, bool FULL>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kernel(const __grid_constant__ BwdArgs a) {
   // A row is loaded while the one before it is reduced (131,072 x 1024 bf16: 519
   // us, 628 without), where registers allow: a layer norm's vector form would
@@ -77,13 +80,15 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kerne
   const int t = sums.t;
   const int teams = blockDim.x / team;
   const long long stride = (long long)gridDim.x * teams;
-  const bool has_f = a.f != nullptr, has_dh = a.dh != nullptr, has_dy = a.dy != nullptr;
-  const bool gate_elem = a.gate_kind == EMB_GATE_ELEM;
-  const float* const gate_col = a.gate_kind == EMB_GATE_COL ? (const float*)a.gate : nullptr;
+  const bool has_f = FULL || a.f != nullptr, has_dh = FULL || a.dh != nullptr, has_dy = FULL || a.dy != nullptr;
+  const int gate_kind = FULL ? (int)EMB_GATE_ELEM : a.gate_kind, act = FULL ? (int)EMB_ACT_SIGMOID : a.act;
+  const bool gate_elem = gate_kind == EMB_GATE_ELEM;
+  const float* const gate_col = gate_kind == EMB_GATE_COL ? (const float*)a.gate : nullptr;
 
   // the vectors are read for each row: registers go to the rows on their way and the sums
-  VecPart<VEC, false, E> wp(a.w_post, 1.0f, t, team, dim), wq(a.w_pre, 1.0f, t, team, dim);
-  VecPart<VEC, false, E> bp(LAYER ? a.b_post : nullptr, 0.0f, t, team, dim), gc(gate_col, 0.0f, t, team, dim);
+  VecPart<VEC, false, E, FULL> wp(a.w_post, 1.0f, t, team, dim), wq(a.w_pre, 1.0f, t, team, dim);
+  VecPart<VEC, false, E, FULL && LAYER> bp(LAYER ? a.b_post : nullptr, 0.0f, t, team, dim);
+  VecPart<VEC, false, E, false> gc(gate_col, 0.0f, t, team, dim);
   ColSums<kHold, E> cols(dyn);
 
   RowPart<ST, VEC, E> rdy, ry;
@@ -106,7 +111,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kerne
     }
     if (has_f) rf.load((const BT*)a.f + r * dim, t, team, dim);
     if (gate_elem) rg.load((const BT*)a.gate + r * dim, t, team, dim);
-    if (a.gate_kind == EMB_GATE_ROW) grow = to_f32<BT>(((const BT*)a.gate)[r]);
+    if (gate_kind == EMB_GATE_ROW) grow = to_f32<BT>(((const BT*)a.gate)[r]);
     st = a.stats[r];
   };
   clear();
@@ -158,10 +163,10 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kerne
       }
     }
     if (!has_f) {
-      if (live && a.dx) RowPart<ST, VEC, E>::store((ST*)a.dx + r * dim, dt, t, team, dim);
+      if (live && (FULL || a.dx)) RowPart<ST, VEC, E>::store((ST*)a.dx + r * dim, dt, t, team, dim);
       continue;
     }
-    if (live && a.dx) {
+    if (live && (FULL || a.dx)) {
       float dx[E];
 #pragma unroll
       for (int k = 0; k < E; ++k) dx[k] = dt[k] * a.res_scale;
@@ -169,19 +174,19 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kerne
     }
     if (gate_elem) {
 #pragma unroll
-      for (int k = 0; k < E; ++k) g[k] = activate(g[k], a.act);
+      for (int k = 0; k < E; ++k) g[k] = activate(g[k], act);
     } else if (gate_col) {
       gc.get(g);
 #pragma unroll
-      for (int k = 0; k < E; ++k) g[k] = activate(g[k], a.act);
+      for (int k = 0; k < E; ++k) g[k] = activate(g[k], act);
     } else {
-      const float v = a.gate_kind == EMB_GATE_ROW ? activate(gr, a.act) : 1.0f;
+      const float v = gate_kind == EMB_GATE_ROW ? activate(gr, act) : 1.0f;
 #pragma unroll
       for (int k = 0; k < E; ++k) g[k] = v;
     }
     float p = 0.0f, q = 0.0f;
     wp.get(w);
-    if (a.gate_kind != EMB_GATE_NONE) {
+    if (gate_kind != EMB_GATE_NONE) {
       float n[E], dg_row = 0.0f;
 #pragma unroll
       for (int k = 0; k < E; ++k) n[k] = 0.0f;
@@ -189,12 +194,12 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kerne
 #pragma unroll
       for (int k = 0; k < E; ++k) {
         n[k] = (f[k] * w[k] + n[k]) * dt[k];
-        if (a.act == EMB_ACT_SIGMOID) n[k] *= g[k] * (1.0f - g[k]);
+        if (act == EMB_ACT_SIGMOID) n[k] *= g[k] * (1.0f - g[k]);
         dg_row += n[k];
         if (gate_col) cols.add(4, k, n[k]);
       }
-      if (live && gate_elem && a.dgate) RowPart<BT, VEC, E>::store((BT*)a.dgate + r * dim, n, t, team, dim);
-      if (a.gate_kind == EMB_GATE_ROW) {
+      if (live && gate_elem && (FULL || a.dgate)) RowPart<BT, VEC, E>::store((BT*)a.dgate + r * dim, n, t, team, dim);
+      if (gate_kind == EMB_GATE_ROW) {
         const float v = sums.sum<false>(dg_row, 0.0f).x;
         if (live && t == 0 && a.dgate) ((BT*)a.dgate)[r] = from_f32<BT>(v);
       }
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kerne
       p += dt[k] * f[k];
       if (LAYER) q += dt[k];
     }
-    if (a.df) {
+    if (FULL || a.df) {
       const float2 m = sums.sum<LAYER>(p, q);
       const float c1 = m.x * a.inv_dim, c2 = LAYER ? m.y * a.inv_dim : 0.0f;
 #pragma unroll
@@ -283,12 +288,12 @@ long long bwd_blocks(long long rows, int dim) {
   return most;
 }
 
-template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
+template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT, bool FULL>
 cudaError_t launch_as(const BwdArgs& a, cudaStream_t st, int* blocks_out) {
   const int threads = std::max(kNormBlock, a.team);
   const int teams = threads / a.team;
   const size_t smem = sizeof(float) * threads * norm_elems<VEC, MAXT>() * (MAXT == 1024 ? kSums : teams > 1 ? 1 : 0);
-  auto* k = norm_gate_bwd_kernel<ST, BT, VEC, LAYER, MAXT>;
+  auto* k = norm_gate_bwd_kernel<ST, BT, VEC, LAYER, MAXT, FULL>;
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -301,13 +306,19 @@ cudaError_t launch_as(const BwdArgs& a, cudaStream_t st, int* blocks_out) {
   *blocks_out = (int)blocks;
   return cudaGetLastError();
 }
+template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
+cudaError_t launch_full(const BwdArgs& a, cudaStream_t st, int* blocks) {
+  const bool full = a.gate_kind == EMB_GATE_ELEM && a.act == EMB_ACT_SIGMOID && a.f && a.dh && a.dy && a.dx && a.df &&
+                    a.dgate && a.w_post && a.w_pre && aligned_to(a.w_post, 16) && aligned_to(a.w_pre, 16) &&
+                    (!LAYER || (a.b_post && aligned_to(a.b_post, 16)));
+  return full ? launch_as<ST, BT, VEC, LAYER, MAXT, true>(a, st, blocks) : launch_as<ST, BT, VEC, LAYER, MAXT, false>(a, st, blocks);
+}
 template <typename ST, typename BT, bool VEC>
 cudaError_t launch(const BwdArgs& a, bool layer, cudaStream_t st, int* blocks) {
   if (a.team <= kNormBlock)
-    return layer ? launch_as<ST, BT, VEC, true, kNormBlock>(a, st, blocks) : launch_as<ST, BT, VEC, false, kNormBlock>(a, st, blocks);
-  if (a.team <= 512)
-    return layer ? launch_as<ST, BT, VEC, true, 512>(a, st, blocks) : launch_as<ST, BT, VEC, false, 512>(a, st, blocks);
-  return layer ? launch_as<ST, BT, VEC, true, 1024>(a, st, blocks) : launch_as<ST, BT, VEC, false, 1024>(a, st, blocks);
+    return layer ? launch_full<ST, BT, VEC, true, kNormBlock>(a, st, blocks) : launch_full<ST, BT, VEC, false, kNormBlock>(a, st, blocks);
+  if (a.team <= 512) return layer ? launch_full<ST, BT, VEC, true, 512>(a, st, blocks) : launch_full<ST, BT, VEC, false, 512>(a, st, blocks);
+  return layer ? launch_full<ST, BT, VEC, true, 1024>(a, st, blocks) : launch_full<ST, BT, VEC, false, 1024>(a, st, blocks);
 }
 
 }  // namespace

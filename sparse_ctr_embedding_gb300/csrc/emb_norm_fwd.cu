@@ -28,7 +28,10 @@ struct FwdArgs {
 // MAXT: most threads of a block.  A thread of a 1024-thread team has 64
 // registers, too few to hold its vectors' elements over the rows: it reads
 // them again from L1 where it needs them.
-template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
+// FULL: the usual case (every array there, a sigmoid gate per element), known when
+// compiling: half the instructions of the other cases are their branches and
+// what the branches' ends move between registers.
+template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT, bool FULL>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kernel(const __grid_constant__ FwdArgs a) {
   __shared__ float2 slots[4][64];  // teams that need them: 64 threads or more, so at most 4 a block
   // A row is loaded while the one before it is reduced (16,384 x 1664, float32
@@ -42,12 +45,13 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kerne
   const int t = sums.t;
   const int teams = blockDim.x / team;
   const long long stride = (long long)gridDim.x * teams;
-  const bool has_f = a.f != nullptr, has_h = a.h != nullptr;
-  const bool gate_elem = a.gate_kind == EMB_GATE_ELEM;
-  const float* const gate_col = a.gate_kind == EMB_GATE_COL ? (const float*)a.gate : nullptr;
-  VecPart<VEC, kHold, E> wp(a.w_post, 1.0f, t, team, dim), wq(a.w_pre, 1.0f, t, team, dim);
-  VecPart<VEC, kHold, E> bp(LAYER ? a.b_post : nullptr, 0.0f, t, team, dim), bq(LAYER ? a.b_pre : nullptr, 0.0f, t, team, dim);
-  VecPart<VEC, kHold, E> gc(gate_col, 0.0f, t, team, dim);
+  const bool has_f = FULL || a.f != nullptr, has_h = FULL || a.h != nullptr;
+  const int gate_kind = FULL ? (int)EMB_GATE_ELEM : a.gate_kind, act = FULL ? (int)EMB_ACT_SIGMOID : a.act;
+  const bool gate_elem = gate_kind == EMB_GATE_ELEM;
+  const float* const gate_col = gate_kind == EMB_GATE_COL ? (const float*)a.gate : nullptr;
+  VecPart<VEC, kHold, E, FULL> wp(a.w_post, 1.0f, t, team, dim), wq(a.w_pre, 1.0f, t, team, dim);
+  VecPart<VEC, kHold, E, FULL && LAYER> bp(LAYER ? a.b_post : nullptr, 0.0f, t, team, dim), bq(LAYER ? a.b_pre : nullptr, 0.0f, t, team, dim);
+  VecPart<VEC, kHold, E, false> gc(gate_col, 0.0f, t, team, dim);
 
   RowPart<ST, VEC, E> rx;
   RowPart<BT, VEC, E> rf, rg;
@@ -59,7 +63,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kerne
     rx.load((const ST*)a.x + r * dim, t, team, dim);
     if (has_f) rf.load((const BT*)a.f + r * dim, t, team, dim);
     if (gate_elem) rg.load((const BT*)a.gate + r * dim, t, team, dim);
-    if (a.gate_kind == EMB_GATE_ROW) grow = to_f32<BT>(((const BT*)a.gate)[r]);
+    if (gate_kind == EMB_GATE_ROW) grow = to_f32<BT>(((const BT*)a.gate)[r]);
   };
   // norm of v in place; returns (mean, 1/sqrt)
   auto norm = [&](float* v) {
@@ -101,13 +105,13 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kerne
     if (has_f) {
       if (gate_elem) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) g[k] = activate(g[k], a.act);
+        for (int k = 0; k < E; ++k) g[k] = activate(g[k], act);
       } else if (gate_col) {
         gc.get(g);
 #pragma unroll
-        for (int k = 0; k < E; ++k) g[k] = activate(g[k], a.act);
+        for (int k = 0; k < E; ++k) g[k] = activate(g[k], act);
       } else {
-        const float v = a.gate_kind == EMB_GATE_ROW ? activate(gr, a.act) : 1.0f;
+        const float v = gate_kind == EMB_GATE_ROW ? activate(gr, act) : 1.0f;
 #pragma unroll
         for (int k = 0; k < E; ++k) g[k] = v;
       }
@@ -132,27 +136,34 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kerne
       for (int k = 0; k < E; ++k) x[k] = LAYER ? x[k] * w[k] + b[k] : x[k] * w[k];
       if (live) RowPart<BT, VEC, E>::store((BT*)a.h + r * dim, x, t, team, dim);
     }
-    if (a.stats && t == 0 && live) a.stats[r] = st;
+    if ((FULL || a.stats) && t == 0 && live) a.stats[r] = st;
   }
 }
 
-template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
+template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT, bool FULL>
 cudaError_t launch_as(const FwdArgs& a, cudaStream_t st) {
   const int threads = std::max(kNormBlock, a.team);
   const int teams = threads / a.team;
   int per_sm = 0;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, norm_gate_fwd_kernel<ST, BT, VEC, LAYER, MAXT>, threads, 0);
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, norm_gate_fwd_kernel<ST, BT, VEC, LAYER, MAXT, FULL>, threads, 0);
   if (e != cudaSuccess) return e;
   const long long blocks = std::min((a.rows + teams - 1) / teams, (long long)std::max(1, per_sm) * sm_count());
-  norm_gate_fwd_kernel<ST, BT, VEC, LAYER, MAXT><<<(int)blocks, threads, 0, st>>>(a);
+  norm_gate_fwd_kernel<ST, BT, VEC, LAYER, MAXT, FULL><<<(int)blocks, threads, 0, st>>>(a);
   return cudaGetLastError();
+}
+template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT>
+cudaError_t launch_full(const FwdArgs& a, cudaStream_t st) {
+  const bool full = a.gate_kind == EMB_GATE_ELEM && a.act == EMB_ACT_SIGMOID && a.f && a.h && a.stats && a.w_post &&
+                    a.w_pre && aligned_to(a.w_post, 16) && aligned_to(a.w_pre, 16) &&
+                    (!LAYER || (a.b_post && a.b_pre && aligned_to(a.b_post, 16) && aligned_to(a.b_pre, 16)));
+  return full ? launch_as<ST, BT, VEC, LAYER, MAXT, true>(a, st) : launch_as<ST, BT, VEC, LAYER, MAXT, false>(a, st);
 }
 template <typename ST, typename BT, bool VEC>
 cudaError_t launch(const FwdArgs& a, bool layer, cudaStream_t st) {
   if (a.team <= kNormBlock)
-    return layer ? launch_as<ST, BT, VEC, true, kNormBlock>(a, st) : launch_as<ST, BT, VEC, false, kNormBlock>(a, st);
-  if (a.team <= 512) return layer ? launch_as<ST, BT, VEC, true, 512>(a, st) : launch_as<ST, BT, VEC, false, 512>(a, st);
-  return layer ? launch_as<ST, BT, VEC, true, 1024>(a, st) : launch_as<ST, BT, VEC, false, 1024>(a, st);
+    return layer ? launch_full<ST, BT, VEC, true, kNormBlock>(a, st) : launch_full<ST, BT, VEC, false, kNormBlock>(a, st);
+  if (a.team <= 512) return layer ? launch_full<ST, BT, VEC, true, 512>(a, st) : launch_full<ST, BT, VEC, false, 512>(a, st);
+  return layer ? launch_full<ST, BT, VEC, true, 1024>(a, st) : launch_full<ST, BT, VEC, false, 1024>(a, st);
 }
 
 }  // namespace
