@@ -1,9 +1,13 @@
 // AdamW over many tensors in one launch, states in float32 or in 8 bits.
 //
 // A pass over memory: w, m and v are read and written once, the gradient read
-// once.  28 bytes a weight in float32; 14 with bf16 gradients and 8-bit
-// states, whose sixty-odd instructions a weight (two 8-bit roundings with a
-// hash each, a division, a square root) then come near the issue rate.
+// once.  28 bytes a weight in float32: bound by memory (100M weights in 429 us,
+// 0.96 of the measured copy rate).  14 bytes with bf16 gradients and 8-bit
+// states: bound by issue, about 90 instructions a weight (two 8-bit roundings
+// and their hash, an exact division and square root: the result has to be the
+// one that IEEE arithmetic gives), 200M weights in 634 us, 0.65 of the copy rate.
+// Each unit's loads are issued before the unit before it is computed (709 us
+// without, at four blocks an SM instead of three).
 //
 // Work is cut into units of 256 consecutive elements of one tensor, one warp
 // each, eight elements a lane: the unit is the block that shares a scale, so
@@ -137,10 +141,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN where eithe
 __device__ __forceinline__ unsigned warp_max(float a) {  // a >= 0 or NaN: the bits order as the values, NaN last
   return __reduce_max_sync(0xffffffffu, __float_as_uint(a));
 }
-template <bool kQ8, int N>
+// PT, GT: the element types of all the launch's parameters and gradients (then
+// without copies and gradient scale), or -1: each tensor's own, branched on for
+// every eight elements.
+template <bool kQ8, int N, int PT, int GT>
 __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ StepArgs<N> a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
+  constexpr bool kPlain = PT >= 0;
+  const float gs = !kPlain && a.grad_scale ? *a.grad_scale : 1.0f;
   const unsigned end = min(a.n_units, (blockIdx.x + 1) * a.span);
   unsigned unit = blockIdx.x * a.span + warp;
   if (unit >= end) return;
@@ -165,8 +173,8 @@ __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ S
       in.vs = t.vs[blk];
     }
     if (!t.vec || t.n - i0 < 8) return;
-    in.g.load(t.g, t.gt, i0);
-    in.p.load(t.p, t.pt, i0);
+    in.g.load(t.g, kPlain ? GT : t.gt, i0);
+    in.p.load(t.p, kPlain ? PT : t.pt, i0);
     if (kQ8) {
       in.cm = *reinterpret_cast<const uint2*>((const unsigned char*)t.m + i0);
       in.cv = *reinterpret_cast<const uint2*>((const unsigned char*)t.v + i0);
@@ -191,15 +199,17 @@ __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ S
     const long long i0 = (long long)blk * EMB_ADAM_BLOCK + lane * 8;
     const int cnt = (int)max(0LL, min(8LL, t.n - i0));
     const bool vec = t.vec && cnt == 8;
+    const int pt = kPlain ? PT : t.pt, gt = kPlain ? GT : t.gt;
+    void* const copy = kPlain ? nullptr : t.copy;
     float p[8], g[8], m[8], u[8];
     if (vec) {
-      in.g.get(t.gt, g);
-      in.p.get(t.pt, p);
+      in.g.get(gt, g);
+      in.p.get(pt, p);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        g[k] = k < cnt ? load1(t.g, t.gt, i0 + k) : 0.0f;
-        p[k] = k < cnt ? load1(t.p, t.pt, i0 + k) : 0.0f;
+        g[k] = k < cnt ? load1(t.g, gt, i0 + k) : 0.0f;
+        p[k] = k < cnt ? load1(t.p, pt, i0 + k) : 0.0f;
       }
     }
     if constexpr (kQ8) {
@@ -244,7 +254,7 @@ __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ S
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float gk = a.grad_scale ? __fmul_rn(g[k], gs) : g[k];
+      const float gk = !kPlain && a.grad_scale ? __fmul_rn(g[k], gs) : g[k];
       m[k] = __fadd_rn(__fmul_rn(m[k], a.beta1), __fmul_rn(gk, a.omb1));
       v[k] = __fadd_rn(__fmul_rn(u[k], a.beta2), __fmul_rn(__fmul_rn(gk, gk), a.omb2));
       u[k] = __fsqrt_rn(v[k]);
@@ -252,14 +262,14 @@ __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ S
       p[k] = __fsub_rn(__fmul_rn(p[k], a.decay), __fdiv_rn(__fmul_rn(m[k], a.lr_c1), den));
     }
     if (vec) {
-      store8(t.p, t.pt, i0, p);
-      if (t.copy) store8(t.copy, t.ct, i0, p);
+      store8(t.p, pt, i0, p);
+      if (copy) store8(copy, t.ct, i0, p);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (k < cnt) {
-          store1(t.p, t.pt, i0 + k, p[k]);
-          if (t.copy) store1(t.copy, t.ct, i0 + k, p[k]);
+          store1(t.p, pt, i0 + k, p[k]);
+          if (copy) store1(copy, t.ct, i0 + k, p[k]);
         }
     }
     if constexpr (kQ8) {
@@ -388,7 +398,15 @@ cudaError_t launch(const emb_adamw_tensor* ts, const void* const* grads, int n, 
   const unsigned blocks_wanted = 6u * (unsigned)sm_count();
   a.span = 8;
   while (a.span < 64 && n_units / (2 * a.span) >= blocks_wanted) a.span *= 2;
-  adamw_kernel<kQ8, N><<<(n_units + a.span - 1) / a.span, 256, 0, st>>>(a);
+  const int grid = (int)((n_units + a.span - 1) / a.span);
+  bool same = a.grad_scale == nullptr;
+  const int pt = a.t[0].pt, gt = a.t[0].gt;
+  for (int i = 0; i < a.n_tensors && same; ++i) same = a.t[i].pt == pt && a.t[i].gt == gt && !a.t[i].copy;
+  if (same && pt == EMB_T_F32 && gt == EMB_T_F32) adamw_kernel<kQ8, N, EMB_T_F32, EMB_T_F32><<<grid, 256, 0, st>>>(a);
+  else if (same && pt == EMB_T_F32 && gt == EMB_T_BF16) adamw_kernel<kQ8, N, EMB_T_F32, EMB_T_BF16><<<grid, 256, 0, st>>>(a);
+  else if (same && pt == EMB_T_BF16 && gt == EMB_T_BF16) adamw_kernel<kQ8, N, EMB_T_BF16, EMB_T_BF16><<<grid, 256, 0, st>>>(a);
+  else if (same && pt == EMB_T_F16 && gt == EMB_T_F16) adamw_kernel<kQ8, N, EMB_T_F16, EMB_T_F16><<<grid, 256, 0, st>>>(a);
+  else adamw_kernel<kQ8, N, -1, -1><<<grid, 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
