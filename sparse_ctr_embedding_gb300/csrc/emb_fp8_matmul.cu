@@ -586,70 +586,89 @@ __device__ __forceinline__ uint4 head16(uint4 q, int keep) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A block's eight warps take 8 / S rows of b, S warps to a row; a lane takes 16
-// neighbouring k's (one scale block for eight lanes) every 512 S, four such
-// pieces of both operands on their way at a time.
-template <int M, int S, typename OT>
+// A block's eight warps take 8 / S groups of R rows of b, S warps to a group; a
+// lane takes 16 neighbouring k's (one scale block for eight lanes) every 512 S.
+// R rows share a's codes and their conversion, half of the work otherwise; eight
+// pieces of b are on their way at a time (four at R = 1).
+template <int M, int S, int R, typename OT>
 __global__ void __launch_bounds__(256) row_kernel(const __grid_constant__ MatmulArgs p) {
-  constexpr int kRows = 8 / S, kBatch = 4;
-  __shared__ float part[8][M];
+  constexpr int kGroups = 8 / S, kBatch = R == 1 ? 4 : 8 / R;
+  __shared__ float part[8][R][M];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int j = blockIdx.x * kRows + warp / S;
-  float acc[M];
+  const int j0 = (blockIdx.x * kGroups + warp / S) * R;
+  float acc[R][M];
 #pragma unroll
-  for (int i = 0; i < M; ++i) acc[i] = 0.0f;
-  if (j < p.n) {
-    const unsigned char* b = p.b + j * p.ldb;
-    const float* sb = p.sb + (j >> p.b_shift);
-    for (int k0 = ((warp % S) * 32 + lane) * 16; k0 < p.k; k0 += kBatch * S * 512) {
-      uint4 qb[kBatch], qa[kBatch][M];
-      float s[kBatch][M];
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int k = k0 + u * S * 512;
-        const bool in = k < p.k;
-        const int kb = k / kBK;
-        qb[u] = in ? __ldg(reinterpret_cast<const uint4*>(b + k)) : make_uint4(0, 0, 0, 0);  // rows are multiples of 16 bytes
-        const float t = in ? __ldg(sb + kb * p.sb_row) : 0.0f;
+    for (int i = 0; i < M; ++i) acc[r][i] = 0.0f;
+  const unsigned char* b[R];
+  const float* sb[R];
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
-          qa[u][i] = in && i < p.m ? __ldg(reinterpret_cast<const uint4*>(p.a + i * p.lda + k)) : make_uint4(0, 0, 0, 0);
-          s[u][i] = in && i < p.m ? t * __ldg(p.sa + kb * p.sa_row + (i >> p.a_shift)) : 0.0f;
-        }
+  for (int r = 0; r < R; ++r) {
+    const int j = min(j0 + r, p.n - 1);  // past the last row: read again, not stored
+    b[r] = p.b + j * p.ldb;
+    sb[r] = p.sb + (j >> p.b_shift);
+  }
+  for (int k0 = ((warp % S) * 32 + lane) * 16; k0 < p.k; k0 += kBatch * S * 512) {
+    uint4 qb[kBatch][R], qa[kBatch][M];
+    float s[kBatch][R], t[kBatch][M];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int k = k0 + u * S * 512;
+      const bool in = k < p.k;
+      const int kb = k / kBK;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        qb[u][r] = in ? __ldg(reinterpret_cast<const uint4*>(b[r] + k)) : make_uint4(0, 0, 0, 0);  // rows are multiples of 16 bytes
+        s[u][r] = in ? __ldg(sb[r] + kb * p.sb_row) : 0.0f;
       }
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int left = p.k - (k0 + u * S * 512);
-        if (left < 16) {  // the row's last piece: what lies past k does not count
-          qb[u] = head16(qb[u], max(left, 0));
+      for (int i = 0; i < M; ++i) {
+        qa[u][i] = in && i < p.m ? __ldg(reinterpret_cast<const uint4*>(p.a + i * p.lda + k)) : make_uint4(0, 0, 0, 0);
+        t[u][i] = in && i < p.m ? __ldg(p.sa + kb * p.sa_row + (i >> p.a_shift)) : 0.0f;
+      }
+    }
 #pragma unroll
-          for (int i = 0; i < M; ++i) qa[u][i] = head16(qa[u][i], max(left, 0));
-        }
+    for (int u = 0; u < kBatch; ++u) {
+      const int left = p.k - (k0 + u * S * 512);
+      if (left < 16) {  // the row's last piece: what lies past k does not count
+#pragma unroll
+        for (int r = 0; r < R; ++r) qb[u][r] = head16(qb[u][r], max(left, 0));
+#pragma unroll
+        for (int i = 0; i < M; ++i) qa[u][i] = head16(qa[u][i], max(left, 0));
+      }
+      float x[M][16];
+#pragma unroll
+      for (int i = 0; i < M; ++i) codes16(qa[u][i], x[i]);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
         float w[16];
-        codes16(qb[u], w);
+        codes16(qb[u][r], w);
 #pragma unroll
         for (int i = 0; i < M; ++i) {
-          float x[16], d = 0.0f;
-          codes16(qa[u][i], x);
+          float d = 0.0f;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) d = fmaf(x[c], w[c], d);
-          acc[i] = fmaf(d, s[u][i], acc[i]);
+          for (int c = 0; c < 16; ++c) d = fmaf(x[i][c], w[c], d);
+          acc[r][i] = fmaf(d, s[u][r] * t[u][i], acc[r][i]);
         }
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < M; ++i) {
-    for (int o = 16; o; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-    if (lane == 0) part[warp][i] = acc[i];
-  }
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      for (int o = 16; o; o >>= 1) acc[r][i] += __shfl_xor_sync(0xffffffffu, acc[r][i], o);
+      if (lane == 0) part[warp][r][i] = acc[r][i];
+    }
   __syncthreads();
-  if (threadIdx.x < kRows * M) {
-    const int r = threadIdx.x / M, i = threadIdx.x % M, col = blockIdx.x * kRows + r;
+  if (threadIdx.x < kGroups * R * M) {
+    const int g = threadIdx.x / (R * M), r = threadIdx.x / M % R, i = threadIdx.x % M;
+    const int col = (blockIdx.x * kGroups + g) * R + r;
     if (col < p.n && i < p.m) {
       float v = 0.0f;
 #pragma unroll
-      for (int s = 0; s < S; ++s) v += part[r * S + s][i];
+      for (int s = 0; s < S; ++s) v += part[g * S + s][r][i];
       ((OT*)p.out)[i * p.ldo + col] = from_f32<OT>(v + (p.bias ? __ldg(p.bias + col) : 0.0f));
     }
   }
@@ -678,7 +697,8 @@ Plan make_plan(long long m, long long n, long long k) {
   Plan pl;
   if (m == 0 || n == 0 || k == 0) return pl;
   pl.k_blocks = (int)((k + kBK - 1) / kBK);
-  if (m <= kRowMax) return pl;
+  // 1 x 16,384 x 8192: 37 us by rows, 45 by tiles; 2 x 8192 x 8192 29 and 23, 2 x 4096 x 8192 18 and 21
+  if (m == 1 || (m == kRowMax && (double)n * k <= 4e7)) return pl;
   const int sms = sm_count();
   const long long mt = (m + kBM - 1) / kBM;
   // The tile's width, and whole tiles or even shares of the steps: whichever a
@@ -757,9 +777,10 @@ cudaError_t launch_tiles(const MatmulArgs& p, const Plan& pl, const CUtensorMap&
 
 template <int M, typename OT>
 cudaError_t launch_rows(const MatmulArgs& p, cudaStream_t st) {
-  // four warps to a row of b when there are too few rows to fill the SMs with one each
-  if (p.k > 1024 && p.n < 32 * sm_count()) row_kernel<M, 4, OT><<<(p.n + 1) / 2, 256, 0, st>>>(p);
-  else row_kernel<M, 1, OT><<<(p.n + 7) / 8, 256, 0, st>>>(p);
+  // Enough rows to give every SM 32 warps: four a warp.  Else one a warp, and four warps to a long one.
+  if (p.n >= 128 * sm_count() / 2) row_kernel<M, 1, 4, OT><<<(p.n + 31) / 32, 256, 0, st>>>(p);
+  else if (p.k > 1024) row_kernel<M, 4, 1, OT><<<(p.n + 1) / 2, 256, 0, st>>>(p);
+  else row_kernel<M, 1, 1, OT><<<(p.n + 7) / 8, 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 

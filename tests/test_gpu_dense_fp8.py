@@ -87,7 +87,8 @@ def check(out, a, sa, b, sb, bias=None):
 SHAPES = [(1, 1, 1), (1, 64, 128), (1, 333, 1000), (2, 128, 64), (3, 1024, 4096), (5, 700, 8192), (8, 96, 200), (9, 40, 300), (16, 256, 512),
           (17, 129, 130), (64, 64, 64), (100, 512, 4096), (127, 255, 129), (128, 256, 128), (128, 128, 1024), (129, 257, 385),
           (200, 1000, 16384), (256, 512, 256), (1000, 300, 1664), (1024, 1664, 2048), (2500, 96, 333), (4096, 640, 768),
-          (40, 2500, 16), (300, 20, 5000)]
+          (40, 2500, 16), (300, 20, 5000), (1, 10001, 300), (1, 9729, 2100), (2, 9800, 1100), (2, 4100, 10000), (10001, 70, 300),
+          (1300, 452, 692), (3000, 1293, 140)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
