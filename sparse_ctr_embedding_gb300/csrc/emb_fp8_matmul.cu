@@ -2,26 +2,37 @@
 //   out[i, j] = bias[j] + sum_b sa[b, i] sb[b, j] sum_{k in b} a[i, k] b[j, k]
 // over blocks b of 128 k's.
 //
-// Tile kernel (m > 2).  A persistent block per SM computes tiles of 128 x BN.
-// One warp brings 128-byte-wide slabs of both operands into a ring of shared
-// memory stages by TMA (128-byte swizzle; rows and columns past the edges
-// arrive as zeros); one thread issues four tcgen05.mma (e4m3, K = 32 each) a
-// slab, which sum one scale block in TMEM; eight warps read that sum from TMEM
-// and add it, times its scales, to float32 accumulators in registers.  Two
-// TMEM accumulators alternate, so the tensor cores work on the next block
-// while the last one is scaled.  The scaling costs one f32 multiply-add per
-// 128 products (a multiply more where b's scales differ by column), about half
-// the issue slots of the 512 cycles the block takes the tensor cores at BN 256.
+// Tile kernel.  A persistent block per SM computes tiles of 128 x BN (256, 128
+// or 64).  One warp brings 128-byte-wide slabs of both operands into a ring of
+// shared memory stages by TMA (128-byte swizzle; rows and columns past the edges
+// arrive as zeros); one elected thread issues four tcgen05.mma (e4m3, K = 32
+// each) a slab, which sum one scale block in TMEM; eight warps read that sum
+// from TMEM and add it, times its scales, to float32 accumulators in registers;
+// one warp fetches the scales.  Two TMEM accumulators alternate, so the tensor
+// cores work on the next block while the last one is scaled.
 //
-// Work is cut into (tile, block) steps.  When the tiles fill the SMs several
-// times over, each is one unit; else all steps are split evenly over the SMs
-// (a tile's blocks then come from several SMs: their float32 partial tiles go
-// to the workspace and a second launch adds them in order).  The split depends
-// on the sizes and the SM count alone.
+// What bounds it (BN 256, cycles a block of 128 k's): the products take 512, the
+// scaling 304 of TMEM reads and 256 of multiply-adds (512 where b's scales
+// differ by column), and with two accumulators the chain products - arrival -
+// reads - release takes half its length, about 850, a block.  131,072 x 1024 x
+// 8192: 750 us, 2930 TFLOP/s, tensor pipe active 0.54 of the time (a product
+// without scales would be 512 of 512); back to back the power limit lowers the
+// clock (970 us).  8192^3: 378 us; by rows 567.  Steps that led here, on the
+// first of these: scaling from a fixed register budget and scales loaded where
+// they are used 1336; packed multiply-adds, registers split by role 1157;
+// scales three steps ahead 972; a warp for the scales 950; the MMA's operands in
+// uniform registers and one completion barrier a stage 789; stores of unaligned
+// rows out of the loop's kernel 750.
 //
-// Row kernel (m <= 2): bound by reading b once; plain CUDA cores, one or more
-// warps per row of b.  From three rows on the tile kernel is faster (4 x 1024 x
-// 8192: 15 us against 18).
+// Work is cut into (tile, block) steps.  Whole tiles go to the SMs in turn, or
+// all steps are split evenly over the SMs (a tile's blocks then come from several
+// SMs: their float32 partial tiles go to the workspace and a second launch adds
+// them in order): make_plan() has the rule.  The split depends on the sizes and
+// the SM count alone.
+//
+// Row kernel (one row, or two by a small b): bound by reading b once; plain CUDA
+// cores.  1 x 1024 x 8192 5.5 us, of which 1.2 is the floor and the rest the
+// latency of a launch and of two loads after one another.
 #include <cuda.h>
 
 #include <algorithm>
@@ -703,7 +714,7 @@ Plan make_plan(long long m, long long n, long long k) {
   const long long mt = (m + kBM - 1) / kBM;
   // The tile's width, and whole tiles or even shares of the steps: whichever a
   // model of the time (us, fitted to 20 shapes from 64 x 1024 x 8192 to 30,584 x
-  // 452 x 692, within a fifth of each) puts first.  A step of 256, 128 or 64
+  // 452 x 692, within 30 % of each) puts first.  A step of 256, 128 or 64
   // columns takes 0.48, 0.33 or 0.29, a tile's end 3.3, 2 or 2; sharing costs the
   // second launch and 0.42 a megabyte of partial tiles.  Measured: 9853 x 448 x
   // 2560 30 whole and 41 shared at 256; 1024 x 1664 x 16,384 64 and 46; 1024 x

@@ -13,6 +13,10 @@
 // 1024-thread teams) over all rows of its team, are joined over a block's
 // teams, and leave as one partial per block; a second launch adds the blocks'
 // partials in order, so the result does not depend on which block ran first.
+// 131,072 x 1024 bf16: 439 us, 0.72 of the measured copy rate; issue and the two
+// dependent sums bound it (16 warps an SM: their sums and rows take 127
+// registers a thread; 85 spill and take 830 us, rows staged in shared memory
+// instead of registers 540).
 #include <algorithm>
 
 #include "emb_norm.cuh"

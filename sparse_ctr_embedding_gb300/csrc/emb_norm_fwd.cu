@@ -6,7 +6,10 @@
 // Bound by memory: x, f and a per-element gate in, y and h out, once each; the
 // vectors stay in registers over a team's rows.  Two row sums (four for a
 // layer norm) separate the loads from the stores, so each team loads its next
-// row before it reduces the current one.
+// row before it reduces the current one.  131,072 x 1024 bf16: 224 us, 0.88 of
+// the measured copy rate; 16,384 x 1664 with a float32 stream 74 us, 0.76.  Rows
+// that are not multiples of eight elements go one element at a time: 65,536 x
+// 1003 281 us, 0.34 (issue: about sixty instructions an element).
 #include <algorithm>
 #include <cmath>
 
