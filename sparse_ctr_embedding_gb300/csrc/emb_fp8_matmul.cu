@@ -60,7 +60,7 @@ struct MatmulArgs {
   const unsigned char *a, *b;
   const float *sa, *sb, *bias;
   void* out;
-  float* partial;            // [slots][kBM][BN]
+  float* partial;            // [slots][kBM * BN]
   long long lda, ldb, ldo;
   long long sa_row, sb_row;  // scales in a row of sa and sb
   int m, n, k;
@@ -527,9 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           }
         }
       } else if (row < p.m) {  // part of a tile: slot (block + tile) is this piece's alone
-        float* dst = p.partial + ((long long)(blockIdx.x + u.tile) * kBM + quarter * 32 + lane) * BN + half * C::kHalf;
+        float* dst = p.partial + (long long)(blockIdx.x + u.tile) * kBM * BN + (warp * C::kHalf * 4 + lane) * 8;
 #pragma unroll
-        for (int c = 0; c < C::kHalf; c += 8) store32<float>(dst + c, acc + c);
+        for (int c = 0; c < C::kHalf; c += 8) store32<float>(dst + c * 32, acc + c);
       }
     }
   }
@@ -541,21 +541,23 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   }
 }
 
-// Adds the pieces of each tile that several blocks computed, in k order.  One
-// block takes 1024 neighbouring elements (whole rows) of a tile, four a thread.
+// Adds the pieces of each tile that several blocks computed, in k order.  A piece
+// lies as the scaling warps store it, whole kilobytes at a time: by warps, by 8
+// columns, by rows (1664 x 452 x 30,584 to bf16: 52 us, and 56 with pieces laid
+// out by rows).  One block takes 32 rows x 32 columns, four columns a thread.
 template <int BN, typename OT>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ MatmulArgs p) {
-  constexpr int kRows = 1024 / BN;
-  const long long tile = blockIdx.x / (kBM / kRows);
-  const int r = (int)(blockIdx.x % (kBM / kRows)) * kRows + threadIdx.x / (BN / 4), c = threadIdx.x % (BN / 4) * 4;
+  constexpr int kBlocks = kBM * BN / 1024, kHalf = TileCfg<BN>::kHalf, kWarpBlocks = kHalf / 32;
+  const long long tile = blockIdx.x / kBlocks;
+  const int q = (int)(blockIdx.x % kBlocks), warp = q / kWarpBlocks, x = threadIdx.x / 8, y = threadIdx.x % 8;
   const long long first = tile * p.k_blocks / p.per_cta, last = ((tile + 1) * p.k_blocks - 1) / p.per_cta;
   if (first == last) return;  // one block had it whole
   int tm, tn;
   tile_at(p, tile, &tm, &tn);
-  const int row = tm * kBM + r, col = tn * BN + c;
+  const int row = tm * kBM + (warp & 3) * 32 + x, col = tn * BN + (warp >> 2) * kHalf + q % kWarpBlocks * 32 + y * 4;
   if (row >= p.m || col >= p.n) return;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const float* src = p.partial + ((first + tile) * kBM + r) * BN + c;
+  const float* src = p.partial + (first + tile) * kBM * BN + q * 1024 + y / 2 * 256 + x * 8 + y % 2 * 4;
 #pragma unroll 8
   for (long long b = first; b <= last; ++b, src += (long long)kBM * BN) {
     const float4 w = *reinterpret_cast<const float4*>(src);
