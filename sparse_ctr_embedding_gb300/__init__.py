@@ -696,13 +696,19 @@ def emb_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
         if out.shape != (m, n):
             raise ValueError(f"out must be [{m}, {n}]")
         ldo = _row_stride(out, "out")
+    wp, ws_bytes = None, 0
     if workspace is None:
-        workspace = _empty(stream, a, emb_fp8_matmul_workspace_size(m, n, k), _U8)
+        ws_bytes = emb_fp8_matmul_workspace_size(m, n, k)
+        if ws_bytes:
+            workspace = _empty(stream, a, ws_bytes, _U8)
+            wp = workspace.data_ptr()
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
+    else:
+        wp, ws_bytes = workspace.data_ptr(), workspace.nbytes
     _check(lib().emb_fp8_matmul(a.data_ptr(), lda, _dense(sa, _F32, "sa"), a_rows, b.data_ptr(), ldb, _dense(sb, _F32, "sb"),
                                 b_rows, m, n, k, None if bias is None else _dense(bias, _F32, "bias"), out.data_ptr(),
-                                _ftype(out.dtype, "out"), ldo, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream)))
+                                _ftype(out.dtype, "out"), ldo, wp, ws_bytes, _raw_stream(stream)))
     return out
 
 
