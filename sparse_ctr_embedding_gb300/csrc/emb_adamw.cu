@@ -1,13 +1,13 @@
 // AdamW over many tensors in one launch, states in float32 or in 8 bits.
 //
 // A pass over memory: w, m and v are read and written once, the gradient read
-// once.  28 bytes a weight in float32: bound by memory (100M weights in 429 us,
-// 0.96 of the measured copy rate).  14 bytes with bf16 gradients and 8-bit
-// states: bound by issue, about 90 instructions a weight (two 8-bit roundings
-// and their hash, an exact division and square root: the result has to be the
-// one that IEEE arithmetic gives), 200M weights in 634 us, 0.65 of the copy rate.
-// Each unit's loads are issued before the unit before it is computed (709 us
-// without, at four blocks an SM instead of three).
+// once.  28 bytes a weight in float32: bound by memory (100M weights in 416 us,
+// 0.99 of the measured copy rate).  14 bytes with bf16 gradients and 8-bit
+// states: bound by issue (two 8-bit roundings and their hash, an exact division
+// and square root: the result has to be the one that IEEE arithmetic gives), 200M
+// weights in 612 us, 0.67 of the copy rate.  Each unit's loads are issued before
+// the unit before it is computed (709 us without, at four blocks an SM instead of
+// three), and plain products and sums are done in pairs (627 us without).
 //
 // Work is cut into units of 256 consecutive elements of one tensor, one warp
 // each, eight elements a lane: the unit is the block that shares a scale, so
@@ -43,7 +43,7 @@ struct StepArgs {
   int n_tensors;
   unsigned n_units;
   unsigned span;        // consecutive units a block takes
-  float beta1, omb1, beta2, omb2, decay, lr_c1, rc2, eps;
+  float beta1, omb1, beta2, omb2, decay, lr_c1, rc2, eps, one;
   unsigned key;
   const float* grad_scale;
 };
@@ -121,16 +121,51 @@ __device__ __forceinline__ unsigned fmix32(unsigned h) {
   return h ^ (h >> 16);
 }
 
+// Two elements side by side: each is rounded by itself as in the scalar operation,
+// in one issue slot for both.  A sum is written as a multiply-add by `one`, a
+// kernel argument: of a product and a sum in pairs the assembler makes one
+// multiply-add with one rounding, whatever their rounding modifiers say.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n.reg .b64 x, y;\n"
+      "mov.b64 x, {%2, %3};\n"
+      "mov.b64 y, {%4, %5};\n"
+      "mul.rn.f32x2 x, x, y;\n"
+      "mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float one, float2 b) {  // one = -1: b - a
+  float2 r;
+  asm("{\n.reg .b64 x, y, z;\n"
+      "mov.b64 x, {%2, %3};\n"
+      "mov.b64 y, {%4, %4};\n"
+      "mov.b64 z, {%5, %6};\n"
+      "fma.rn.f32x2 x, x, y, z;\n"
+      "mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(one), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 pair(const float* a, int k) { return make_float2(a[2 * k], a[2 * k + 1]); }
+__device__ __forceinline__ void put(float* a, int k, float2 x) {
+  a[2 * k] = x.x;
+  a[2 * k + 1] = x.y;
+}
+
 // A magnitude in code units to one of the two codes around it, upwards with the
 // probability of its distance from the lower one.  Codes from 2^-6 on have 3
 // mantissa bits: adding 20 random bits below them and cutting rounds to one of
 // them.  Below 2^-6 codes are 2^-9 apart; adding 2^-6 first puts that spacing at
 // the same bit.  The block's largest value is 448 up to three units in its last
 // place, and r20 leaves seven, so it is never carried past 448.  mag is finite.
-__device__ __forceinline__ float round_random(float mag, unsigned r20) {
-  const float base = mag < 0.015625f ? 0.015625f : 0.0f;
-  const unsigned cut = (__float_as_uint(__fadd_rn(mag, base)) + r20) & ~0xFFFFFu;
-  return __fsub_rn(__uint_as_float(cut), base);
+__device__ __forceinline__ float2 round_random(float2 mag, float one, unsigned r20x, unsigned r20y) {
+  const float2 base = make_float2(mag.x < 0.015625f ? 0.015625f : 0.0f, mag.y < 0.015625f ? 0.015625f : 0.0f);
+  const float2 sum = add2(mag, one, base);
+  const unsigned x = (__float_as_uint(sum.x) + r20x) & ~0xFFFFFu, y = (__float_as_uint(sum.y) + r20y) & ~0xFFFFFu;
+  return add2(base, -one, make_float2(__uint_as_float(x), __uint_as_float(y)));
 }
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN where either is
@@ -226,15 +261,10 @@ __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ S
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 x = e4m3x2_to_f32((unsigned short)(w[k >> 1] >> (16 * (k & 1))));
-        const float2 y = e4m3x2_to_f32((unsigned short)(w[2 + (k >> 1)] >> (16 * (k & 1))));
-        m[2 * k] = __fmul_rn(x.x, in.ms);
-        m[2 * k + 1] = __fmul_rn(x.y, in.ms);
-        u[2 * k] = __fmul_rn(y.x, in.vs);
-        u[2 * k + 1] = __fmul_rn(y.y, in.vs);
+        put(m, k, mul2(e4m3x2_to_f32((unsigned short)(w[k >> 1] >> (16 * (k & 1)))), both(in.ms)));
+        const float2 y = mul2(e4m3x2_to_f32((unsigned short)(w[2 + (k >> 1)] >> (16 * (k & 1)))), both(in.vs));
+        put(u, k, mul2(y, y));
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = __fmul_rn(u[k], u[k]);
     } else {
       if (vec) {
         in.m.get(EMB_T_F32, m);
@@ -253,13 +283,17 @@ __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ S
     }
     float v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float gk = !kPlain && a.grad_scale ? __fmul_rn(g[k], gs) : g[k];
-      m[k] = __fadd_rn(__fmul_rn(m[k], a.beta1), __fmul_rn(gk, a.omb1));
-      v[k] = __fadd_rn(__fmul_rn(u[k], a.beta2), __fmul_rn(__fmul_rn(gk, gk), a.omb2));
-      u[k] = __fsqrt_rn(v[k]);
-      const float den = __fadd_rn(__fmul_rn(u[k], a.rc2), a.eps);
-      p[k] = __fsub_rn(__fmul_rn(p[k], a.decay), __fdiv_rn(__fmul_rn(m[k], a.lr_c1), den));
+    for (int k = 0; k < 4; ++k) {
+      const float2 gk = !kPlain && a.grad_scale ? mul2(pair(g, k), both(gs)) : pair(g, k);
+      const float2 mk = add2(mul2(pair(m, k), both(a.beta1)), a.one, mul2(gk, both(a.omb1)));
+      const float2 vk = add2(mul2(pair(u, k), both(a.beta2)), a.one, mul2(mul2(gk, gk), both(a.omb2)));
+      const float2 uk = make_float2(__fsqrt_rn(vk.x), __fsqrt_rn(vk.y));
+      const float2 den = add2(mul2(uk, both(a.rc2)), a.one, both(a.eps)), num = mul2(mk, both(a.lr_c1));
+      const float2 quo = make_float2(__fdiv_rn(num.x, den.x), __fdiv_rn(num.y, den.y));
+      put(p, k, add2(quo, -a.one, mul2(pair(p, k), both(a.decay))));
+      put(m, k, mk);
+      put(v, k, vk);
+      put(u, k, uk);
     }
     if (vec) {
       store8(t.p, pt, i0, p);
@@ -298,11 +332,13 @@ __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ S
       const unsigned mix = ((unsigned)(e0 >> 32) * 0x9e3779b9u) ^ a.key;
       float qm[8], qu[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const unsigned r = fmix32(((unsigned)e0 + k) ^ mix);
-        const float xm = __fmul_rn(m[k], im);
-        qm[k] = copysignf(round_random(fabsf(xm), ((r & 0xffffu) << 4) + 8u), xm);
-        qu[k] = fmaxf(round_random(__fmul_rn(u[k], iu), ((r >> 16) << 4) + 8u), u[k] > 0.0f ? 0.001953125f : 0.0f);
+      for (int k = 0; k < 4; ++k) {
+        const unsigned rx = fmix32(((unsigned)e0 + 2 * k) ^ mix), ry = fmix32(((unsigned)e0 + 2 * k + 1) ^ mix);
+        const float2 xm = mul2(pair(m, k), both(im));
+        const float2 rm = round_random(make_float2(fabsf(xm.x), fabsf(xm.y)), a.one, ((rx & 0xffffu) << 4) + 8u, ((ry & 0xffffu) << 4) + 8u);
+        put(qm, k, make_float2(copysignf(rm.x, xm.x), copysignf(rm.y, xm.y)));
+        const float2 ru = round_random(mul2(pair(u, k), both(iu)), a.one, ((rx >> 16) << 4) + 8u, ((ry >> 16) << 4) + 8u);
+        put(qu, k, make_float2(fmaxf(ru.x, u[2 * k] > 0.0f ? 0.001953125f : 0.0f), fmaxf(ru.y, u[2 * k + 1] > 0.0f ? 0.001953125f : 0.0f)));
       }
       if (!finite) {  // such a value would have carried out of its bits: it becomes the code NaN
 #pragma unroll
@@ -392,6 +428,7 @@ cudaError_t launch(const emb_adamw_tensor* ts, const void* const* grads, int n, 
   a.lr_c1 = (float)(p->lr / c1);
   a.rc2 = (float)(1.0 / std::sqrt(c2));
   a.eps = (float)p->eps;
+  a.one = 1.0f;
   a.key = p->seed * 0x9e3779b9u + (unsigned)p->step * 0x85ebca6bu;
   a.grad_scale = p->grad_scale_d;
   // a block takes up to 64 consecutive units (8 a warp), fewer when that would leave SMs without one
