@@ -3,7 +3,7 @@
 // A pass over memory: w, m and v are read and written once, the gradient read
 // once.  28 bytes a weight in float32: bound by memory (100M weights in 416 us,
 // 0.99 of the measured copy rate).  14 bytes with bf16 gradients and 8-bit
-// states: bound by issue (two 8-bit roundings and their hash, an exact division
+// states: bound by issue (86 instructions: two 8-bit roundings and their hash, an exact division
 // and square root: the result has to be the one that IEEE arithmetic gives), 200M
 // weights in 612 us, 0.67 of the copy rate.  Each unit's loads are issued before
 // the unit before it is computed (709 us without, at four blocks an SM instead of
