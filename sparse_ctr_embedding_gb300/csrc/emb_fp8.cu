@@ -95,15 +95,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quantize_kernel(const __grid_c
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[i][k] = to_f32<T>(raw[i][k]);
   }
-  // The largest magnitude of each row's four.  fmaxf passes NaN over, as it should;
-  // a thread that meets an infinity makes its infinities NaN first (e4m3 has none)
-  // and takes the maxima again.
+  // The largest magnitude of each row's four, from 0 on: fmaxf passes NaN over
+  // beside a number, but of four NaN it makes NaN, whose bits would win the warp's
+  // maximum.  A thread that meets an infinity makes its infinities NaN first (e4m3
+  // has none) and takes the maxima again.
   float top[kRows];
   auto maxima = [&] {
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      top[i] = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
+      top[i] = fmaxf(fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3]))), 0.0f);
       m = fmaxf(m, top[i]);
     }
     return m;

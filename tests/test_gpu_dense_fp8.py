@@ -187,3 +187,28 @@ def test_linear_layer_gradients_against_differences():
         mine = float((got.cpu().double() * v).sum())
         terms = (dy.double().abs() @ w.double().abs() if at == 0 else dy.double().abs().t() @ x.double().abs()) * v.abs()
         assert abs(mine - slope) <= (2 * 2.0 ** -4 + 2.0 ** -8) * float(terms.sum()), (mine, slope)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("run", [4, 8, 64])
+def test_quantize_scale_beside_runs_of_non_finite_values(run, block_rows, dtype):
+    """Values that are not finite leave their block's scale to the finite ones, also
+    where whole groups of neighbours are of that kind (a pooled row with one
+    diverged slot), on and off the groups' boundaries, along rows and columns."""
+    g = torch.Generator().manual_seed(run)
+    x = torch.randn(260, 400, generator=g)
+    for i, bad in enumerate((float("nan"), float("inf"), -float("inf"))):
+        for j, at in enumerate((0, 4, 61, 128, 129, 190)):
+            x[3 * j + i, at:at + run] = bad
+            x[128 + at // 3:128 + at // 3 + run, 20 * i + j + 200] = bad
+    x[40, 128:256] = float("nan")       # a block with nothing finite at all
+    x[41, :128] = float("inf")
+    x = x.to(dtype)
+    q, s, qt, st = E.emb_fp8_quantize(x.cuda(), block_rows=block_rows, transpose=True)
+    for got, scale, src in ((q, s, x), (qt, st, x.t())):
+        rq, rs = block_scales(src, block_rows)
+        assert torch.equal(scale.cpu(), rs)
+        assert torch.equal(bits(got), bits(rq))
+    q1, s1 = E.emb_fp8_quantize(x.cuda(), block_rows=block_rows)
+    assert torch.equal(bits(q1), bits(q)) and torch.equal(s1, s)
