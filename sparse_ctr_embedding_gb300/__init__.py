@@ -835,7 +835,10 @@ class AdamW:
     "q8": m and sqrt(v) as e4m3 codes with a scale per 256 elements,
     stochastically rounded from `seed`.  The states live in `arena` (m, v, m_scale,
     v_scale: all tensors one after another, each from a multiple of 256 elements),
-    which with `step_count` is the checkpoint; load_state takes per-tensor lists."""
+    which with `step_count` is the checkpoint; load_state takes per-tensor lists.
+    A parameter, copy or state that is given other storage (p.data = ..., half(),
+    set_()) is found by its address at the next step and described anew (the old
+    storage is held until then); its size and device must stay."""
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999),
                  eps: float = 1e-8, weight_decay: float = 0.01, state: str = "f32", seed: int = 0,
@@ -861,20 +864,48 @@ class AdamW:
         self.arena = {"m": zeros(total, st), "v": zeros(total, st),
                       "m_scale": zeros(total // block, torch.float32) if q8 else None,
                       "v_scale": zeros(total // block, torch.float32) if q8 else None}
-        self._tensors = (_AdamwTensor * len(self.params))()
-        base = {k: 0 if v is None else v.data_ptr() for k, v in self.arena.items()}
+        self._total, self._state_type = total, st
+        self._grad_dtypes = [p.dtype for p in self.params]
+        self._bind()
+
+    def _used(self):
+        """Every tensor whose address a step uses, the gradients apart."""
+        return self.params + [c for c in self._copies if c is not None] + [v for v in self.arena.values() if v is not None]
+
+    def _bind(self) -> None:
+        """Describes parameters, copies and states to the library, as they are now.  The
+        addresses are kept for the steps, and with them an alias of each tensor: as
+        long as it lives no other tensor can come to lie there, so an address that is
+        still the same is still the same memory."""
+        q8, block = self._state == 1, EMB_ADAM_BLOCK
+        base, size = {}, {"m": self._total, "v": self._total, "m_scale": self._total // block, "v_scale": self._total // block}
+        for k, v in self.arena.items():
+            if (v is None) != (k.endswith("scale") and not q8) or (v is not None and (v.numel() != size[k] or v.device != self.device)):
+                raise ValueError(f"arena {k} does not match the state kind {self.state} and {self._total} elements")
+            base[k] = 0 if v is None else _dense(v, torch.float32 if k.endswith("scale") else self._state_type, f"arena {k}")
+        if len(self.params) != len(self._n):
+            raise ValueError("the number of parameters has changed")
+        tensors = (_AdamwTensor * len(self.params))()
+        st = self._state_type.itemsize
         for i, (p, c) in enumerate(zip(self.params, self._copies)):
             if p.device != self.device:
                 raise ValueError("parameters must be on one device")
+            if p.numel() != self._n[i]:
+                raise ValueError(f"parameter {i} had {self._n[i]} elements and has {p.numel()}")
             if c is not None and c.numel() != p.numel():
                 raise ValueError("a copy must have its parameter's size")
-            at, kind = self._at[i], _ftype(p.dtype, "param")
-            self._tensors[i] = _AdamwTensor(_dense(p, p.dtype, "param"), None if c is None else _dense(c, c.dtype, "copy"),
-                                            base["m"] + at * st.itemsize, base["v"] + at * st.itemsize,
-                                            base["m_scale"] + at // block * 4 if q8 else None,
-                                            base["v_scale"] + at // block * 4 if q8 else None, self._n[i], at,
-                                            kind, kind, 0 if c is None else _ftype(c.dtype, "copy"))
-        self._grad_dtypes = [p.dtype for p in self.params]
+            at = self._at[i]
+            tensors[i] = _AdamwTensor(_dense(p, p.dtype, "param"), None if c is None else _dense(c, c.dtype, "copy"),
+                                      base["m"] + at * st, base["v"] + at * st,
+                                      base["m_scale"] + at // block * 4 if q8 else None,
+                                      base["v_scale"] + at // block * 4 if q8 else None, self._n[i], at,
+                                      _ftype(p.dtype, "param"), _ftype(self._grad_dtypes[i], "grad"),
+                                      0 if c is None else _ftype(c.dtype, "copy"))
+        used = self._used()
+        for t in used:
+            if (t.storage_offset() + t.numel()) * t.itemsize > t.untyped_storage().nbytes():
+                raise ValueError("a parameter, copy or state has lost its storage")
+        self._tensors, self._addresses, self._aliases = tensors, list(map(torch.Tensor.data_ptr, used)), [t.detach() for t in used]
 
     def load_state(self, step: int, m, v, m_scale=None, v_scale=None) -> None:
         """Sets the states from one tensor per parameter (the layout of `arena`, without its padding)."""
@@ -905,6 +936,8 @@ class AdamW:
         T = torch.Tensor
         if list(map(T.numel, grads)) != self._n or not all(map(T.is_contiguous, grads)) or not all(map(_on_cuda, grads)):
             raise ValueError("each gradient must be a contiguous CUDA tensor of its parameter's size")
+        if list(map(T.data_ptr, self._used())) != self._addresses:
+            self._bind()                    # a parameter, copy or state has moved
         dtypes = list(map(_dtype_of, grads))
         if dtypes != self._grad_dtypes:
             kinds = [_ftype(g, "grad") for g in dtypes]

@@ -184,3 +184,83 @@ def test_refusals():
         opt.step([p.clone()])
     assert ei.value.name == "EMB_ERR_INVALID_ARG"
     assert opt.step_count == 0
+
+
+@pytest.mark.parametrize("state", ["f32", "q8"])
+def test_parameters_copies_and_states_that_move(state):
+    """New storage under the same tensors (p.data = ..., half(), set_(), a replaced
+    state): a step updates what the tensors are now, and writes nothing where they were."""
+    g = torch.Generator().manual_seed(4)
+    init = [torch.randn(n, generator=g) for n in (700, 33, 5)]
+    grads = [[torch.randn(n, generator=g).cuda() for n in (700, 33, 5)] for _ in range(5)]
+
+    def start():
+        p = [t.cuda() for t in init]
+        c = [torch.empty(700, dtype=BF16, device="cuda"), None, None]
+        return p, c, E.AdamW(p, lr=1e-2, state=state, seed=1, copies=c)
+
+    p, c, opt = start()
+    still_p, still_c, still = start()
+    same = lambda: all(torch.equal(a, b) for a, b in zip(p, still_p)) and torch.equal(c[0], still_c[0])  # noqa: E731
+    opt.step(grads[0])
+    still.step(grads[0])
+    assert same()
+    kept = [p[0].data, p[1].detach(), c[0].data]     # the storage that the tensors leave
+    p[0].data = p[0].data.clone()
+    p[1].set_(p[1].clone())
+    c[0].data = torch.empty_like(c[0].data)
+    before = [t.clone() for t in kept]
+    opt.step(grads[1])
+    still.step(grads[1])
+    assert same() and torch.equal(kept[0], before[0]) and torch.equal(kept[2], before[2])
+    old = opt.arena["m"]
+    opt.arena["m"] = old.clone()
+    seen = old.view(torch.uint8).clone()
+    opt.step(grads[2])
+    still.step(grads[2])
+    assert same() and torch.equal(old.view(torch.uint8), seen)
+    for key in opt.arena:
+        if opt.arena[key] is not None:
+            assert torch.equal(opt.arena[key].view(torch.uint8), still.arena[key].view(torch.uint8)), key
+    # a parameter of another type, as module.half() leaves it: the step of an optimizer made for it
+    wide = p[2].data
+    p[2].data = p[2].data.half()
+    twin = [p[2].detach().clone()]
+    of = E.AdamW(twin, lr=1e-2, state=state, seed=1)
+    at = opt._at[2]
+    cut = {k: None if v is None else [v[at // 256:at // 256 + 1] if k.endswith("scale") else v[at:at + 5]] for k, v in opt.arena.items()}
+    of.load_state(opt.step_count, **cut)
+    of._tensors[0].first = at
+    before = wide.clone()
+    opt.step(grads[3])
+    of.step([grads[3][2]])
+    assert torch.equal(p[2], twin[0]) and torch.equal(wide, before)
+
+
+def test_parameters_that_change_size_or_lose_their_storage_are_refused():
+    p = [torch.zeros(300, device="cuda"), torch.zeros(20, device="cuda")]
+    opt = E.AdamW(p, state="q8")
+    grads = [torch.ones(300, device="cuda"), torch.ones(20, device="cuda")]
+    whole = p[0].data
+    for other in (torch.zeros(200, device="cuda"), torch.zeros(600, device="cuda")[::2], torch.zeros(300),
+                  torch.zeros(300, dtype=torch.float64, device="cuda")):
+        p[0].data = other
+        with pytest.raises((ValueError, TypeError)):
+            opt.step(grads)
+        assert opt.step_count == 0 and bool((p[1] == 0).all())
+    p[0].data = whole
+    q = torch.zeros(40, device="cuda")
+    p[1].data = q[20:]
+    q.untyped_storage().resize_(0)
+    with pytest.raises(ValueError):
+        opt.step(grads)
+    p[1].data = torch.zeros(20, device="cuda")
+    arena = opt.arena["v"]
+    for bad in (arena[:256], arena.float(), None):
+        opt.arena["v"] = bad
+        with pytest.raises((ValueError, TypeError)):
+            opt.step(grads)
+    opt.arena["v"] = arena
+    assert opt.step_count == 0 and bool((p[0] == 0).all())
+    opt.step(grads)
+    assert bool((p[0] < 0).all()) and bool((p[1] < 0).all())
