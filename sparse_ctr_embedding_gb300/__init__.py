@@ -25,7 +25,7 @@ __all__ = [
     "emb_table_create", "emb_table_create_device", "emb_table_destroy", "emb_table_get_stats", "emb_table_plan",
     "emb_lookup_fwd", "emb_lookup_fwd_record", "emb_lookup_fwd_dedup", "emb_bwd_adagrad_recorded", "emb_bwd_workspace_size", "emb_bwd_adagrad", "emb_bwd_adagrad_noalloc",
     "emb_bwd_ftrl", "emb_bwd_ftrl_recorded", "emb_table_export_z", "emb_table_import_z",
-    "emb_debug_fail_device_alloc", "emb_debug_live_device_allocs", "emb_debug_set_probe_bound", "Pipeline",
+    "emb_debug_fail_device_alloc", "emb_debug_live_device_allocs", "emb_debug_set_probe_bound", "emb_debug_lose_op_wait", "Pipeline",
     "emb_bwd_unique_keys", "emb_bwd_phase_events", "EMB_NOALLOC_SCRATCH_BYTES", "EMB_SORT_DIGIT_BITS", "BWD_PHASES",
     "emb_resolve", "emb_table_export", "emb_table_export_rows", "emb_table_slots", "emb_check_device_flag",
     "emb_status_string", "emb_last_error",
@@ -154,6 +154,7 @@ def lib():
             "emb_pipeline_release": [_vp, _i64],
             "emb_pipeline_wait": [_vp, _i64],
             "emb_debug_set_probe_bound": [_vp, _i64],
+            "emb_debug_lose_op_wait": [ctypes.c_int32, _i64],
             "emb_table_import_z": [_vp, _vp, _vp],
             "emb_resolve": [_vp, _vp, _i64, _vp, _vp, _vp],
             "emb_table_export": [_vp, _vp, _vp, _vp, _vp],
@@ -512,6 +513,12 @@ def emb_debug_set_probe_bound(table: Table, bound: int) -> None:
     """Fault injection: lower the table's probe bound (as a corrupted table would)."""
     _check(lib().emb_debug_set_probe_bound(table.handle, int(bound)))
     table.stats = emb_table_get_stats(table)
+
+
+def emb_debug_lose_op_wait(role: Optional[str], step: int = 0) -> None:
+    """From now on the wait of this role ("load", "product", "scales", "other") at this step of a tiled
+    emb_fp8_matmul counts as run out (None: none, the default)."""
+    _check(lib().emb_debug_lose_op_wait(-1 if role is None else ("load", "product", "scales", "other").index(role), int(step)))
 
 
 class Pipeline:

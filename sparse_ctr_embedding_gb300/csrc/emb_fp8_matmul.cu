@@ -36,6 +36,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "emb_dense.cuh"
@@ -54,6 +55,7 @@ constexpr int kLaunchRegs = 168, kScaleRegs = 224, kOtherRegs = 56;
 static_assert(kScaleWarps * 32 * kScaleRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kTmaWarp = kScaleWarps, kMmaWarp = kScaleWarps + 1, kFetchWarp = kScaleWarps + 2;
 constexpr int kAhead = 8;            // steps whose scales are held or on their way
+constexpr int kAfterLoads = 0;       // lost_warp: not a warp's wait, but the block is told when its last load is issued
 constexpr unsigned kWaitLimit = 1u << 21;  // polls of one wait before the kernel gives up
 
 struct MatmulArgs {
@@ -69,6 +71,8 @@ struct MatmulArgs {
   long long steps;           // m_tiles * n_tiles * k_blocks
   long long per_cta;         // steps a block takes; 0: whole tiles, block-stride
   int wide_out;              // rows of out are aligned to 32 bytes
+  int lost_warp;             // the warp whose wait at step lost_step counts as run out; -1: none
+  unsigned lost_step;
 };
 
 // ------------------------------------------------------------------ PTX
@@ -94,6 +98,12 @@ __device__ __forceinline__ bool mbar_try(unsigned bar, unsigned parity) {
       : "memory");
   return ok != 0;
 }
+// What a wait that ran out does: the block's other waits end too, and the host is told.
+__device__ __forceinline__ bool give_up(volatile int* stop) {
+  *stop = 1;
+  atomicOr(&g_op_flags, EMB_FLAG_OP_TIMEOUT);
+  return false;
+}
 // Waits for a barrier's phase; false when the limit ran out here or in another
 // warp of the block (`stop`), after which the caller leaves its loops.
 __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity, volatile int* stop) {
@@ -102,9 +112,11 @@ __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity, volatil
     if (mbar_try(bar, parity)) return true;
     if (*stop) return false;
   }
-  *stop = 1;
-  atomicOr(&g_op_flags, EMB_FLAG_OP_TIMEOUT);
-  return false;
+  return give_up(stop);
+}
+// After a wait has run out: waits for a barrier of what is still in flight.
+__device__ __forceinline__ void mbar_drain(unsigned bar, unsigned parity) {
+  for (unsigned i = 0; i < kWaitLimit && !mbar_try(bar, parity); ++i) {}
 }
 // One lane of a converged warp.  A branch on it (and not on a lane number) lets
 // the compiler keep what the lane issues in uniform registers: with the latter
@@ -254,6 +266,15 @@ __device__ __forceinline__ bool next_unit(const MatmulArgs& p, long long* pos, l
   tile_at(p, u->tile, &u->tm, &u->tn);
   return true;
 }
+// Where a test asked for a step's wait to run out (emb_debug_lose_op_wait): ends the
+// unit before that step, and tells after it that the step is reached.  Not asked in
+// the scaling warps, where even once a unit it cost products by rows 3 %.
+__device__ __forceinline__ void cut_lost(const MatmulArgs& p, int role, unsigned it, Unit* u) {
+  if (p.lost_warp == role) u->kb1 = u->kb0 + (int)min((unsigned)(u->kb1 - u->kb0), p.lost_step - it);
+}
+__device__ __forceinline__ bool at_lost(const MatmulArgs& p, int role, unsigned it) {
+  return p.lost_warp == role && p.lost_step == it;
+}
 __device__ __forceinline__ void my_range(const MatmulArgs& p, long long* pos, long long* end) {
   if (p.per_cta == 0) {
     *pos = blockIdx.x;
@@ -298,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   __shared__ __align__(8) unsigned long long bars[2 * C::kStages + 2 + 2 * kAhead];
   __shared__ unsigned tmem_slot;
   __shared__ int stop_flag;
+  __shared__ unsigned issued[3];  // steps whose loads, products and scales were issued
   volatile int* stop = &stop_flag;
   const unsigned smem = (smem_u32(raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -340,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       unsigned it = 0;
       bool go = true;
       while (go && next_unit(p, &pos, end, &u)) {
+        cut_lost(p, kTmaWarp, it, &u);
         for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
           const unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
           go = __all_sync(0xffffffffu, mbar_wait(done0 + 8 * s, ph ^ 1, stop));
@@ -352,12 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           }
           __syncwarp();
         }
+        if (go && at_lost(p, kTmaWarp, it)) go = give_up(stop);
       }
-      if (!go) {  // gave up: the loads in flight must land before the block ends
-        const unsigned n = min(it, (unsigned)C::kStages);
-        for (unsigned j = it - n; j < it; ++j)
-          for (unsigned i = 0; i < kWaitLimit && !mbar_try(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1); ++i) {}
-      }
+      if (p.lost_warp == kAfterLoads) give_up(stop);
+      issued[0] = it;
     }
     if (warp == kMmaWarp) {
       // f32 accumulator, e4m3 x e4m3, both K-major, N = BN, M = 128
@@ -365,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       unsigned it = 0;
       bool go = true;
       while (go && next_unit(p, &pos, end, &u)) {
+        cut_lost(p, kMmaWarp, it, &u);
         for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
           const unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
           const unsigned t = it & 1, tph = (it >> 1) & 1;
@@ -382,11 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           }
           __syncwarp();
         }
+        if (go && at_lost(p, kMmaWarp, it)) go = give_up(stop);
       }
-      if (!go && it > 0) {  // gave up: wait for the products in flight before TMEM is freed
-        const unsigned j = it - 1;
-        for (unsigned i = 0; i < kWaitLimit && !mbar_try(done0 + 8 * (j % C::kStages), (j / C::kStages) & 1); ++i) {}
-      }
+      issued[1] = it;
     }
     if (warp == kFetchWarp) {
       // The steps' scales, by 4-byte asynchronous copies (rows of scales have no
@@ -394,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       unsigned it = 0;
       bool go = true;
       while (go && next_unit(p, &pos, end, &u)) {
+        cut_lost(p, kFetchWarp, it, &u);
         const float *sa[kBM / 32], *sb[BCOL ? BN / 32 : 1];
 #pragma unroll
         for (int i = 0; i < kBM / 32; ++i)
@@ -416,7 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           }
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sfull0 + 8 * slot) : "memory");
         }
+        if (go && at_lost(p, kFetchWarp, it)) go = give_up(stop);
       }
+      issued[2] = it;
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncwarp();
@@ -535,6 +558,18 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   }
   tc_fence_before();
   __syncthreads();
+  // A wait ran out, of whichever warp: those that issued copies or products may have
+  // left their loops in good order, with some in flight that no one has waited for.
+  // They land before TMEM is freed and the block ends.
+  if (*stop) {  // the same for the block: written before the barrier only
+    const unsigned n = warp < kScaleWarps + 3 && warp >= kScaleWarps ? issued[warp - kScaleWarps] : 0;
+    if (warp == kTmaWarp)
+      for (unsigned j = n - min(n, (unsigned)C::kStages); j < n; ++j) mbar_drain(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1);
+    if (warp == kMmaWarp && n > 0) mbar_drain(done0 + 8 * ((n - 1) % C::kStages), ((n - 1) / C::kStages) & 1);
+    if (warp == kFetchWarp)
+      for (unsigned j = n - min(n, (unsigned)kAhead); j < n; ++j) mbar_drain(sfull0 + 8 * (j % kAhead), (j / kAhead) & 1);
+    __syncthreads();
+  }
   if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN));
@@ -698,6 +733,9 @@ __global__ void __launch_bounds__(256) bias_kernel(const __grid_constant__ Matmu
 
 // ------------------------------------------------------------------ host side
 
+std::atomic<int> g_lost_warp{-1};  // emb_debug_lose_op_wait
+std::atomic<unsigned> g_lost_step{0};
+
 struct Plan {
   int bn = 0;             // 0: row kernel
   int m_tiles = 0, n_tiles = 0, k_blocks = 0;
@@ -854,7 +892,7 @@ extern "C" emb_status emb_fp8_matmul(const void* a_d, int64_t lda, const float* 
   const MatmulArgs p{(const unsigned char*)a_d, (const unsigned char*)b_d, sa_d, sb_d, bias_d, out_d, (float*)workspace_d,
                      lda, ldb, ldo, as ? (m + 127) / 128 : m, bs ? (n + 127) / 128 : n, (int)m, (int)n, (int)k, as, bs,
                      pl.m_tiles, pl.n_tiles, pl.k_blocks, (long long)pl.m_tiles * pl.n_tiles * pl.k_blocks, pl.per_cta,
-                     aligned_to(out_d, 32) && (ldo * ob) % 32 == 0};
+                     aligned_to(out_d, 32) && (ldo * ob) % 32 == 0, g_lost_warp.load(), g_lost_step.load()};
   CUtensorMap ma{}, mb{};
   if (pl.bn && (!make_map(&ma, a_d, m, k, lda, kBM) || !make_map(&mb, b_d, n, k, ldb, pl.bn)))
     return fail(EMB_ERR_CUDA, "cuTensorMapEncodeTiled failed or is not available");
@@ -864,6 +902,14 @@ extern "C" emb_status emb_fp8_matmul(const void* a_d, int64_t lda, const float* 
   else if (out_t == EMB_T_BF16) e = launch<__nv_bfloat16>(p, pl, ma, mb, st);
   else e = launch<__half>(p, pl, ma, mb, st);
   if (e != cudaSuccess) return cuda_fail(e, "emb_fp8_matmul launch");
+  return EMB_OK;
+}
+
+extern "C" emb_status emb_debug_lose_op_wait(int32_t role, int64_t step) {
+  if (role < -1 || role > 3 || step < 0 || step > 0x7fffffffLL) return fail(EMB_ERR_INVALID_ARG, "role must be -1 to 3, step 0 to 2^31 - 1");
+  const int warps[4] = {kTmaWarp, kMmaWarp, kFetchWarp, kAfterLoads};
+  g_lost_step.store((unsigned)step);
+  g_lost_warp.store(role < 0 ? -1 : warps[role]);
   return EMB_OK;
 }
 

@@ -153,3 +153,11 @@ def test_constants_match_the_header():
     text = open(E.HEADER).read()
     for name in ("EMB_FLAG_OP_TIMEOUT", "EMB_FP8_BLOCK", "EMB_ADAM_BLOCK", "EMB_NORM_MAX_DIM"):
         assert int(re.search(rf"^#define {name}\s+(\d+)", text, re.M).group(1)) == getattr(E, name)
+
+
+def test_lost_waits_are_refused_out_of_range():
+    for role, step in ((-2, 0), (4, 0), (0, -1), (0, 1 << 31)):
+        refused(E.lib().emb_debug_lose_op_wait(role, step))
+    with pytest.raises(ValueError):
+        E.emb_debug_lose_op_wait("store")
+    E.emb_debug_lose_op_wait(None)

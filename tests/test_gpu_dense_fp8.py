@@ -212,3 +212,34 @@ def test_quantize_scale_beside_runs_of_non_finite_values(run, block_rows, dtype)
         assert torch.equal(bits(got), bits(rq))
     q1, s1 = E.emb_fp8_quantize(x.cuda(), block_rows=block_rows)
     assert torch.equal(bits(q1), bits(q)) and torch.equal(s1, s)
+
+
+@pytest.mark.parametrize("b_rows", [1, 128])
+@pytest.mark.parametrize("m,n,k", [(300, 512, 5120), (5000, 1100, 640), (20_011, 400, 300), (40_003, 40, 300)])
+def test_a_wait_that_runs_out(m, n, k, b_rows):
+    """Each warp that issues work loses its wait at the first step, while the ring of
+    stages fills, and later, or the block is told to stop when the last loads are on
+    their way: the product ends, raises its flag once, and leaves the GPU fit for the
+    next product, which is right."""
+    a, sa, b, sb = operands(m, n, k, 1, b_rows, seed=9)
+    want = E.emb_fp8_matmul(a, sa, b, sb)
+    check(want, a, sa, b, sb)
+    steps = -(-k // 128)
+    try:
+        for role in ("load", "product", "scales", "other"):
+            for step in (0, 1, 2, min(steps - 1, 6)):
+                E.emb_debug_lose_op_wait(role, step)
+                E.emb_fp8_matmul(a, sa, b, sb)
+                E.emb_debug_lose_op_wait(None)
+                assert E.emb_check_op_flag() == E.EMB_FLAG_OP_TIMEOUT, (role, step)
+                assert E.emb_check_op_flag() == 0
+                assert torch.equal(E.emb_fp8_matmul(a, sa, b, sb), want), (role, step)
+                assert E.emb_check_op_flag() == 0
+    finally:
+        E.emb_debug_lose_op_wait(None)
+    one = E.emb_fp8_matmul(a[:1], sa[:, :1].contiguous(), b, sb)
+    E.emb_debug_lose_op_wait("load", 0)       # a single row waits for nothing
+    try:
+        assert torch.equal(E.emb_fp8_matmul(a[:1], sa[:, :1].contiguous(), b, sb), one) and E.emb_check_op_flag() == 0
+    finally:
+        E.emb_debug_lose_op_wait(None)
