@@ -587,16 +587,34 @@ class Pipeline:
 #
 # These run as often as a layer does, some for microseconds: one condition per
 # tensor finds the usual case, and only a call that fails it is looked at again
-# for its message.  The current stream is read as its raw handle.
+# for its message.  The current stream is read as its raw handle.  A kernel runs
+# on the current device, so every tensor of a call has to be there.
 
 _F8, _F32, _U8 = torch.float8_e4m3fn, torch.float32, torch.uint8
 _new = torch.empty
 
 
-def _raw_stream(stream) -> int:
+_current_device = torch._C._cuda_getDevice
+
+
+def _launch_device(t: torch.Tensor, name: str) -> int:
+    """The current device, which has to be this tensor's."""
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != _current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return dev
+
+
+def _raw_stream(stream, dev: Optional[int] = None) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        return torch._C._cuda_getCurrentRawStream(_current_device() if dev is None else dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        return int(stream)
+    if dev is not None and stream.device_index != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors are on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _empty(stream, like: torch.Tensor, shape, dtype) -> torch.Tensor:
@@ -608,14 +626,16 @@ def _empty(stream, like: torch.Tensor, shape, dtype) -> torch.Tensor:
         return _new(shape, dtype=dtype, device=like.device)
 
 
-def _dense(t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
-    """The address of a contiguous CUDA tensor of this type."""
+def _dense(t: Optional[torch.Tensor], dtype, name: str, dev: int) -> Optional[int]:
+    """The address of a contiguous tensor of this type on the launch's device."""
     if t is None:
         return None
-    if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.is_cuda and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the others are on cuda:{dev}")
     raise ValueError(f"{name} must be a contiguous CUDA tensor")
 
 
@@ -626,10 +646,10 @@ def _ftype(dtype, name: str) -> int:
     return code
 
 
-def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Checks a CUDA matrix with neighbouring columns; returns the distance of its rows."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _row_stride(t: torch.Tensor, name: str, dev: int) -> int:
+    """Checks a matrix with neighbouring columns on the launch's device; returns the distance of its rows."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix")
     (rows, cols), (ld, step) = t.shape, t.stride()
@@ -638,10 +658,10 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     return ld if rows > 1 else max(ld, cols)
 
 
-def _code_stride(t: torch.Tensor, name: str) -> int:
+def _code_stride(t: torch.Tensor, name: str, dev: int) -> int:
     if t.dtype is not _F8:
         raise TypeError(f"{name} must be {_F8}, got {t.dtype}")
-    ld = _row_stride(t, name)
+    ld = _row_stride(t, name, dev)
     return -(-ld // 16) * 16 if ld % 16 and (t.shape[0] <= 1 or t.shape[1] == 0) else ld
 
 
@@ -650,7 +670,8 @@ def emb_fp8_quantize(x: torch.Tensor, block_rows: int = 1, transpose: bool = Fal
     may be strided): (q, s), with q[rows, cols] and s[ceil(cols/128),
     ceil(rows/block_rows)]; with transpose=True (q, s, qt, st), the codes of
     x.T in blocks along x's rows as well, from the same pass."""
-    ldx = _row_stride(x, "x")
+    dev = _launch_device(x, "x")
+    ldx = _row_stride(x, "x", dev)
     if block_rows not in (1, EMB_FP8_BLOCK):
         raise ValueError("block_rows must be 1 or 128")
     r, c = x.shape
@@ -659,11 +680,11 @@ def emb_fp8_quantize(x: torch.Tensor, block_rows: int = 1, transpose: bool = Fal
     q, s = _empty(stream, x, (r, ldq), _F8), _empty(stream, x, (cb, rows), _F32)
     if not transpose:
         _check(lib().emb_fp8_quantize(x.data_ptr(), _ftype(x.dtype, "x"), r, c, ldx, block_rows, q.data_ptr(), ldq, s.data_ptr(),
-                                      None, 0, None, _raw_stream(stream)))
+                                      None, 0, None, _raw_stream(stream, dev)))
         return (q if ldq == c else q[:, :c]), s
     qt, st = _empty(stream, x, (c, ldqt), _F8), _empty(stream, x, (rb, cols), _F32)
     _check(lib().emb_fp8_quantize(x.data_ptr(), _ftype(x.dtype, "x"), r, c, ldx, block_rows, q.data_ptr(), ldq, s.data_ptr(),
-                                  qt.data_ptr(), ldqt, st.data_ptr(), _raw_stream(stream)))
+                                  qt.data_ptr(), ldqt, st.data_ptr(), _raw_stream(stream, dev)))
     return (q if ldq == c else q[:, :c]), s, (qt if ldqt == r else qt[:, :r]), st
 
 
@@ -689,7 +710,8 @@ def emb_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
     """a[m, k] @ b[n, k].T of codes and scales from emb_fp8_quantize (+ bias[n]).
     workspace: emb_fp8_matmul_workspace_size bytes that the caller keeps; made
     for the call if None."""
-    lda, ldb = _code_stride(a, "a"), _code_stride(b, "b")
+    dev = _launch_device(a, "a")
+    lda, ldb = _code_stride(a, "a", dev), _code_stride(b, "b", dev)
     (m, k), (n, kb) = a.shape, b.shape
     if kb != k:
         raise ValueError(f"a and b must have the same columns, got {k} and {kb}")
@@ -702,20 +724,20 @@ def emb_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
     else:
         if out.shape != (m, n):
             raise ValueError(f"out must be [{m}, {n}]")
-        ldo = _row_stride(out, "out")
+        ldo = _row_stride(out, "out", dev)
     wp, ws_bytes = None, 0
     if workspace is None:
         ws_bytes = emb_fp8_matmul_workspace_size(m, n, k)
         if ws_bytes:
             workspace = _empty(stream, a, ws_bytes, _U8)
             wp = workspace.data_ptr()
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
     else:
         wp, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    _check(lib().emb_fp8_matmul(a.data_ptr(), lda, _dense(sa, _F32, "sa"), a_rows, b.data_ptr(), ldb, _dense(sb, _F32, "sb"),
-                                b_rows, m, n, k, None if bias is None else _dense(bias, _F32, "bias"), out.data_ptr(),
-                                _ftype(out.dtype, "out"), ldo, wp, ws_bytes, _raw_stream(stream)))
+    _check(lib().emb_fp8_matmul(a.data_ptr(), lda, _dense(sa, _F32, "sa", dev), a_rows, b.data_ptr(), ldb, _dense(sb, _F32, "sb", dev),
+                                b_rows, m, n, k, None if bias is None else _dense(bias, _F32, "bias", dev),
+                                out.data_ptr(), _ftype(out.dtype, "out"), ldo, wp, ws_bytes, _raw_stream(stream, dev)))
     return out
 
 
@@ -736,20 +758,20 @@ def _norm_gate(x: torch.Tensor, block_dtype: torch.dtype, gate, norm: str, act: 
     return _NormGate(r, d, _ftype(x.dtype, "x"), _ftype(block_dtype, "f"), _NORM[norm], kind, _ACT[act], eps, res_scale)
 
 
-def _vector(t: Optional[torch.Tensor], dim: int, name: str):
+def _vector(t: Optional[torch.Tensor], dim: int, name: str, dev: int):
     if t is None:
         return None
     if t.numel() != dim:
         raise ValueError(f"{name} must have {dim} elements")
-    return _dense(t, _F32, name)
+    return _dense(t, _F32, name, dev)
 
 
-def _same(t: Optional[torch.Tensor], shape, dtype, name: str):
+def _same(t: Optional[torch.Tensor], shape, dtype, name: str, dev: int):
     if t is None:
         return None
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    return _dense(t, dtype, name)
+    return _dense(t, dtype, name, dev)
 
 
 def emb_norm_gate_fwd(x: torch.Tensor, f: Optional[torch.Tensor], gate: Optional[torch.Tensor] = None, *,
@@ -766,11 +788,13 @@ def emb_norm_gate_fwd(x: torch.Tensor, f: Optional[torch.Tensor], gate: Optional
     block_dtype = f.dtype if f is not None else block_dtype or st_type
     d = _norm_gate(x, block_dtype, gate, norm, act, eps, res_scale)
     dim = d.dim
-    xp, fp, gp = _dense(x, st_type, "x"), _same(f, shape, block_dtype, "f"), None if gate is None else _dense(gate, gate.dtype, "gate")
-    wp = None if w_post is None else _vector(w_post, dim, "w_post")
-    bp = None if b_post is None else _vector(b_post, dim, "b_post")
-    wq = None if w_pre is None else _vector(w_pre, dim, "w_pre")
-    bq = None if b_pre is None else _vector(b_pre, dim, "b_pre")
+    dev = _launch_device(x, "x")
+    xp, fp = _dense(x, st_type, "x", dev), _same(f, shape, block_dtype, "f", dev)
+    gp = None if gate is None else _dense(gate, gate.dtype, "gate", dev)
+    wp = None if w_post is None else _vector(w_post, dim, "w_post", dev)
+    bp = None if b_post is None else _vector(b_post, dim, "b_post", dev)
+    wq = None if w_pre is None else _vector(w_pre, dim, "w_pre", dev)
+    bq = None if b_pre is None else _vector(b_pre, dim, "b_pre", dev)
     y = h = st = yp = hp = sp = None
     if f is not None:
         y = _empty(stream, x, shape, st_type)
@@ -781,7 +805,7 @@ def emb_norm_gate_fwd(x: torch.Tensor, f: Optional[torch.Tensor], gate: Optional
     if stats:
         st = _empty(stream, x, (shape[0], 4), _F32)
         sp = st.data_ptr()
-    _check(lib().emb_norm_gate_fwd(ctypes.byref(d), xp, fp, gp, wp, bp, wq, bq, yp, hp, sp, _raw_stream(stream)))
+    _check(lib().emb_norm_gate_fwd(ctypes.byref(d), xp, fp, gp, wp, bp, wq, bq, yp, hp, sp, _raw_stream(stream, dev)))
     return y, h, st
 
 
@@ -809,29 +833,31 @@ def emb_norm_gate_bwd(dy: Optional[torch.Tensor], dh: Optional[torch.Tensor], y:
     d = _norm_gate(y, bt, gate, norm, act, eps, res_scale)
     r, dim = shape
     f32 = _F32
-    ins = (_same(dy, shape, st_type, "dy"), _same(dh, shape, bt, "dh"), _dense(y, st_type, "y"), _same(f, shape, bt, "f"),
-           None if gate is None else _dense(gate, gate.dtype, "gate"), _same(stats, (r, 4), f32, "stats"),
-           _vector(w_post, dim, "w_post"), _vector(b_post, dim, "b_post"), _vector(w_pre, dim, "w_pre"))
-    _vector(b_pre, dim, "b_pre")
+    dev = _launch_device(y, "y")
+    ins = (_same(dy, shape, st_type, "dy", dev), _same(dh, shape, bt, "dh", dev), _dense(y, st_type, "y", dev),
+           _same(f, shape, bt, "f", dev), None if gate is None else _dense(gate, gate.dtype, "gate", dev),
+           _same(stats, (r, 4), f32, "stats", dev), _vector(w_post, dim, "w_post", dev), _vector(b_post, dim, "b_post", dev),
+           _vector(w_pre, dim, "w_pre", dev))
+    _vector(b_pre, dim, "b_pre", dev)
     out = {"dx": _empty(stream, y, shape, st_type), "df": None if f is None else _empty(stream, y, shape, bt),
            "dgate": None if gate is None else _empty(stream, y, gate.shape, gate.dtype)}
     for name, v in (("dw_post", w_post), ("db_post", b_post), ("dw_pre", w_pre), ("db_pre", b_pre)):
         out[name] = None if v is None else _empty(stream, y, (dim,), f32)
     if workspace is None:
         workspace = _empty(stream, y, emb_norm_gate_bwd_workspace_size(r, dim), torch.uint8)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
     _check(lib().emb_norm_gate_bwd(ctypes.byref(d), *ins, *[None if v is None else v.data_ptr() for v in out.values()],
-                                   workspace.data_ptr(), workspace.nbytes, _raw_stream(stream)))
+                                   workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev)))
     return out
 
 
-def emb_adamw_step(tensors, grads, params: _AdamwParams, stream=None) -> None:
+def emb_adamw_step(tensors, grads, params: _AdamwParams, stream=None, dev: Optional[int] = None) -> None:
     """One step over a ctypes array of _AdamwTensor and the address of an array of gradient pointers (AdamW makes both)."""
-    _check(lib().emb_adamw_step(tensors, grads, len(tensors), ctypes.byref(params), _raw_stream(stream)))
+    _check(lib().emb_adamw_step(tensors, grads, len(tensors), ctypes.byref(params), _raw_stream(stream, dev)))
 
 
-_dtype_of, _on_cuda = operator.attrgetter("dtype"), operator.attrgetter("is_cuda")
+_dtype_of = operator.attrgetter("dtype")
 
 
 class AdamW:
@@ -862,6 +888,10 @@ class AdamW:
         q8 = self._state == 1
         block = EMB_ADAM_BLOCK
         self._n = [p.numel() for p in self.params]
+        self._dev = self.params[0].get_device()
+        if self._dev < 0:
+            raise ValueError("param must be a contiguous CUDA tensor")
+        self._devs = [self._dev] * len(self.params)
         self._at = [0]
         for n in self._n:
             self._at.append(self._at[-1] + -(-n // block) * block)
@@ -887,22 +917,20 @@ class AdamW:
         q8, block = self._state == 1, EMB_ADAM_BLOCK
         base, size = {}, {"m": self._total, "v": self._total, "m_scale": self._total // block, "v_scale": self._total // block}
         for k, v in self.arena.items():
-            if (v is None) != (k.endswith("scale") and not q8) or (v is not None and (v.numel() != size[k] or v.device != self.device)):
+            if (v is None) != (k.endswith("scale") and not q8) or (v is not None and v.numel() != size[k]):
                 raise ValueError(f"arena {k} does not match the state kind {self.state} and {self._total} elements")
-            base[k] = 0 if v is None else _dense(v, torch.float32 if k.endswith("scale") else self._state_type, f"arena {k}")
+            base[k] = 0 if v is None else _dense(v, torch.float32 if k.endswith("scale") else self._state_type, f"arena {k}", self._dev)
         if len(self.params) != len(self._n):
             raise ValueError("the number of parameters has changed")
         tensors = (_AdamwTensor * len(self.params))()
         st = self._state_type.itemsize
         for i, (p, c) in enumerate(zip(self.params, self._copies)):
-            if p.device != self.device:
-                raise ValueError("parameters must be on one device")
             if p.numel() != self._n[i]:
                 raise ValueError(f"parameter {i} had {self._n[i]} elements and has {p.numel()}")
             if c is not None and c.numel() != p.numel():
                 raise ValueError("a copy must have its parameter's size")
             at = self._at[i]
-            tensors[i] = _AdamwTensor(_dense(p, p.dtype, "param"), None if c is None else _dense(c, c.dtype, "copy"),
+            tensors[i] = _AdamwTensor(_dense(p, p.dtype, "param", self._dev), None if c is None else _dense(c, c.dtype, "copy", self._dev),
                                       base["m"] + at * st, base["v"] + at * st,
                                       base["m_scale"] + at // block * 4 if q8 else None,
                                       base["v_scale"] + at // block * 4 if q8 else None, self._n[i], at,
@@ -941,8 +969,10 @@ class AdamW:
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients are needed, got {len(grads)}")
         T = torch.Tensor
-        if list(map(T.numel, grads)) != self._n or not all(map(T.is_contiguous, grads)) or not all(map(_on_cuda, grads)):
-            raise ValueError("each gradient must be a contiguous CUDA tensor of its parameter's size")
+        if list(map(T.numel, grads)) != self._n or not all(map(T.is_contiguous, grads)) or list(map(T.get_device, grads)) != self._devs:
+            raise ValueError(f"each gradient must be a contiguous tensor on cuda:{self._dev} of its parameter's size")
+        if _current_device() != self._dev:
+            raise ValueError(f"the parameters are on cuda:{self._dev}, the current device is cuda:{_current_device()}")
         if list(map(T.data_ptr, self._used())) != self._addresses:
             self._bind()                    # a parameter, copy or state has moved
         dtypes = list(map(_dtype_of, grads))
@@ -953,8 +983,8 @@ class AdamW:
             self._grad_dtypes = dtypes
         ptrs = array.array("Q", map(T.data_ptr, grads))
         p = _AdamwParams(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, self.step_count + 1,
-                         self._state, self.seed & 0xFFFFFFFF, _dense(grad_scale, torch.float32, "grad_scale"))
-        emb_adamw_step(self._tensors, ptrs.buffer_info()[0], p, stream)
+                         self._state, self.seed & 0xFFFFFFFF, _dense(grad_scale, torch.float32, "grad_scale", self._dev))
+        emb_adamw_step(self._tensors, ptrs.buffer_info()[0], p, stream, self._dev)
         self.step_count += 1
 
 

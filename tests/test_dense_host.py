@@ -161,3 +161,71 @@ def test_lost_waits_are_refused_out_of_range():
     with pytest.raises(ValueError):
         E.emb_debug_lose_op_wait("store")
     E.emb_debug_lose_op_wait(None)
+
+
+class OnDevice(torch.Tensor):
+    """A host tensor that says it is on GPU `where`: for the checks that come before any launch."""
+
+    @classmethod
+    def __torch_function__(cls, func, types, args=(), kwargs=None):
+        if func == torch.Tensor.get_device:
+            return args[0].where
+        if func == torch.Tensor.is_cuda.__get__:
+            return True
+        return super().__torch_function__(func, types, args, kwargs or {})
+
+
+def on(where, t):
+    t = t.as_subclass(OnDevice)
+    t.where = where
+    return t
+
+
+class NoLaunch:
+    """The library without its launches."""
+
+    def __init__(self, lib):
+        self.lib = lib
+
+    def __getattr__(self, name):
+        def launched(*args):
+            raise AssertionError(name + " was called")
+        return getattr(self.lib, name) if name.endswith("workspace_size") else launched
+
+
+F8 = torch.float8_e4m3fn
+
+
+def calls(where):
+    """Each operator with its tensors on the GPUs that `where` names (default 0)."""
+    w = lambda k, t: on(where.get(k, 0), t)  # noqa: E731
+    z = lambda *s: torch.zeros(*s)  # noqa: E731
+    vec = lambda: {k: w(k, z(6)) for k in ("w_post", "b_post", "w_pre", "b_pre")}  # noqa: E731
+    return {
+        "quantize": lambda: E.emb_fp8_quantize(w("x", z(4, 6))),
+        "matmul": lambda: E.emb_fp8_matmul(w("a", z(4, 16).to(F8)), w("sa", z(1, 4)), w("b", z(8, 16).to(F8)), w("sb", z(1, 8)), bias=w("bias", z(8)),
+                                           out=w("out", z(4, 8)), workspace=w("workspace", z(64))),
+        "fwd": lambda: E.emb_norm_gate_fwd(w("x", z(4, 6)), w("f", z(4, 6)), w("gate", z(4, 6)), norm="layer", **vec()),
+        "bwd": lambda: E.emb_norm_gate_bwd(w("dy", z(4, 6)), w("dh", z(4, 6)), w("y", z(4, 6)), w("f", z(4, 6)), w("gate", z(4, 6)),
+                                           w("stats", z(4, 4)), norm="layer", workspace=w("workspace", z(4000)), **vec()),
+    }
+
+
+@pytest.mark.parametrize("op,names", [("quantize", "x"), ("matmul", "a sa b sb bias out workspace"), ("fwd", "x f gate w_post b_post w_pre b_pre"),
+                                      ("bwd", "dy dh y f gate stats w_post b_post w_pre b_pre workspace")])
+def test_operands_on_another_device_are_refused(monkeypatch, op, names):
+    """One operand on another GPU, or all on one that is not current: refused before anything is launched."""
+    stub = NoLaunch(E.lib())
+    monkeypatch.setattr(E, "lib", lambda: stub)
+    monkeypatch.setattr(E, "_current_device", lambda: 0)
+    monkeypatch.setattr(E, "_raw_stream", lambda stream, dev=None: 0)
+    with pytest.raises(AssertionError, match="was called"):
+        calls({})[op]()                      # all on the current device: it would have been launched
+    for name in names.split():
+        with pytest.raises(ValueError, match="cuda:"):
+            calls({name: 1})[op]()
+    monkeypatch.setattr(E, "_current_device", lambda: 1)
+    with pytest.raises(ValueError, match="cuda:1"):
+        calls({})[op]()
+    with pytest.raises(AssertionError, match="was called"):
+        calls({n: 1 for n in names.split()})[op]()

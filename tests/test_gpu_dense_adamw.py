@@ -264,3 +264,45 @@ def test_parameters_that_change_size_or_lose_their_storage_are_refused():
     assert opt.step_count == 0 and bool((p[0] == 0).all())
     opt.step(grads)
     assert bool((p[0] < 0).all()) and bool((p[1] < 0).all())
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on GPU 1."""
+
+    @classmethod
+    def __torch_function__(cls, func, types, args=(), kwargs=None):
+        if func == torch.Tensor.get_device:
+            return 1
+        return super().__torch_function__(func, types, args, kwargs or {})
+
+
+def test_tensors_on_another_device_are_refused(monkeypatch):
+    """A gradient, its scale, a copy or a parameter on another GPU, or another GPU current: nothing is launched."""
+    away = lambda t: t.as_subclass(Elsewhere)  # noqa: E731
+    z = lambda n, **kw: torch.zeros(n, device="cuda", **kw)  # noqa: E731
+    opt = E.AdamW([z(300), z(7)])
+
+    def launched(*a):
+        raise AssertionError("launched")
+
+    monkeypatch.setattr(E, "emb_adamw_step", launched)
+    for bad in ([z(300), away(z(7))], [away(z(300)), away(z(7))]):
+        with pytest.raises(ValueError, match="cuda:0"):
+            opt.step(bad)
+    with pytest.raises(ValueError, match="cuda:0"):
+        opt.step([z(300), z(7)], grad_scale=away(z(1)))
+    with pytest.raises(ValueError, match="cuda:0"):
+        E.AdamW([z(300), away(z(7))])
+    with pytest.raises(ValueError, match="cuda:0"):
+        E.AdamW([z(300)], copies=[away(z(300, dtype=BF16))])
+    monkeypatch.setattr(E, "_current_device", lambda: 1)
+    with pytest.raises(ValueError, match="cuda:1"):
+        opt.step([z(300), z(7)])
+    monkeypatch.undo()
+    with pytest.raises(ValueError, match="stream"):
+        monkeypatch.setattr(torch.cuda.Stream, "device_index", property(lambda self: 1), raising=False)
+        opt.step([z(300), z(7)], stream=torch.cuda.Stream())
+    monkeypatch.undo()
+    assert opt.step_count == 0
+    opt.step([z(300), z(7)], stream=torch.cuda.Stream())
+    assert opt.step_count == 1
