@@ -902,12 +902,15 @@ class AdamW:
                       "m_scale": zeros(total // block, torch.float32) if q8 else None,
                       "v_scale": zeros(total // block, torch.float32) if q8 else None}
         self._total, self._state_type = total, st
+        self._params = self._hyper = None
+        self._given = [c for c in self._copies if c is not None]
+        self._states = [k for k, v in self.arena.items() if v is not None]
         self._grad_dtypes = [p.dtype for p in self.params]
         self._bind()
 
     def _used(self):
         """Every tensor whose address a step uses, the gradients apart."""
-        return self.params + [c for c in self._copies if c is not None] + [v for v in self.arena.values() if v is not None]
+        return [*self.params, *self._given, *map(self.arena.__getitem__, self._states)]
 
     def _bind(self) -> None:
         """Describes parameters, copies and states to the library, as they are now.  The
@@ -982,8 +985,13 @@ class AdamW:
                 t.grad_t = kind
             self._grad_dtypes = dtypes
         ptrs = array.array("Q", map(T.data_ptr, grads))
-        p = _AdamwParams(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, self.step_count + 1,
-                         self._state, self.seed & 0xFFFFFFFF, _dense(grad_scale, torch.float32, "grad_scale", self._dev))
+        hyper = (self.lr, *self.betas, self.eps, self.weight_decay, self.seed)
+        if hyper != self._hyper:
+            self._params = _AdamwParams(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, 0, self._state,
+                                        self.seed & 0xFFFFFFFF, None)
+            self._hyper = hyper
+        p = self._params
+        p.step, p.grad_scale = self.step_count + 1, _dense(grad_scale, _F32, "grad_scale", self._dev)
         emb_adamw_step(self._tensors, ptrs.buffer_info()[0], p, stream, self._dev)
         self.step_count += 1
 
