@@ -586,6 +586,9 @@ EMB_API emb_status emb_fp8_matmul(const void* a_d, int64_t lda, const float* sa_
  *            of a norm that is absent are 0); the backward reads them.  May be
  *            NULL (serving).
  * Arrays are contiguous; all arithmetic is float32, each output rounded once.
+ * The sigmoid is good to 12 * 2^-24 of itself where x and y are float32 or the gate
+ * is per channel (in the backward: where the gate is float32), else to 6 * 2^-24 of
+ * 1; below 2^-126 it is 0.
  */
 typedef enum { EMB_NORM_RMS = 0, EMB_NORM_LAYER = 1 } emb_norm;
 typedef enum { EMB_GATE_NONE = 0, EMB_GATE_ELEM = 1, EMB_GATE_ROW = 2, EMB_GATE_COL = 3 } emb_gate;

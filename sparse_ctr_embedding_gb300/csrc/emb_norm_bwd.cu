@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kerne
   // spill (32,768 x 2048: 339 us without, 405 with).
   constexpr bool kPre = MAXT < 1024 && !(VEC && LAYER);
   constexpr bool kHold = MAXT < 1024;  // registers enough to keep the sums over the rows
+  constexpr bool kFine = sizeof(BT) == 4;  // float32 gradients of the block and its gate: see activate()
   constexpr int E = norm_elems<VEC, MAXT>();
   extern __shared__ float dyn[];
   __shared__ float2 slots[4][64];
@@ -178,13 +179,13 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kerne
     }
     if (gate_elem) {
 #pragma unroll
-      for (int k = 0; k < E; ++k) g[k] = activate(g[k], act);
+      for (int k = 0; k < E; ++k) g[k] = activate<kFine>(g[k], act);
     } else if (gate_col) {
       gc.get(g);
 #pragma unroll
-      for (int k = 0; k < E; ++k) g[k] = activate(g[k], act);
+      for (int k = 0; k < E; ++k) g[k] = activate<true>(g[k], act);
     } else {
-      const float v = gate_kind == EMB_GATE_ROW ? activate(gr, act) : 1.0f;
+      const float v = gate_kind == EMB_GATE_ROW ? activate<kFine>(gr, act) : 1.0f;
 #pragma unroll
       for (int k = 0; k < E; ++k) g[k] = v;
     }

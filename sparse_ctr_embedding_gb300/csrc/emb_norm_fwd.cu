@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kerne
   // stream: 78 us, 96 without), where registers allow.
   constexpr bool kPre = MAXT < 1024;
   constexpr bool kHold = MAXT < 1024;  // registers enough to keep the vectors over the rows
+  constexpr bool kFine = sizeof(ST) == 4;  // float32 rows: see activate()
   constexpr int E = norm_elems<VEC, MAXT>();
   const int team = a.team, dim = a.dim;
   const int my_team = threadIdx.x / team;
@@ -55,6 +56,10 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kerne
   VecPart<VEC, kHold, E, FULL> wp(a.w_post, 1.0f, t, team, dim), wq(a.w_pre, 1.0f, t, team, dim);
   VecPart<VEC, kHold, E, FULL && LAYER> bp(LAYER ? a.b_post : nullptr, 0.0f, t, team, dim), bq(LAYER ? a.b_pre : nullptr, 0.0f, t, team, dim);
   VecPart<VEC, kHold, E, false> gc(gate_col, 0.0f, t, team, dim);
+  if (kHold && gate_col) {  // once, not for each row
+#pragma unroll
+    for (int k = 0; k < E; ++k) gc.v[kHold ? k : 0] = activate<true>(gc.v[kHold ? k : 0], act);
+  }
 
   RowPart<ST, VEC, E> rx;
   RowPart<BT, VEC, E> rf, rg;
@@ -108,13 +113,15 @@ __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kerne
     if (has_f) {
       if (gate_elem) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) g[k] = activate(g[k], act);
+        for (int k = 0; k < E; ++k) g[k] = activate<kFine>(g[k], act);
       } else if (gate_col) {
         gc.get(g);
+        if (!kHold) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) g[k] = activate(g[k], act);
+          for (int k = 0; k < E; ++k) g[k] = activate<true>(g[k], act);
+        }
       } else {
-        const float v = gate_kind == EMB_GATE_ROW ? activate(gr, act) : 1.0f;
+        const float v = gate_kind == EMB_GATE_ROW ? activate<kFine>(gr, act) : 1.0f;
 #pragma unroll
         for (int k = 0; k < E; ++k) g[k] = v;
       }

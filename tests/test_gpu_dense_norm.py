@@ -277,3 +277,56 @@ def test_unaligned_views_and_another_stream():
     g2 = E.emb_norm_gate_bwd(d["dy"].cuda(), d["dh"].cuda(), y, f, c["gate"], st, w_post=c["w_post"], w_pre=c["w_pre"], eps=1e-5)
     check_bwd(d, y, g1, False, "sigmoid", 1.0)
     check_bwd(d, y, g2, False, "sigmoid", 1.0)
+
+
+@pytest.mark.parametrize("st,bt", [(F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("kind", ["elem", "row", "col"])
+@pytest.mark.parametrize("dim,full", [(64, False), (64, True), (4, False), (8192, False)])
+def test_sigmoid_of_float32_rows(st, bt, kind, dim, full):
+    """With x = 0 and f = 1 (whose norm is exactly 1 here) y is the sigmoid itself.
+    Where rows are float32 it is good to 12 u over the whole range of gates: the
+    power of two 4 u, its correction, the sum and y's product 1 u each, the
+    reciprocal 2 u.  The gate's gradient a (1 - a) has a's error twice, and for
+    a near 1 what 1 - a cancels."""
+    g = torch.Generator().manual_seed(dim)
+    top = 87.0                       # below, the sigmoid leaves the normal range
+    gates = torch.cat([torch.linspace(-top, top, 700), torch.randn(300, generator=g) * 4, torch.tensor([0.0, -0.0, top, -top])])
+    gates = gates.to(bt)
+    if kind == "col":
+        gate = gates.float()[torch.arange(dim) % gates.numel()]
+        rows, all_gates = 3, gate.expand(3, dim)
+    else:
+        rows = gates.numel()
+        gate = gates[:, None] if kind == "row" else gates[(torch.arange(rows)[:, None] + torch.arange(dim)) % rows]
+        all_gates = gate.expand(rows, dim)
+    x, f, one = torch.zeros(rows, dim, dtype=st).cuda(), torch.ones(rows, dim, dtype=bt).cuda(), torch.ones(dim).cuda()
+    kw = dict(w_post=one, w_pre=one, eps=1e-30) if full else dict(w_post=one, eps=1e-30, pre=False)
+    y, h, stats = E.emb_norm_gate_fwd(x, f, gate.cuda(), **kw)
+    assert bool((stats[:, 1] == 1).all())
+    a = 1 / (1 + torch.exp(-all_gates.double()))
+    err = (y.cpu().double() - a).abs()
+    assert bool((err <= 12 * U * a + 2.0 ** -126).all()), float((err / a).max() / U)
+    if bt != F32 and kind != "col":
+        return                        # the gradient is rounded to the gate's type
+    dy = torch.zeros(rows, dim)       # one row at a time in the sums over rows, one column in those over columns
+    dy[torch.arange(rows), torch.arange(rows) % dim] = 1.0
+    got = E.emb_norm_gate_bwd(dy.cuda(), None, y, f, gate.cuda(), stats, w_post=one, eps=1e-30)["dgate"].cpu().double()
+    slope = torch.where(dy != 0, a * (1 - a), torch.zeros_like(a))
+    want = slope.sum(1, keepdim=True) if kind == "row" else slope.sum(0) if kind == "col" else slope
+    of = torch.where(dy != 0, a, torch.zeros_like(a))
+    size = of.sum(1, keepdim=True) if kind == "row" else of.sum(0) if kind == "col" else of
+    err = (got.reshape(want.shape) - want).abs()
+    assert bool((err <= 12 * U * want + 5 * U * size + 2.0 ** -126).all())
+
+
+@pytest.mark.parametrize("st,bt", [(F32, F32), (F32, F16), (BF16, BF16)])
+def test_sigmoid_of_gates_out_of_range(st, bt):
+    """Gates of any size and NaN: 0, 1 or NaN, nothing else in the row touched."""
+    gate = torch.zeros(7, 64, dtype=bt)
+    values = torch.tensor([200.0, -200.0, 65504.0, -65504.0, float("inf"), -float("inf"), float("nan")]).to(bt)
+    gate[:, 5] = values
+    x, f, one = torch.zeros(7, 64, dtype=st).cuda(), torch.ones(7, 64, dtype=bt).cuda(), torch.ones(64).cuda()
+    y = E.emb_norm_gate_fwd(x, f, gate.cuda(), w_post=one, eps=1e-30, pre=False)[0].cpu().float()
+    assert y[:6, 5].tolist() == [1.0, 0.0, 1.0, 0.0, 1.0, 0.0] and bool(torch.isnan(y[6, 5]))
+    y[:, 5] = 0.5
+    assert bool((y == 0.5).all())
