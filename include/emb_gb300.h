@@ -672,8 +672,10 @@ EMB_API emb_status emb_adamw_step(const emb_adamw_tensor* tensors, const void* c
                                   const emb_adamw_params* params, void* stream);
 
 /*
- * emb_check_op_flag -- synchronise `stream`, read and clear the flag word of
- * the dense operators on the current device.  EMB_ERR_DEVICE_FLAG if a bit was
+ * emb_check_op_flag -- read and clear the flag word of the dense operators on the
+ * current device, in one step after the work before it on `stream`, and synchronise
+ * `stream`.  A bit that work of another stream raises meanwhile is reported by this
+ * check or the next.  EMB_ERR_DEVICE_FLAG if a bit was
  * set since the last check: EMB_FLAG_OP_TIMEOUT, a kernel's bounded wait ran
  * out and its output is not valid.
  */

@@ -38,13 +38,15 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <mutex>
 
 #include "emb_dense.cuh"
 
 namespace emb {
 namespace {
 
-__device__ unsigned g_op_flags;  // EMB_FLAG_OP_* bits since the last emb_check_op_flag
+__device__ unsigned g_op_flags;   // EMB_FLAG_OP_* bits since the last emb_check_op_flag
+__device__ unsigned g_op_taken;   // what the last check read
 
 constexpr int kBM = 128;             // rows of a tile
 constexpr int kBK = EMB_FP8_BLOCK;   // k's of a step: one scale block, 128 bytes of a row
@@ -731,6 +733,9 @@ __global__ void __launch_bounds__(256) bias_kernel(const __grid_constant__ Matmu
   }
 }
 
+// Reads and clears the flag word in one step: a kernel of another stream may raise a bit at any time.
+__global__ void take_flags_kernel() { g_op_taken = atomicExch(&g_op_flags, 0u); }
+
 // ------------------------------------------------------------------ host side
 
 std::atomic<int> g_lost_warp{-1};  // emb_debug_lose_op_wait
@@ -914,11 +919,14 @@ extern "C" emb_status emb_debug_lose_op_wait(int32_t role, int64_t step) {
 }
 
 extern "C" emb_status emb_check_op_flag(void* stream, uint32_t* flags_out) {
-  EMB_CUDA(cudaStreamSynchronize((cudaStream_t)stream));
+  static std::mutex one_check;  // g_op_taken holds one check's bits at a time
+  const std::lock_guard<std::mutex> hold(one_check);
+  cudaStream_t st = (cudaStream_t)stream;
   unsigned f = 0;
-  const unsigned zero = 0;
-  EMB_CUDA(cudaMemcpyFromSymbol(&f, g_op_flags, sizeof f));
-  if (f) EMB_CUDA(cudaMemcpyToSymbol(g_op_flags, &zero, sizeof zero));
+  take_flags_kernel<<<1, 1, 0, st>>>();
+  EMB_CUDA(cudaGetLastError());
+  EMB_CUDA(cudaMemcpyFromSymbolAsync(&f, g_op_taken, sizeof f, 0, cudaMemcpyDeviceToHost, st));
+  EMB_CUDA(cudaStreamSynchronize(st));
   if (flags_out) *flags_out = f;
   if (f) return fail(EMB_ERR_DEVICE_FLAG, "a dense operator's bounded wait ran out: its output is not valid");
   return EMB_OK;

@@ -243,3 +243,31 @@ def test_a_wait_that_runs_out(m, n, k, b_rows):
         assert torch.equal(E.emb_fp8_matmul(a[:1], sa[:, :1].contiguous(), b, sb), one) and E.emb_check_op_flag() == 0
     finally:
         E.emb_debug_lose_op_wait(None)
+
+
+def test_flag_of_another_stream_is_reported_once():
+    """Products that give up on a side stream while checks run on this one: each of
+    them is reported, by a check beside it or by the one after it."""
+    a, sa, b, sb = operands(300, 512, 1024, 1, 128, seed=11)
+    E.emb_fp8_matmul(a, sa, b, sb)
+    ws = torch.empty(E.emb_fp8_matmul_workspace_size(300, 512, 1024), dtype=torch.uint8, device="cuda")
+    out = torch.empty(300, 512, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(100):
+        E.emb_debug_lose_op_wait("product", 1)
+        E.emb_fp8_matmul(a, sa, b, sb, out=out, workspace=ws, stream=s)
+        E.emb_debug_lose_op_wait(None)
+        beside = E.emb_check_op_flag()
+        s.synchronize()
+        assert beside | E.emb_check_op_flag(s) == E.EMB_FLAG_OP_TIMEOUT
+        assert E.emb_check_op_flag() == 0
+
+
+def test_flag_of_a_fresh_process():
+    """The check as the first CUDA call of a process."""
+    import os
+    import subprocess
+    import sys
+    code = "import sparse_ctr_embedding_gb300 as E; assert E.emb_check_op_flag() == 0"
+    subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(E.__file__)), check=True, timeout=300)
