@@ -946,14 +946,17 @@ class AdamW:
         self._tensors, self._addresses, self._aliases = tensors, list(map(torch.Tensor.data_ptr, used)), [t.detach() for t in used]
 
     def load_state(self, step: int, m, v, m_scale=None, v_scale=None) -> None:
-        """Sets the states from one tensor per parameter (the layout of `arena`, without its padding)."""
+        """Sets the states from one tensor per parameter (the layout of `arena`, without its padding): all of them, or none if one does not fit."""
+        to, of = [], []
         for key, parts in (("m", m), ("v", v), ("m_scale", m_scale), ("v_scale", v_scale)):
             whole = self.arena[key]
             if (parts is None) != (whole is None):
                 raise ValueError(f"{key} does not match the state kind {self.state}")
             if parts is None:
                 continue
-            to, of = [], []
+            parts = list(parts)
+            if len(parts) != len(self.params):
+                raise ValueError(f"{key}: expected {len(self.params)} tensors")
             for part, at, n in zip(parts, self._at, self._n):
                 if key.endswith("scale"):
                     at, n = at // EMB_ADAM_BLOCK, -(-n // EMB_ADAM_BLOCK)
@@ -961,9 +964,7 @@ class AdamW:
                     raise ValueError(f"{key}: expected {n} elements of {whole.dtype}")
                 to.append(whole[at:at + n].view(torch.uint8))
                 of.append(part.reshape(-1).view(torch.uint8))
-            if len(to) != len(self.params):
-                raise ValueError(f"{key}: expected {len(self.params)} tensors")
-            torch._foreach_copy_(to, of)
+        torch._foreach_copy_(to, of)
         self.step_count = int(step)
 
     def step(self, grads: Sequence[torch.Tensor], grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:

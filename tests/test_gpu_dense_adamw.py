@@ -306,3 +306,24 @@ def test_tensors_on_another_device_are_refused(monkeypatch):
     assert opt.step_count == 0
     opt.step([z(300), z(7)], stream=torch.cuda.Stream())
     assert opt.step_count == 1
+
+
+def test_load_state_takes_all_or_nothing():
+    """A refused state leaves the optimizer as it was; lists of another length are refused."""
+    for state, keys in (("f32", ("m", "v")), ("q8", ("m", "v", "m_scale", "v_scale"))):
+        opt = E.AdamW([torch.zeros(300, device="cuda"), torch.zeros(5, device="cuda")], state=state)
+        opt.step([torch.ones(300, device="cuda"), torch.ones(5, device="cuda")])
+        cut = {k: [opt.arena[k][:2 if k.endswith("scale") else 300], opt.arena[k][2:3] if k.endswith("scale") else opt.arena[k][512:517]]
+               for k in keys}
+        good = {k: [x.clone().view(torch.uint8).zero_().view(x.dtype) for x in parts] for k, parts in cut.items()}
+        before = {k: opt.arena[k].view(torch.uint8).clone() for k in keys}
+        short = [good["v"][0], good["v"][1][:4]]
+        for bad in ({"v": short}, {"v": good["v"][:1]}, {"m": good["m"] + [good["m"][0]]}, {"v": good["v"] + [good["v"][1]]},
+                    {"v": None}, {"v": [x.double() for x in good["v"]]}):
+            with pytest.raises(ValueError):
+                opt.load_state(7, **{**good, **bad})
+            assert opt.step_count == 1
+            for k in keys:
+                assert torch.equal(opt.arena[k].view(torch.uint8), before[k]), (state, k, list(bad))
+        opt.load_state(7, **good)
+        assert opt.step_count == 7 and all(bool((x.float() == 0).all()) for parts in cut.values() for x in parts)
