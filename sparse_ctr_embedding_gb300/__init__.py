@@ -991,6 +991,8 @@ class AdamW:
             self._params = _AdamwParams(self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay, 0, self._state,
                                         self.seed & 0xFFFFFFFF, None)
             self._hyper = hyper
+        if grad_scale is not None and grad_scale.numel() != 1:
+            raise ValueError(f"grad_scale must have one element, got {grad_scale.numel()}")
         p = self._params
         p.step, p.grad_scale = self.step_count + 1, _dense(grad_scale, _F32, "grad_scale", self._dev)
         emb_adamw_step(self._tensors, ptrs.buffer_info()[0], p, stream, self._dev)

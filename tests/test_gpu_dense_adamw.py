@@ -327,3 +327,11 @@ def test_load_state_takes_all_or_nothing():
                 assert torch.equal(opt.arena[k].view(torch.uint8), before[k]), (state, k, list(bad))
         opt.load_state(7, **good)
         assert opt.step_count == 7 and all(bool((x.float() == 0).all()) for parts in cut.values() for x in parts)
+
+
+def test_gradient_scale_is_one_number():
+    opt = E.AdamW([torch.zeros(8, device="cuda")])
+    for n in (0, 2):
+        with pytest.raises(ValueError):
+            opt.step([torch.ones(8, device="cuda")], grad_scale=torch.ones(n, device="cuda"))
+    assert opt.step_count == 0 and bool((opt.params[0] == 0).all())
