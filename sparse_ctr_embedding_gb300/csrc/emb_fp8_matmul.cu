@@ -467,7 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         go = go && mbar_wait(done0 + 8 * stage, ph, stop);
         go = __all_sync(0xffffffffu, go);
         if (!go) break;
-        if (!BCOL && lane == 0) mbar_arrive(sempty0 + 8 * slot);
+        if (!BCOL) {  // all lanes have read their scales: the vote above orders no memory
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sempty0 + 8 * slot);
+        }
         tc_fence_after();
         const unsigned taddr = tmem + ((unsigned)(quarter * 32) << 16) + t * BN + half * C::kHalf;
         // Columns in chunks: the next one, and its scales, are on their way while one is added.
