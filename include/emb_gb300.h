@@ -702,11 +702,15 @@ EMB_API emb_status emb_check_op_flag(void* stream, uint32_t* flags_out);
  *    the scales; role 3, whatever the step: another one, when the last loads are
  *    on their way.  The products then end early and raise EMB_FLAG_OP_TIMEOUT.
  *    role -1: none (the default).  Process-wide.
+ *  - emb_debug_fp8_matmul_plan(m, n, k, plan): how emb_fp8_matmul splits a
+ *    product on the current device: plan[0] columns of a tile (0: no tiles), [1]
+ *    tiles, [2] blocks, [3] steps of a block (0: whole tiles, in turn).
  */
 EMB_API emb_status emb_debug_fail_device_alloc(int64_t after);
 EMB_API int64_t emb_debug_live_device_allocs(void);
 EMB_API emb_status emb_debug_set_probe_bound(emb_table* table, int64_t bound);
 EMB_API emb_status emb_debug_lose_op_wait(int32_t role, int64_t step);
+EMB_API emb_status emb_debug_fp8_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t* plan);
 
 /* Human-readable status name, and the calling thread's last error message
  * (no counterpart in the pages). */

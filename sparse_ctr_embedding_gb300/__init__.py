@@ -25,7 +25,8 @@ __all__ = [
     "emb_table_create", "emb_table_create_device", "emb_table_destroy", "emb_table_get_stats", "emb_table_plan",
     "emb_lookup_fwd", "emb_lookup_fwd_record", "emb_lookup_fwd_dedup", "emb_bwd_adagrad_recorded", "emb_bwd_workspace_size", "emb_bwd_adagrad", "emb_bwd_adagrad_noalloc",
     "emb_bwd_ftrl", "emb_bwd_ftrl_recorded", "emb_table_export_z", "emb_table_import_z",
-    "emb_debug_fail_device_alloc", "emb_debug_live_device_allocs", "emb_debug_set_probe_bound", "emb_debug_lose_op_wait", "Pipeline",
+    "emb_debug_fail_device_alloc", "emb_debug_live_device_allocs", "emb_debug_set_probe_bound", "emb_debug_lose_op_wait",
+    "emb_debug_fp8_matmul_plan", "Pipeline",
     "emb_bwd_unique_keys", "emb_bwd_phase_events", "EMB_NOALLOC_SCRATCH_BYTES", "EMB_SORT_DIGIT_BITS", "BWD_PHASES",
     "emb_resolve", "emb_table_export", "emb_table_export_rows", "emb_table_slots", "emb_check_device_flag",
     "emb_status_string", "emb_last_error",
@@ -155,6 +156,7 @@ def lib():
             "emb_pipeline_wait": [_vp, _i64],
             "emb_debug_set_probe_bound": [_vp, _i64],
             "emb_debug_lose_op_wait": [ctypes.c_int32, _i64],
+            "emb_debug_fp8_matmul_plan": [_i64, _i64, _i64, ctypes.POINTER(_i64)],
             "emb_table_import_z": [_vp, _vp, _vp],
             "emb_resolve": [_vp, _vp, _i64, _vp, _vp, _vp],
             "emb_table_export": [_vp, _vp, _vp, _vp, _vp],
@@ -519,6 +521,13 @@ def emb_debug_lose_op_wait(role: Optional[str], step: int = 0) -> None:
     """From now on the wait of this role ("load", "product", "scales", "other") at this step of a tiled
     emb_fp8_matmul counts as run out (None: none, the default)."""
     _check(lib().emb_debug_lose_op_wait(-1 if role is None else ("load", "product", "scales", "other").index(role), int(step)))
+
+
+def emb_debug_fp8_matmul_plan(m: int, n: int, k: int) -> Tuple[int, int, int, int]:
+    """(columns of a tile or 0, tiles, blocks, steps of a block or 0 for whole tiles) of an emb_fp8_matmul."""
+    plan = (_i64 * 4)()
+    _check(lib().emb_debug_fp8_matmul_plan(m, n, k, plan))
+    return tuple(plan)
 
 
 class Pipeline:

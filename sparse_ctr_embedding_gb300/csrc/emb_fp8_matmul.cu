@@ -921,6 +921,19 @@ extern "C" emb_status emb_debug_lose_op_wait(int32_t role, int64_t step) {
   return EMB_OK;
 }
 
+extern "C" emb_status emb_debug_fp8_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t* plan) {
+  size_t bytes = 0;
+  if (!plan) return fail(EMB_ERR_INVALID_ARG, "plan is NULL");
+  const emb_status rc = emb_fp8_matmul_workspace_size(m, n, k, &bytes);
+  if (rc != EMB_OK) return rc;
+  const Plan pl = make_plan(m, n, k);
+  plan[0] = pl.bn;
+  plan[1] = (int64_t)pl.m_tiles * pl.n_tiles;
+  plan[2] = pl.grid;
+  plan[3] = pl.per_cta;
+  return EMB_OK;
+}
+
 extern "C" emb_status emb_check_op_flag(void* stream, uint32_t* flags_out) {
   static std::mutex one_check;  // g_op_taken holds one check's bits at a time
   const std::lock_guard<std::mutex> hold(one_check);

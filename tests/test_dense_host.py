@@ -229,3 +229,11 @@ def test_operands_on_another_device_are_refused(monkeypatch, op, names):
         calls({})[op]()
     with pytest.raises(AssertionError, match="was called"):
         calls({n: 1 for n in names.split()})[op]()
+
+
+def test_plan_of_a_product():
+    refused(E.lib().emb_debug_fp8_matmul_plan(4, 4, 4, None))
+    refused(E.lib().emb_debug_fp8_matmul_plan(4, -1, 4, (ctypes.c_int64 * 4)()))
+    assert E.emb_debug_fp8_matmul_plan(1, 100, 300)[0] == 0
+    cols, tiles, blocks, steps = E.emb_debug_fp8_matmul_plan(1000, 300, 500)
+    assert cols in (64, 128, 256) and tiles == 8 * -(-300 // cols) and blocks >= 1 and steps >= 0

@@ -335,3 +335,64 @@ def test_gradient_scale_is_one_number():
         with pytest.raises(ValueError):
             opt.step([torch.ones(8, device="cuda")], grad_scale=torch.ones(n, device="cuda"))
     assert opt.step_count == 0 and bool((opt.params[0] == 0).all())
+
+
+def check_8bit_step(opt, dev, p, deq, grads, sizes, first, seed, t, scale=None):
+    """One step of an 8-bit optimizer from known weights and dequantised states: bit for bit; returns the states after it."""
+    after = []
+    for i, n in enumerate(sizes):
+        w, m, _, u = adamw32(p[i], grads[i], deq[i][0], None, deq[i][1], (*HYPER, t), True, grad_scale=scale)
+        p[i] = w.to(p[i].dtype)
+        assert torch.equal(dev[i].cpu(), p[i]), (t, i)
+        bits = random_bits(first[i], n, seed, t)
+        (qm, sm), (qu, su) = round_state(m, bits & 0xFFFF), round_state(u, bits >> 16)
+        qu = torch.where((u > 0) & (qu == 0), torch.full_like(qu, 2.0 ** -9), qu)
+        at, blk = opt._at[i], -(-n // 256)
+        assert torch.equal(opt.arena["m"][at:at + n].cpu().float(), qm) and torch.equal(opt.arena["v"][at:at + n].cpu().float(), qu), (t, i)
+        assert torch.equal(opt.arena["m_scale"][at // 256:at // 256 + blk].cpu(), sm), (t, i)
+        assert torch.equal(opt.arena["v_scale"][at // 256:at // 256 + blk].cpu(), su), (t, i)
+        after.append((qm * sm.repeat_interleave(256)[:n], qu * su.repeat_interleave(256)[:n]))
+    return after
+
+
+# Totals from 4M elements on give a warp several units (4M: two, 16M: eight), tiny and empty
+# tensors between them let it pass over several tensors within its share.
+LONG = [[1_400_003, 0, 1, 300, 257] + [17] * 30 + [2_600_000, 5, 0, 64] + [129, 1] * 20 + [300_001],
+        [16_500_000, 33, 0, 1000]]
+
+
+@pytest.mark.parametrize("sizes", LONG, ids=lambda s: f"{len(s)}x{max(s)}")
+@pytest.mark.parametrize("state", ["f32", "q8"])
+@pytest.mark.parametrize("types", ["plain", "mixed"])
+def test_several_units_a_warp(sizes, state, types):
+    """Bit for bit where a warp goes through several units and tensors: of one type
+    and aligned, or of mixed types with every third tensor off its alignment."""
+    g = torch.Generator().manual_seed(len(sizes))
+    kinds = [(F32, BF16)] if types == "plain" else [(F32, BF16), (BF16, BF16), (F16, F32)]
+    p, grads, dev, first = [], [], [], []
+    for i, n in enumerate(sizes):
+        pt, gt = kinds[i % len(kinds)]
+        p.append(torch.randn(n, generator=g).to(pt))
+        grads.append([(torch.randn(n, generator=g) * 1e-2).to(gt) for _ in range(2)])
+        off = 1 if types == "mixed" and i % 3 == 0 else 0
+        dev.append(torch.empty(n + off, dtype=pt, device="cuda")[off:])
+        dev[-1].copy_(p[-1])
+    opt = E.AdamW(dev, lr=HYPER[0], betas=HYPER[1:3], eps=HYPER[3], weight_decay=HYPER[4], state=state, seed=5)
+    for i in range(len(sizes)):
+        first.append(opt._at[i] + (3 << 32))    # the upper half of an element's number counts too
+        opt._tensors[i].first = first[-1]
+    m = [torch.zeros(n) for n in sizes]
+    v = [torch.zeros(n) for n in sizes]
+    deq = list(zip(m, v))
+    for t in (1, 2):
+        now = [gr[t - 1] for gr in grads]
+        opt.step([x.cuda() for x in now])
+        if state == "q8":
+            deq = check_8bit_step(opt, dev, p, deq, now, sizes, first, 5, t)
+            continue
+        for i, n in enumerate(sizes):
+            w, m[i], v[i], _ = adamw32(p[i], now[i], m[i], v[i], None, (*HYPER, t), False)
+            p[i] = w.to(p[i].dtype)
+            at = opt._at[i]
+            assert torch.equal(dev[i].cpu(), p[i]), (t, i)
+            assert torch.equal(opt.arena["m"][at:at + n].cpu(), m[i]) and torch.equal(opt.arena["v"][at:at + n].cpu(), v[i]), (t, i)

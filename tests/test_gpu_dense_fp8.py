@@ -271,3 +271,51 @@ def test_flag_of_a_fresh_process():
     import sys
     code = "import sparse_ctr_embedding_gb300 as E; assert E.emb_check_op_flag() == 0"
     subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(E.__file__)), check=True, timeout=300)
+
+
+def test_linear_layer_gradients_against_differences_as_a_whole():
+    """The input and the weight gradient of a quantised layer against central
+    differences of the 64-bit loss <dy, x w^T>, every element of a sample: the loss
+    is linear in each, so the differences are its derivatives up to 64-bit
+    rounding.  Operands are rounded by at most 2^-4 of themselves, a part of one
+    side independent from element to element, so the differences' norm stays within
+    a tenth of the gradient's (a zero or negated gradient is off by 1 and by 2)."""
+    g = torch.Generator().manual_seed(7)
+    B, I, O = 96, 136, 80
+    x, w, dy = torch.randn(B, I, generator=g), torch.randn(O, I, generator=g) / I ** 0.5, torch.randn(B, O, generator=g)
+    _, _, qxt, sxt = E.emb_fp8_quantize(x.cuda(), 1, transpose=True)
+    _, _, qwt, swt = E.emb_fp8_quantize(w.cuda(), 128, transpose=True)
+    qd, sd, qdt, sdt = E.emb_fp8_quantize(dy.cuda(), 1, transpose=True)
+    dx = E.emb_fp8_matmul(qd, sd, qwt, swt, out_dtype=F32).cpu().double()
+    dw = E.emb_fp8_matmul(qdt, sdt, qxt, sxt, out_dtype=F32).cpu().double()
+    X, Wt, D = x.double(), w.double(), dy.double()
+    loss = lambda X, Wt: (D * (X @ Wt.t())).sum()  # noqa: E731
+    for got, base, of in ((dx, X, lambda z: loss(z, Wt)), (dw, Wt, lambda z: loss(X, z))):
+        at = torch.randperm(base.numel(), generator=g)[:400]
+        slope = torch.empty(400, dtype=torch.float64)
+        for i, j in enumerate(at.tolist()):
+            up, down = base.clone(), base.clone()
+            up.view(-1)[j] += 0.5
+            down.view(-1)[j] -= 0.5
+            slope[i] = of(up) - of(down)
+        mine = got.reshape(-1)[at]
+        assert float((mine - slope).norm() / slope.norm()) < 0.1
+
+
+@pytest.mark.parametrize("b_rows", [1, 128])
+@pytest.mark.parametrize("out,wide", [(BF16, True), (F32, False)])
+@pytest.mark.parametrize("m,n,k,bn", [(10_001, 1100, 300, 256), (20_011, 400, 640, 256), (5000, 1100, 300, 128), (2500, 2333, 640, 128),
+                                      (40_003, 40, 300, 64), (40_003, 64, 1100, 64)])
+def test_matmul_of_several_tiles_a_block(m, n, k, bn, out, wide, b_rows):
+    """Whole tiles, three or more to a block, of each width: stages, scales and
+    accumulators go on from tile to tile, and a tile's output is stored while the next
+    one's products run.  Every element; rows of the output on and off 32 bytes."""
+    cols, tiles, blocks, steps = E.emb_debug_fp8_matmul_plan(m, n, k)
+    assert cols == bn and steps == 0 and tiles > 2 * blocks      # else this test has lost its subject
+    a, sa, b, sb = operands(m, n, k, 1, b_rows, seed=12)
+    bias = torch.randn(n, generator=torch.Generator().manual_seed(n)).cuda()
+    ld = -(-n // 16) * 16 if wide else n | 1
+    hold = torch.full((m, ld), 7.0, dtype=out, device="cuda")
+    got = E.emb_fp8_matmul(a, sa, b, sb, bias=bias, out=hold[:, :n])
+    check(got, a, sa, b, sb, bias)
+    assert bool((hold[:, n:] == 7.0).all())

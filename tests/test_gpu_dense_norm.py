@@ -330,3 +330,23 @@ def test_sigmoid_of_gates_out_of_range(st, bt):
     assert y[:6, 5].tolist() == [1.0, 0.0, 1.0, 0.0, 1.0, 0.0] and bool(torch.isnan(y[6, 5]))
     y[:, 5] = 0.5
     assert bool((y == 0.5).all())
+
+
+@pytest.mark.parametrize("layer", [False, True])
+@pytest.mark.parametrize("gate", ["elem", "row", "col"])
+@pytest.mark.parametrize("rows,dim", [(40_000, 64), (5000, 1001), (3000, 2048), (2000, 1100)])
+def test_forward_of_many_rows_a_team(rows, dim, gate, layer):
+    """Several rows to each team, the next one loaded while one is reduced: y, h and the statistics of every row."""
+    st, bt = TYPES[(dim + layer) % len(TYPES)]
+    d = make(rows, dim, st, bt, layer, gate, seed=dim)
+    check_fwd(d, layer, "sigmoid", 0.75, *run_fwd(d, layer, "sigmoid", 0.75))
+
+
+@pytest.mark.parametrize("st,bt", [(F32, F32), (BF16, BF16), (F32, F16)])
+@pytest.mark.parametrize("dim", [1100, 2047, 4096, 8191, 8192])
+def test_layer_norm_with_gates_in_large_teams(dim, st, bt):
+    """Every array there, layer norms, a gate per element, teams of 512 and 1024 threads: forward and backward."""
+    d = make(400, dim, st, bt, True, "elem", seed=dim)
+    y, h, stats = run_fwd(d, True, "sigmoid", 0.75)
+    check_fwd(d, True, "sigmoid", 0.75, y, h, stats)
+    check_bwd(d, y, run_bwd(d, y, stats, True, "sigmoid", 0.75), True, "sigmoid", 0.75)
