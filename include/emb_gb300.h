@@ -544,7 +544,8 @@ EMB_API emb_status emb_fp8_quantize(const void* x_d, emb_ftype x_t, int64_t rows
  *   out[i, j] = bias[j] + sum over blocks b of 128 k's of
  *               sa[b, i'] * sb[b, j'] * (sum over k in b of a[i, k] * b[j, k])
  * with i' = i (a_block_rows 1) or i / 128 (128), j' likewise: the codes and
- * scales emb_fp8_quantize writes.  Sums are float32; out is rounded once.
+ * scales emb_fp8_quantize writes.  Sums are float32; out is rounded once.  The two
+ * scales are multiplied first, so their product should be a normal float32 number.
  *   linear layer     y[B, O]  : a = x, b = W[O, I] (128)
  *   its input grad   dx[B, I] : a = dy, b = W transposed (128)
  *   its weight grad  dW[O, I] : a = dy transposed, b = x transposed (both 1)

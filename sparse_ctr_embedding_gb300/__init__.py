@@ -603,13 +603,13 @@ _F8, _F32, _U8 = torch.float8_e4m3fn, torch.float32, torch.uint8
 _new = torch.empty
 
 
-_current_device = torch._C._cuda_getDevice
+_current_device = getattr(torch._C, "_cuda_getDevice", None)   # absent where torch has no CUDA
 
 
 def _launch_device(t: torch.Tensor, name: str) -> int:
     """The current device, which has to be this tensor's."""
     dev = t.get_device()
-    if dev < 0 or not t.is_cuda:
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if dev != _current_device():
         raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{_current_device()}")
@@ -880,7 +880,8 @@ class AdamW:
     which with `step_count` is the checkpoint; load_state takes per-tensor lists.
     A parameter, copy or state that is given other storage (p.data = ..., half(),
     set_()) is found by its address at the next step and described anew (the old
-    storage is held until then); its size and device must stay."""
+    storage is held until then); its size and device must stay.  A CUDA
+    graph replays the step number, the rates and the addresses it was captured with."""
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999),
                  eps: float = 1e-8, weight_decay: float = 0.01, state: str = "f32", seed: int = 0,

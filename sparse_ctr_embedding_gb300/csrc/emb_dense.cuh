@@ -1,5 +1,6 @@
-// Device helpers shared by the dense-tower operators (emb_fp8.cu, emb_norm.cu,
-// emb_adamw.cu): typed loads and stores of eight elements, 8-bit codes.
+// Device helpers shared by the dense-tower operators (emb_fp8.cu, emb_fp8_matmul.cu,
+// emb_norm_fwd.cu, emb_norm_bwd.cu, emb_adamw.cu): typed loads and stores of eight
+// elements, 8-bit codes.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -6,9 +6,10 @@
 // 128-element row pieces.  The tile stays in registers while the largest
 // magnitudes of its rows (warp reductions), its columns (in shared memory over
 // the warps) or all of it are found; the transposed codes go through shared
-// memory so that they leave as whole rows too.  65,536 x 3200 float32: 162 us
-// one way (0.95 of the measured copy rate), 222 both ways (0.84; 254 with 256
-// threads a tile); 131,072 x 1024 bf16 86 and 135.
+// memory so that they leave as whole rows too.  In a loop, 65,536 x 3200 float32:
+// 159 us one way (0.97 of the measured copy rate), 222 both ways (0.84; 254 with 256
+// threads a tile); 131,072 x 1024 bf16 87 and 135.  Rows off the vectors' alignment
+// go element by element: 65,536 x 1003 float32 68 and 94 (0.72 and 0.62).
 #include <algorithm>
 
 #include "emb_dense.cuh"

@@ -14,15 +14,18 @@
 // What bounds it (BN 256, cycles a block of 128 k's): the products take 512, the
 // scaling 304 of TMEM reads and 256 of multiply-adds (512 where b's scales
 // differ by column), and with two accumulators the chain products - arrival -
-// reads - release takes half its length, about 850, a block.  131,072 x 1024 x
-// 8192: 750 us, 2930 TFLOP/s, tensor pipe active 0.54 of the time (a product
-// without scales would be 512 of 512); back to back the power limit lowers the
-// clock (970 us).  8192^3: 378 us; by rows 567.  Steps that led here, on the
-// first of these: scaling from a fixed register budget and scales loaded where
-// they are used 1336; packed multiply-adds, registers split by role 1157;
-// scales three steps ahead 972; a warp for the scales 950; the MMA's operands in
-// uniform registers and one completion barrier a stage 789; stores of unaligned
-// rows out of the loop's kernel 750.
+// reads - release takes half its length, about 850, a block.  Times in this file are
+// of calls in a loop, unless they say apart (L2 flushed before each call); of a pair,
+// both were taken in turn when the choice was made.  131,072 x 1024 x 8192: 770 us
+// apart, 2850 TFLOP/s (at 19,456 x 1024 x 4096 the tensor pipe is active 0.59 of the
+// time; a product without scales would be 512 of 512); in a loop the power limit
+// lowers the clock: 890 to 970, by the operands' values.  8192^3: 431; by rows 597.
+// Steps that led here, on the first of these, with pauses between the
+// calls: scaling from a fixed register budget and scales loaded where they are used
+// 1336; packed multiply-adds, registers split by role 1157; scales three steps ahead
+// 972; a warp for the scales 950; the MMA's operands in uniform registers and one
+// completion barrier a stage 789; stores of unaligned rows out of the loop's kernel
+// 750.
 //
 // Work is cut into (tile, block) steps.  Whole tiles go to the SMs in turn, or
 // all steps are split evenly over the SMs (a tile's blocks then come from several
@@ -30,9 +33,12 @@
 // them in order): make_plan() has the rule.  The split depends on the sizes and
 // the SM count alone.
 //
-// Row kernel (one row, or two by a small b): bound by reading b once; plain CUDA
-// cores.  1 x 1024 x 8192 5.5 us, of which 1.2 is the floor and the rest the
-// latency of a launch and of two loads after one another.
+// Row kernel (one row, or two by a small b): reads b once; plain CUDA cores.
+// 1 x 1024 x 8192: 5.5 us from DRAM, 3.9 in a graph of such calls (b then in L2), of
+// which 1.2 is the floor and the rest the latency of a launch, of one round of loads
+// (codes and scales are asked for together) and of the sums over lanes and warps.
+// 1 x 16,384 x 8192: 33 us, floor 20; the conversions of the codes bound it (issue
+// active 0.78 of the time, DRAM 0.50).
 #include <cuda.h>
 
 #include <algorithm>
@@ -311,7 +317,8 @@ __device__ __forceinline__ void store32(OT* dst, const float* v) {  // 32 bytes
 
 // BCOL: b's scales differ by column (else one per 128 columns: one a warp).
 // WIDE: rows of out are aligned to 32 bytes.  (Both ways of storing in one kernel
-// cost the main loop its registers: 131,072 x 1024 x 8192 900 us instead of 790.)
+// cost the main loop its registers: 131,072 x 1024 x 8192 900 us instead of 790, with
+// pauses between the calls.)
 template <int BN, typename OT, bool BCOL, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant__ CUtensorMap map_a,
                                                            const __grid_constant__ CUtensorMap map_b,
@@ -538,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
           }
         } else {
           // through shared memory, so that a half warp stores 16 neighbours of a row
-          // (10,046 x 1293 x 475 to f16: 155 us with a row to a lane, 61 so)
+          // (10,046 x 1293 x 475 to f16: 155 us with a row to a lane, 61 so; 39 by now)
 #pragma unroll
           for (int c = 0; c < C::kHalf; c += 16) {
             if (col0 + c >= p.n) break;  // the same for the warp
@@ -756,7 +763,8 @@ Plan make_plan(long long m, long long n, long long k) {
   Plan pl;
   if (m == 0 || n == 0 || k == 0) return pl;
   pl.k_blocks = (int)((k + kBK - 1) / kBK);
-  // 1 x 16,384 x 8192: 37 us by rows, 45 by tiles; 2 x 8192 x 8192 29 and 23, 2 x 4096 x 8192 18 and 21
+  // 1 x 16,384 x 8192: 37 us by rows, 45 by tiles; 2 x 8192 x 8192 29 and 23, 2 x 4096 x 8192 18 and 21.
+  // The bound for two rows lies between the last two sizes (6.7e7 and 3.4e7 codes); others were not measured.
   if (m == 1 || (m == kRowMax && (double)n * k <= 4e7)) return pl;
   const int sms = sm_count();
   const long long mt = (m + kBM - 1) / kBM;
@@ -766,7 +774,9 @@ Plan make_plan(long long m, long long n, long long k) {
   // columns takes 0.48, 0.33 or 0.29, a tile's end 3.3, 2 or 2; sharing costs the
   // second launch and 0.42 a megabyte of partial tiles.  Measured: 9853 x 448 x
   // 2560 30 whole and 41 shared at 256; 1024 x 1664 x 16,384 64 and 46; 1024 x
-  // 8192 x 131,072 by rows 1250 and 1470.
+  // 8192 x 131,072 by rows 1250 and 1470.  One set of constants serves both kinds of
+  // scales: the size of the workspace does not depend on the kind.  By rows a step
+  // takes up to 1.4 times as long (8192^3 597 us, 431), which lengthens both sides.
   double best = 0.0;
   const double step_us[3] = {0.48, 0.33, 0.29}, end_us[3] = {3.3, 2.0, 2.0};
   for (int w = 0; w < 3; ++w) {

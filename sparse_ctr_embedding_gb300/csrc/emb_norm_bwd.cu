@@ -13,10 +13,14 @@
 // 1024-thread teams) over all rows of its team, are joined over a block's
 // teams, and leave as one partial per block; a second launch adds the blocks'
 // partials in order, so the result does not depend on which block ran first.
-// 131,072 x 1024 bf16: 439 us, 0.72 of the measured copy rate; issue and the two
-// dependent sums bound it (16 warps an SM: their sums and rows take 127
-// registers a thread; 85 spill and take 830 us, rows staged in shared memory
-// instead of registers 540).
+// 131,072 x 1024 bf16: 447 us in a loop, 0.71 of the measured copy rate.  Neither
+// memory nor issue is full (DRAM 0.45, issue 0.54 of the time at 65,536 rows): the two
+// dependent sums a row are latency, with 16 warps an SM to hide it.  The warps' sums and
+// rows take 127 registers a thread; 85 spill and take 830 us, rows staged in shared
+// memory instead of registers 540 (this form then 520).
+// Teams of 1024 threads (dims above 4096, or above 2048 off the vectors' alignment)
+// have 64 registers a thread and spill (0.2 to 1.5 KB of loads a thread): 16,384 x 8192 bf16 628 us
+// (0.50), with layer norms 835 (0.38), float32 1575 (0.40).
 #include <algorithm>
 
 #include "emb_norm.cuh"
@@ -70,9 +74,9 @@ struct ColSums {
 // what the branches' ends move between registers.
 template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT, bool FULL>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_bwd_kernel(const __grid_constant__ BwdArgs a) {
-  // A row is loaded while the one before it is reduced (131,072 x 1024 bf16: 519
-  // us, 628 without), where registers allow: a layer norm's vector form would
-  // spill (32,768 x 2048: 339 us without, 405 with).
+  // A row is loaded while the one before it is reduced (131,072 x 1024 bf16: 447
+  // us, 460 without), where registers allow: a layer norm's vector form would
+  // spill (32,768 x 2048 bf16: 288 us without, 290 with).
   constexpr bool kPre = MAXT < 1024 && !(VEC && LAYER);
   constexpr bool kHold = MAXT < 1024;  // registers enough to keep the sums over the rows
   constexpr bool kFine = sizeof(BT) == 4;  // float32 gradients of the block and its gate: see activate()

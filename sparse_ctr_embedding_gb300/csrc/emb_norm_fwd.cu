@@ -6,10 +6,11 @@
 // Bound by memory: x, f and a per-element gate in, y and h out, once each; the
 // vectors stay in registers over a team's rows.  Two row sums (four for a
 // layer norm) separate the loads from the stores, so each team loads its next
-// row before it reduces the current one.  131,072 x 1024 bf16: 224 us, 0.88 of
-// the measured copy rate; 16,384 x 1664 with a float32 stream 74 us, 0.76.  Rows
-// that are not multiples of eight elements go one element at a time: 65,536 x
-// 1003 281 us, 0.34 (issue: about sixty instructions an element).
+// row before it reduces the current one.  In a loop, 131,072 x 1024 bf16: 219 us, 0.90
+// of the measured copy rate; 16,384 x 1664 with a float32 stream 77 us, 0.73.  Rows
+// that are not multiples of eight elements go one element at a time: 65,536 x 1003
+// bf16 279 us, 0.35 (issue: about sixty instructions an element).  Teams of 1024
+// threads have 64 registers a thread and spill in some forms (up to 160 bytes).
 #include <algorithm>
 #include <cmath>
 
@@ -38,7 +39,7 @@ template <typename ST, typename BT, bool VEC, bool LAYER, int MAXT, bool FULL>
 __global__ void __launch_bounds__(MAXT, MAXT <= 256 ? 2 : 1) norm_gate_fwd_kernel(const __grid_constant__ FwdArgs a) {
   __shared__ float2 slots[4][64];  // teams that need them: 64 threads or more, so at most 4 a block
   // A row is loaded while the one before it is reduced (16,384 x 1664, float32
-  // stream: 78 us, 96 without), where registers allow.
+  // stream: 77 us, 114 without; 131,072 x 1024 bf16 219, 288), where registers allow.
   constexpr bool kPre = MAXT < 1024;
   constexpr bool kHold = MAXT < 1024;  // registers enough to keep the vectors over the rows
   constexpr bool kFine = sizeof(ST) == 4;  // float32 rows: see activate()
