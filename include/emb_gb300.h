@@ -567,6 +567,67 @@ EMB_API emb_status emb_fp8_matmul(const void* a_d, int64_t lda, const float* sa_
                                   int64_t n, int64_t k, const float* bias_d, void* out_d, emb_ftype out_t,
                                   int64_t ldo, void* workspace_d, size_t ws_bytes, void* stream);
 
+#define EMB_FP4_BLOCK 32 /* neighbouring elements of a row that share one 4-bit scale, or rows of a tile that do */
+
+/*
+ * emb_fp4_quantize -- 4-bit codes of a matrix x[rows, cols] in the microscaling
+ * format (OCP Microscaling Formats v1.0, MXFP4): e2m1 codes (0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 and a sign) and one power of two for each block of 32 columns of
+ * block_rows rows, block_rows 1 or 32 (fewer at the edges).  With A the block's
+ * largest magnitude:
+ *   E = floor(log2 A) - 2, not below -127;  q = x * 2^-E, rounded to the nearest code (ties to
+ *   even, 6 beyond 6: a block's largest values may lie up to 8);  scale byte = E + 127.
+ * A block of zeros has the byte 0.  A block with a value that is not finite has
+ * the byte 255, NaN: all 32 read as NaN, and products with them are NaN.
+ *   x_d     x_t[rows, cols], rows ldx elements apart.
+ *   q_d     uint8[rows, ceil(cols/2)], rows ldq bytes apart: two codes a byte, the
+ *           first in the low four bits.  16-byte aligned, ldq a multiple of 16;
+ *           what lies past cols up to the row's next 16 bytes is set to zero.
+ *   s_d     uint8[ceil(rows/128)][ceil(cols/128)][32][4][4], in the order in which the
+ *           tensor cores read scales: that of row r and block b (of 32 columns) is at
+ *           [r/128][b/4][r%32][r%128/32][b%4]; those past the edges are set to 0.
+ *   qt_d, st_d  the same of the transposed matrix [cols, rows] (rows ldqt bytes apart),
+ *           quantised in blocks of 32 of x's rows by block_rows of its columns, in the
+ *           same pass.  With block_rows 32 both orientations hold the same values.
+ * Either pair may be NULL, not both.  Errors: INVALID_ARG, UNSUPPORTED (rows or cols
+ * above 2^31 - 65536, more than 2^31 - 1 tiles of 128 x 128).
+ */
+EMB_API emb_status emb_fp4_quantize(const void* x_d, emb_ftype x_t, int64_t rows, int64_t cols, int64_t ldx,
+                                    int32_t block_rows, void* q_d, int64_t ldq, void* s_d, void* qt_d, int64_t ldqt,
+                                    void* st_d, void* stream);
+
+/*
+ * emb_fp4_dequantize -- the values that codes and scales stand for, q * 2^E, into
+ * out_t[rows, cols] (rows ldo elements apart): exact in float32 and bfloat16, rounded
+ * once in float16.  A row of codes is read in whole 16 bytes.  Errors as emb_fp4_quantize.
+ */
+EMB_API emb_status emb_fp4_dequantize(const void* q_d, int64_t ldq, const void* s_d, int64_t rows, int64_t cols,
+                                      void* out_d, emb_ftype out_t, int64_t ldo, void* stream);
+
+/*
+ * emb_fp4_matmul -- product of two matrices in 4-bit codes, both with the summed index
+ * along their rows, as emb_fp4_quantize writes them:
+ *   out[i, j] = bias[j] + sum over k of (a[i, k] 2^Ea) * (b[j, k] 2^Eb)
+ * Sums are float32; out is rounded once.  The layer's three products are those of
+ * emb_fp8_matmul.
+ *   a_d, b_d      uint8[m, ceil(k/2)] and uint8[n, ceil(k/2)], rows lda / ldb bytes apart,
+ *                 16-byte aligned, lda and ldb multiples of 16.  A row is read in whole 16 bytes;
+ *                 codes past k are not used, but that of an odd k's last byte has to be 0 (the
+ *                 quantiser's is).
+ *   sa_d, sb_d    their scales, 16-byte aligned; those of blocks past k are not NaN (the quantiser's are 0).
+ *   bias_d        float32[n] or NULL.
+ *   out_d         out_t[m, n], rows ldo elements apart, ldo >= n.
+ *   workspace_d   emb_fp4_matmul_workspace_size() bytes (may be 0: NULL),
+ *                 32-byte aligned; calls that share it must be ordered.
+ * The order of the sums depends on the sizes and the GPU's SM count alone, so
+ * results repeat bitwise.  k = 0 gives the bias (or zeros).  Errors: INVALID_ARG, WORKSPACE,
+ * UNSUPPORTED (m, n or k above 2^31 - 65536), CUDA.
+ */
+EMB_API emb_status emb_fp4_matmul_workspace_size(int64_t m, int64_t n, int64_t k, size_t* bytes);
+EMB_API emb_status emb_fp4_matmul(const void* a_d, int64_t lda, const void* sa_d, const void* b_d, int64_t ldb,
+                                  const void* sb_d, int64_t m, int64_t n, int64_t k, const float* bias_d, void* out_d,
+                                  emb_ftype out_t, int64_t ldo, void* workspace_d, size_t ws_bytes, void* stream);
+
 /*
  * emb_norm_gate_fwd -- the seam between two residual blocks in one pass: the
  * norm after a block, its gate and residual scale, and the norm before the

@@ -33,7 +33,8 @@ __all__ = [
     "EMB_FLAG_PROBE_BOUND", "EMB_FLAG_BAD_OFFSETS", "EMB_FLAG_SLOT_MISMATCH", "EMB_FLAG_BAD_ROW",
     "emb_fp8_quantize", "emb_fp8_matmul", "emb_fp8_matmul_workspace_size", "emb_norm_gate_fwd", "emb_norm_gate_bwd",
     "emb_norm_gate_bwd_workspace_size", "emb_adamw_step", "AdamW", "emb_check_op_flag",
-    "EMB_FLAG_OP_TIMEOUT", "EMB_FP8_BLOCK", "EMB_ADAM_BLOCK", "EMB_NORM_MAX_DIM",
+    "emb_fp4_quantize", "emb_fp4_dequantize", "emb_fp4_matmul", "emb_fp4_matmul_workspace_size",
+    "EMB_FLAG_OP_TIMEOUT", "EMB_FP8_BLOCK", "EMB_FP4_BLOCK", "EMB_ADAM_BLOCK", "EMB_NORM_MAX_DIM",
 ]
 
 EMB_OK = 0
@@ -45,6 +46,7 @@ EMB_NOALLOC_SCRATCH_BYTES = 64 << 20
 EMB_SORT_DIGIT_BITS = 7
 EMB_FLAG_OP_TIMEOUT = 16
 EMB_FP8_BLOCK = 128
+EMB_FP4_BLOCK = 32
 EMB_ADAM_BLOCK = 256
 EMB_NORM_MAX_DIM = 8192
 BWD_PHASES = ("expand", "sort", "reduce", "fixup")
@@ -167,6 +169,11 @@ def lib():
             "emb_fp8_matmul_workspace_size": [_i64, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)],
             "emb_fp8_matmul": [_vp, _i64, _vp, ctypes.c_int32, _vp, _i64, _vp, ctypes.c_int32, _i64, _i64, _i64, _vp,
                                _vp, ctypes.c_int, _i64, _vp, ctypes.c_size_t, _vp],
+            "emb_fp4_quantize": [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int32, _vp, _i64, _vp, _vp, _i64, _vp, _vp],
+            "emb_fp4_dequantize": [_vp, _i64, _vp, _i64, _i64, _vp, ctypes.c_int, _i64, _vp],
+            "emb_fp4_matmul_workspace_size": [_i64, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)],
+            "emb_fp4_matmul": [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, ctypes.c_int, _i64, _vp,
+                               ctypes.c_size_t, _vp],
             "emb_norm_gate_fwd": [ctypes.POINTER(_NormGate)] + [_vp] * 11,
             "emb_norm_gate_bwd_workspace_size": [ctypes.POINTER(_NormGate), ctypes.POINTER(ctypes.c_size_t)],
             "emb_norm_gate_bwd": [ctypes.POINTER(_NormGate)] + [_vp] * 17 + [ctypes.c_size_t, _vp],
@@ -747,6 +754,113 @@ def emb_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
     _check(lib().emb_fp8_matmul(a.data_ptr(), lda, _dense(sa, _F32, "sa", dev), a_rows, b.data_ptr(), ldb, _dense(sb, _F32, "sb", dev),
                                 b_rows, m, n, k, None if bias is None else _dense(bias, _F32, "bias", dev),
                                 out.data_ptr(), _ftype(out.dtype, "out"), ldo, wp, ws_bytes, _raw_stream(stream, dev)))
+    return out
+
+
+def _packed_stride(t: torch.Tensor, name: str, dev: int) -> int:
+    if t.dtype is not _U8:
+        raise TypeError(f"{name} must be {_U8}, got {t.dtype}")
+    ld = _row_stride(t, name, dev)
+    return -(-ld // 16) * 16 if ld % 16 and (t.shape[0] <= 1 or t.shape[1] == 0) else ld
+
+
+def _scale4(s: torch.Tensor, rows: int, cols: int, name: str, dev: int) -> int:
+    """The address of the scales of 4-bit codes [rows, cols]."""
+    shape = ((rows + 127) >> 7, (cols + 127) >> 7, 32, 4, 4)
+    if s.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(s.shape)}")
+    return _dense(s, _U8, name, dev)
+
+
+def emb_fp4_quantize(x: torch.Tensor, block_rows: int = 1, transpose: bool = False, stream=None):
+    """Microscaled 4-bit codes (e2m1, a power of two per 32 columns of block_rows
+    rows, 1 or 32) of x[rows, cols] (float32, bfloat16 or float16; rows may be
+    strided): (q, s), with q uint8[rows, ceil(cols/2)] (the first code of a byte in
+    its low four bits) and s uint8[ceil(rows/128), ceil(cols/128), 32, 4, 4] in the
+    tensor cores' order; with transpose=True (q, s, qt, st), the codes of x.T in
+    blocks along x's rows as well, from the same pass."""
+    dev = _launch_device(x, "x")
+    ldx = _row_stride(x, "x", dev)
+    if block_rows not in (1, EMB_FP4_BLOCK):
+        raise ValueError("block_rows must be 1 or 32")
+    r, c = x.shape
+    rb, cb, wq, wqt = (r + 127) >> 7, (c + 127) >> 7, (c + 1) >> 1, (r + 1) >> 1
+    ldq, ldqt = (wq + 15) & ~15, (wqt + 15) & ~15
+    q, s = _empty(stream, x, (r, ldq), _U8), _empty(stream, x, (rb, cb, 32, 4, 4), _U8)
+    if not transpose:
+        _check(lib().emb_fp4_quantize(x.data_ptr(), _ftype(x.dtype, "x"), r, c, ldx, block_rows, q.data_ptr(), ldq, s.data_ptr(),
+                                      None, 0, None, _raw_stream(stream, dev)))
+        return (q if ldq == wq else q[:, :wq]), s
+    qt, st = _empty(stream, x, (c, ldqt), _U8), _empty(stream, x, (cb, rb, 32, 4, 4), _U8)
+    _check(lib().emb_fp4_quantize(x.data_ptr(), _ftype(x.dtype, "x"), r, c, ldx, block_rows, q.data_ptr(), ldq, s.data_ptr(),
+                                  qt.data_ptr(), ldqt, st.data_ptr(), _raw_stream(stream, dev)))
+    return (q if ldq == wq else q[:, :wq]), s, (qt if ldqt == wqt else qt[:, :wqt]), st
+
+
+def emb_fp4_dequantize(q: torch.Tensor, s: torch.Tensor, cols: Optional[int] = None, dtype: torch.dtype = torch.bfloat16,
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values [rows, cols] that 4-bit codes and scales stand for.  cols: default
+    two per byte of q (give it where it is odd)."""
+    dev = _launch_device(q, "q")
+    ldq = _packed_stride(q, "q", dev)
+    rows, width = q.shape
+    if cols is None:
+        cols = 2 * width
+    elif (cols + 1) >> 1 != width:
+        raise ValueError(f"q has {width} bytes a row, {cols} codes take {(cols + 1) >> 1}")
+    sp = _scale4(s, rows, cols, "s", dev)
+    if out is None:
+        out, ldo = _empty(stream, q, (rows, cols), dtype), cols
+    else:
+        if out.shape != (rows, cols):
+            raise ValueError(f"out must be [{rows}, {cols}]")
+        ldo = _row_stride(out, "out", dev)
+    _check(lib().emb_fp4_dequantize(q.data_ptr(), ldq, sp, rows, cols, out.data_ptr(), _ftype(out.dtype, "out"), ldo,
+                                    _raw_stream(stream, dev)))
+    return out
+
+
+def emb_fp4_matmul_workspace_size(m: int, n: int, k: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().emb_fp4_matmul_workspace_size(m, n, k, ctypes.byref(b)))
+    return b.value
+
+
+def emb_fp4_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor,
+                   out_dtype: torch.dtype = torch.bfloat16, bias: Optional[torch.Tensor] = None,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """a[m, k] @ b[n, k].T of 4-bit codes and scales from emb_fp4_quantize (+ bias[n]).
+    workspace: emb_fp4_matmul_workspace_size bytes (k: twice the bytes of a row) that
+    the caller keeps; made for the call if None."""
+    dev = _launch_device(a, "a")
+    lda, ldb = _packed_stride(a, "a", dev), _packed_stride(b, "b", dev)
+    (m, w), (n, wb) = a.shape, b.shape
+    if wb != w:
+        raise ValueError(f"a and b must have the same columns, got {w} and {wb} bytes")
+    k = 2 * w
+    if bias is not None and bias.numel() != n:
+        raise ValueError(f"bias must have {n} elements")
+    sap, sbp = _scale4(sa, m, k, "sa", dev), _scale4(sb, n, k, "sb", dev)
+    if out is None:
+        out, ldo = _empty(stream, a, (m, n), out_dtype), n
+    else:
+        if out.shape != (m, n):
+            raise ValueError(f"out must be [{m}, {n}]")
+        ldo = _row_stride(out, "out", dev)
+    wp, ws_bytes = None, 0
+    if workspace is None:
+        ws_bytes = emb_fp4_matmul_workspace_size(m, n, k)
+        if ws_bytes:
+            workspace = _empty(stream, a, ws_bytes, _U8)
+            wp = workspace.data_ptr()
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
+    else:
+        wp, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    _check(lib().emb_fp4_matmul(a.data_ptr(), lda, sap, b.data_ptr(), ldb, sbp, m, n, k,
+                                None if bias is None else _dense(bias, _F32, "bias", dev), out.data_ptr(),
+                                _ftype(out.dtype, "out"), ldo, wp, ws_bytes, _raw_stream(stream, dev)))
     return out
 
 

@@ -1,6 +1,6 @@
 """Build the sm_103a shared library in-tree: sparse_ctr_embedding_gb300/_build/libemb_gb300.so.
 
-nvcc compiles each translation unit in parallel and links a shared library
+nvcc compiles each translation unit that changed, in parallel, and links a shared library
 with the CUDA runtime linked statically, exporting only the C ABI declared in
 include/emb_gb300.h.
 """
@@ -17,7 +17,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD, "libemb_gb300.so")
 HEADER = os.path.join(ROOT, "include", "emb_gb300.h")
 SOURCES = ["emb_table.cu", "emb_fwd.cu", "emb_bwd.cu", "emb_pipe.cu", "emb_build.cu",
-           "emb_fp8.cu", "emb_fp8_matmul.cu", "emb_norm_fwd.cu", "emb_norm_bwd.cu", "emb_adamw.cu"]
+           "emb_fp8.cu", "emb_fp8_matmul.cu", "emb_norm_fwd.cu", "emb_norm_bwd.cu", "emb_adamw.cu",
+           "emb_fp4.cu", "emb_fp4_matmul.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -43,19 +44,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     procs = []
     objs = []
+    common = max(os.path.getmtime(f) for f in [__file__, *_inputs()] if not f.endswith(".cu"))
     for src in SOURCES:
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
         objs.append(obj)
-        cmd = [NVCC, *ARCH, *CFLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+        newest = max(common, os.path.getmtime(os.path.join(CSRC, src)))
+        if not force and os.path.exists(obj) and os.path.getmtime(obj) > newest:
+            continue
+        part = f"{obj}.tmp{os.getpid()}.o"      # an object that is there is whole
+        cmd = [NVCC, *ARCH, *CFLAGS, "-c", os.path.join(CSRC, src), "-o", part]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+        procs.append((src, obj, part, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
-    for src, p in procs:
+    for src, obj, part, p in procs:
         out, _ = p.communicate()
-        if p.returncode != 0:
+        if p.returncode == 0:
+            os.replace(part, obj)
+        else:
             failed.append(f"{src}:\n{out.decode(errors='replace')}")
-        elif verbose and out:
+        if p.returncode == 0 and verbose and out:
             print(out.decode(errors="replace"), file=sys.stderr)
     if failed:
         raise RuntimeError("nvcc failed\n" + "\n".join(failed))

@@ -39,14 +39,12 @@
 // (codes and scales are asked for together) and of the sums over lanes and warps.
 // 1 x 16,384 x 8192: 33 us, floor 20; the conversions of the codes bound it (issue
 // active 0.78 of the time, DRAM 0.50).
-#include <cuda.h>
-
 #include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <mutex>
 
-#include "emb_dense.cuh"
+#include "emb_tiles.cuh"
 
 namespace emb {
 namespace {
@@ -54,9 +52,8 @@ namespace {
 __device__ unsigned g_op_flags;   // EMB_FLAG_OP_* bits since the last emb_check_op_flag
 __device__ unsigned g_op_taken;   // what the last check read
 
-constexpr int kBM = 128;             // rows of a tile
 constexpr int kBK = EMB_FP8_BLOCK;   // k's of a step: one scale block, 128 bytes of a row
-constexpr int kScaleWarps = 8;
+constexpr int kScaleWarps = kSumWarps;
 constexpr int kThreads = (kScaleWarps + 4) * 32;  // then a TMA warp, an MMA warp, a warp for the scales, an idle one
 // Registers: the scaling warps' accumulators need more than an even share, the other four warps little.
 constexpr int kLaunchRegs = 168, kScaleRegs = 224, kOtherRegs = 56;
@@ -64,7 +61,7 @@ static_assert(kScaleWarps * 32 * kScaleRegs + 128 * kOtherRegs <= kThreads * kLa
 constexpr int kTmaWarp = kScaleWarps, kMmaWarp = kScaleWarps + 1, kFetchWarp = kScaleWarps + 2;
 constexpr int kAhead = 8;            // steps whose scales are held or on their way
 constexpr int kAfterLoads = 0;       // lost_warp: not a warp's wait, but the block is told when its last load is issued
-constexpr unsigned kWaitLimit = 1u << 21;  // polls of one wait before the kernel gives up
+constexpr int kLostWarps[4] = {kTmaWarp, kMmaWarp, kFetchWarp, kAfterLoads};  // by the role of emb_debug_lose_op_wait
 
 struct MatmulArgs {
   const unsigned char *a, *b;
@@ -85,70 +82,10 @@ struct MatmulArgs {
 
 // ------------------------------------------------------------------ PTX
 
-__device__ __forceinline__ unsigned smem_u32(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void mbar_init(unsigned bar, unsigned count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(unsigned bar, unsigned bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(unsigned bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(unsigned bar, unsigned parity) {
-  unsigned ok;
-  asm volatile(
-      "{\n.reg .pred p;\n"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      "selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// What a wait that ran out does: the block's other waits end too, and the host is told.
-__device__ __forceinline__ bool give_up(volatile int* stop) {
-  *stop = 1;
-  atomicOr(&g_op_flags, EMB_FLAG_OP_TIMEOUT);
-  return false;
-}
-// Waits for a barrier's phase; false when the limit ran out here or in another
-// warp of the block (`stop`), after which the caller leaves its loops.
+__device__ __forceinline__ bool give_up(volatile int* stop) { return emb::give_up(stop, &g_op_flags); }
 __device__ __forceinline__ bool mbar_wait(unsigned bar, unsigned parity, volatile int* stop) {
-  if (mbar_try(bar, parity)) return true;
-  for (unsigned i = 0; i < kWaitLimit; ++i) {
-    if (mbar_try(bar, parity)) return true;
-    if (*stop) return false;
-  }
-  return give_up(stop);
+  return emb::mbar_wait(bar, parity, stop, &g_op_flags);
 }
-// After a wait has run out: waits for a barrier of what is still in flight.
-__device__ __forceinline__ void mbar_drain(unsigned bar, unsigned parity) {
-  for (unsigned i = 0; i < kWaitLimit && !mbar_try(bar, parity); ++i) {}
-}
-// One lane of a converged warp.  A branch on it (and not on a lane number) lets
-// the compiler keep what the lane issues in uniform registers: with the latter
-// each tcgen05.mma took about 100 cycles to issue.
-__device__ __forceinline__ bool elect_one() {
-  unsigned one;
-  asm volatile(
-      "{\n.reg .pred p;\n"
-      "elect.sync _|p, 0xffffffff;\n"
-      "selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(one));
-  return one != 0;
-}
-__device__ __forceinline__ void tma_load(unsigned dst, const CUtensorMap* map, int x, int y, unsigned bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void tc_commit(unsigned bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // D[128 x N] (+)= A B^T, 32 k's, e4m3 operands in shared memory.
 __device__ __forceinline__ void tc_mma(unsigned d, unsigned long long a, unsigned long long b, unsigned idesc, bool add) {
   asm volatile(
@@ -157,50 +94,6 @@ __device__ __forceinline__ void tc_mma(unsigned d, unsigned long long a, unsigne
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"((unsigned)add)
       : "memory");
-}
-// Starts reading 32 columns of this warp's 32 TMEM lanes, one lane a thread.
-__device__ __forceinline__ void tc_load32(unsigned addr, unsigned* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
-      "[%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
-        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
-        "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
-        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(addr)
-      : "memory");
-}
-__device__ __forceinline__ void tc_load16(unsigned addr, unsigned* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
-        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(addr)
-      : "memory");
-}
-// Waits for the loads above; the registers pass through so that no use of them moves before it.
-__device__ __forceinline__ void tc_wait32(unsigned* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
-                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
-                 "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
-                 "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
-}
-__device__ __forceinline__ void tc_wait16(unsigned* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
-                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
-}
-template <int N>
-__device__ __forceinline__ void tc_load(unsigned addr, unsigned* v) {
-  if constexpr (N == 16) tc_load16(addr, v);
-  else tc_load32(addr, v);
-}
-template <int N>
-__device__ __forceinline__ void tc_wait(unsigned* v) {
-  if constexpr (N == 16) tc_wait16(v);
-  else tc_wait32(v);
 }
 
 // Two floats side by side, and their products and multiply-adds (one issue slot for two).
@@ -221,12 +114,6 @@ __device__ __forceinline__ void fma2(f32x2 a, f32x2 b, float* c) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(c[0]), "=f"(c[1]) : "l"(r));
 }
 
-// Shared memory descriptor of a K-major operand: rows of 128 bytes, 128-byte
-// swizzle (layout 2), eight-row groups 1024 bytes apart, descriptor version 1.
-__device__ __forceinline__ unsigned long long smem_desc(unsigned addr) {
-  return (unsigned long long)((addr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-
 // ------------------------------------------------------------------ tile kernel
 
 template <int BN>
@@ -240,40 +127,6 @@ struct TileCfg {
   static constexpr int kBytes = kStages * kStageBytes + kScaleBytes + kStoreBytes + 1024;  // + room to align
 };
 
-struct Unit {  // consecutive blocks of one tile
-  int tm, tn, kb0, kb1;
-  long long tile;
-};
-
-// Tiles in groups of 16 rows of tiles, column by column within a group: the
-// blocks at work at one time then share few slabs of a and b in L2.
-__device__ __forceinline__ void tile_at(const MatmulArgs& p, long long t, int* tm, int* tn) {
-  constexpr int kGroup = 16;
-  const long long per_group = (long long)kGroup * p.n_tiles;
-  const int g = (int)(t / per_group);
-  const int in = (int)(t - g * per_group);
-  const int rows = min(kGroup, p.m_tiles - g * kGroup);
-  *tm = g * kGroup + in % rows;
-  *tn = in / rows;
-}
-
-// The block's next unit from its position: a tile number, or a step.
-__device__ __forceinline__ bool next_unit(const MatmulArgs& p, long long* pos, long long end, Unit* u) {
-  if (*pos >= end) return false;
-  if (p.per_cta == 0) {
-    u->tile = *pos;
-    u->kb0 = 0;
-    u->kb1 = p.k_blocks;
-    *pos += gridDim.x;
-  } else {
-    u->tile = *pos / p.k_blocks;
-    u->kb0 = (int)(*pos - u->tile * p.k_blocks);
-    u->kb1 = (int)min((long long)p.k_blocks, u->kb0 + (end - *pos));
-    *pos += u->kb1 - u->kb0;
-  }
-  tile_at(p, u->tile, &u->tm, &u->tn);
-  return true;
-}
 // Where a test asked for a step's wait to run out (emb_debug_lose_op_wait): ends the
 // unit before that step, and tells after it that the step is reached.  Not asked in
 // the scaling warps, where even once a unit it cost products by rows 3 %.
@@ -283,38 +136,6 @@ __device__ __forceinline__ void cut_lost(const MatmulArgs& p, int role, unsigned
 __device__ __forceinline__ bool at_lost(const MatmulArgs& p, int role, unsigned it) {
   return p.lost_warp == role && p.lost_step == it;
 }
-__device__ __forceinline__ void my_range(const MatmulArgs& p, long long* pos, long long* end) {
-  if (p.per_cta == 0) {
-    *pos = blockIdx.x;
-    *end = (long long)p.m_tiles * p.n_tiles;
-  } else {
-    *pos = blockIdx.x * p.per_cta;
-    *end = min(p.steps, *pos + p.per_cta);
-  }
-}
-
-template <typename OT>
-__device__ __forceinline__ void store32(OT* dst, const float* v) {  // 32 bytes
-  if constexpr (sizeof(OT) == 4) {
-    Raw8<float> r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.set2(i, v[2 * i], v[2 * i + 1]);
-    r.store((float*)dst);
-  } else {
-    Raw8<OT> lo, hi;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      lo.set2(i, v[2 * i], v[2 * i + 1]);
-      hi.set2(i, v[8 + 2 * i], v[8 + 2 * i + 1]);
-    }
-    const unsigned* a = reinterpret_cast<const unsigned*>(lo.v);
-    const unsigned* b = reinterpret_cast<const unsigned*>(hi.v);
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]),
-                 "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3])
-                 : "memory");
-  }
-}
-
 // BCOL: b's scales differ by column (else one per 128 columns: one a warp).
 // WIDE: rows of out are aligned to 32 bytes.  (Both ways of storing in one kernel
 // cost the main loop its registers: 131,072 x 1024 x 8192 900 us instead of 790, with
@@ -522,50 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
         }
       }
       if (!go) break;
-      if (u.kb0 == 0 && u.kb1 == p.k_blocks) {
-        if constexpr (WIDE) {
-          if (row < p.m) {
-            OT* dst = (OT*)p.out + row * p.ldo + col0;
-            constexpr int kVec = 32 / sizeof(OT);
-#pragma unroll
-            for (int c = 0; c < C::kHalf; c += kVec) {
-              if (p.bias) {
-#pragma unroll
-                for (int j = 0; j < kVec; ++j)
-                  if (col0 + c + j < p.n) acc[c + j] += __ldg(p.bias + col0 + c + j);
-              }
-              if (col0 + c + kVec <= p.n) {
-                store32<OT>(dst + c, acc + c);
-              } else {
-#pragma unroll
-                for (int j = 0; j < kVec; ++j)
-                  if (col0 + c + j < p.n) dst[c + j] = from_f32<OT>(acc[c + j]);
-              }
-            }
-          }
-        } else {
-          // through shared memory, so that a half warp stores 16 neighbours of a row
-          // (10,046 x 1293 x 475 to f16: 155 us with a row to a lane, 61 so; 39 by now)
-#pragma unroll
-          for (int c = 0; c < C::kHalf; c += 16) {
-            if (col0 + c >= p.n) break;  // the same for the warp
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = acc[c + j];
-            __syncwarp();
-            const int col = col0 + c + (lane & 15);
-            const float bias = p.bias && col < p.n ? __ldg(p.bias + col) : 0.0f;
-            OT* dst = (OT*)p.out + (row - lane) * p.ldo + col;
-#pragma unroll 4
-            for (int r = lane >> 4; r < 32; r += 2)
-              if (row - lane + r < p.m && col < p.n) dst[r * p.ldo] = from_f32<OT>(stage[r * 17 + (lane & 15)] + bias);
-          }
-        }
-      } else if (row < p.m) {  // part of a tile: slot (block + tile) is this piece's alone
-        float* dst = p.partial + (long long)(blockIdx.x + u.tile) * kBM * BN + (warp * C::kHalf * 4 + lane) * 8;
-#pragma unroll
-        for (int c = 0; c < C::kHalf; c += 8) store32<float>(dst + c * 32, acc + c);
-      }
+      store_unit<BN, OT, WIDE>(p, u, warp, lane, row, col0, acc, stage);
     }
   }
   tc_fence_before();
@@ -586,37 +364,6 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN));
   }
-}
-
-// Adds the pieces of each tile that several blocks computed, in k order.  A piece
-// lies as the scaling warps store it, whole kilobytes at a time: by warps, by 8
-// columns, by rows (1664 x 452 x 30,584 to bf16: 52 us, and 56 with pieces laid
-// out by rows).  One block takes 32 rows x 32 columns, four columns a thread.
-template <int BN, typename OT>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ MatmulArgs p) {
-  constexpr int kBlocks = kBM * BN / 1024, kHalf = TileCfg<BN>::kHalf, kWarpBlocks = kHalf / 32;
-  const long long tile = blockIdx.x / kBlocks;
-  const int q = (int)(blockIdx.x % kBlocks), warp = q / kWarpBlocks, x = threadIdx.x / 8, y = threadIdx.x % 8;
-  const long long first = tile * p.k_blocks / p.per_cta, last = ((tile + 1) * p.k_blocks - 1) / p.per_cta;
-  if (first == last) return;  // one block had it whole
-  int tm, tn;
-  tile_at(p, tile, &tm, &tn);
-  const int row = tm * kBM + (warp & 3) * 32 + x, col = tn * BN + (warp >> 2) * kHalf + q % kWarpBlocks * 32 + y * 4;
-  if (row >= p.m || col >= p.n) return;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const float* src = p.partial + (first + tile) * kBM * BN + q * 1024 + y / 2 * 256 + x * 8 + y % 2 * 4;
-#pragma unroll 8
-  for (long long b = first; b <= last; ++b, src += (long long)kBM * BN) {
-    const float4 w = *reinterpret_cast<const float4*>(src);
-    v.x += w.x;
-    v.y += w.y;
-    v.z += w.z;
-    v.w += w.w;
-  }
-  const float o[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (col + j < p.n) ((OT*)p.out)[row * p.ldo + col + j] = from_f32<OT>(o[j] + (p.bias ? __ldg(p.bias + col + j) : 0.0f));
 }
 
 // ------------------------------------------------------------------ row kernel
@@ -734,21 +481,12 @@ __global__ void __launch_bounds__(256) row_kernel(const __grid_constant__ Matmul
   }
 }
 
-// out = bias: a product over no k's.
-template <typename OT>
-__global__ void __launch_bounds__(256) bias_kernel(const __grid_constant__ MatmulArgs p) {
-  for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < (long long)p.m * p.n; e += (long long)gridDim.x * 256) {
-    const long long i = e / p.n, j = e - i * p.n;
-    ((OT*)p.out)[i * p.ldo + j] = from_f32<OT>(p.bias ? p.bias[j] : 0.0f);
-  }
-}
-
 // Reads and clears the flag word in one step: a kernel of another stream may raise a bit at any time.
 __global__ void take_flags_kernel() { g_op_taken = atomicExch(&g_op_flags, 0u); }
 
 // ------------------------------------------------------------------ host side
 
-std::atomic<int> g_lost_warp{-1};  // emb_debug_lose_op_wait
+std::atomic<int> g_lost_role{-1};  // emb_debug_lose_op_wait
 std::atomic<unsigned> g_lost_step{0};
 
 struct Plan {
@@ -804,33 +542,6 @@ Plan make_plan(long long m, long long n, long long k) {
   return pl;
 }
 
-typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-  static const EncodeTiled fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return (EncodeTiled)f;
-  }();
-  return fn;
-}
-
-// Slabs of 128 k's by `box_rows` rows of a code matrix; what lies outside is read as zeros.
-bool make_map(CUtensorMap* map, const void* base, long long rows, long long k, long long ld, int box_rows) {
-  const EncodeTiled fn = encode_tiled();
-  if (!fn) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
-  const cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)box_rows}, step[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int BN, typename OT>
 cudaError_t launch_tiles(const MatmulArgs& p, const Plan& pl, const CUtensorMap& ma, const CUtensorMap& mb, cudaStream_t st) {
   auto* k = p.wide_out ? (p.b_shift ? tile_kernel<BN, OT, false, true> : tile_kernel<BN, OT, true, true>)
@@ -840,7 +551,7 @@ cudaError_t launch_tiles(const MatmulArgs& p, const Plan& pl, const CUtensorMap&
   k<<<pl.grid, kThreads, TileCfg<BN>::kBytes, st>>>(ma, mb, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || pl.per_cta == 0) return e;
-  join_kernel<BN, OT><<<pl.m_tiles * pl.n_tiles * (kBM * BN / 1024), 256, 0, st>>>(p);
+  join_kernel<BN, OT, MatmulArgs><<<pl.m_tiles * pl.n_tiles * (kBM * BN / 1024), 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -856,7 +567,7 @@ cudaError_t launch_rows(const MatmulArgs& p, cudaStream_t st) {
 template <typename OT>
 cudaError_t launch(const MatmulArgs& p, const Plan& pl, const CUtensorMap& ma, const CUtensorMap& mb, cudaStream_t st) {
   if (p.k == 0) {
-    bias_kernel<OT><<<(int)std::min<long long>(((long long)p.m * p.n + 255) / 256, 8LL * sm_count()), 256, 0, st>>>(p);
+    bias_kernel<OT, MatmulArgs><<<(int)std::min<long long>(((long long)p.m * p.n + 255) / 256, 8LL * sm_count()), 256, 0, st>>>(p);
     return cudaGetLastError();
   }
   if (pl.bn == 0) {
@@ -868,6 +579,14 @@ cudaError_t launch(const MatmulArgs& p, const Plan& pl, const CUtensorMap& ma, c
 }
 
 }  // namespace
+
+void lost_wait(int* role, unsigned* step) {
+  *role = g_lost_role.load();
+  *step = g_lost_step.load();
+}
+
+cudaError_t op_flags(unsigned** word) { return cudaGetSymbolAddress((void**)word, g_op_flags); }
+
 }  // namespace emb
 
 using namespace emb;
@@ -907,10 +626,13 @@ extern "C" emb_status emb_fp8_matmul(const void* a_d, int64_t lda, const float* 
   const Plan pl = make_plan(m, n, k);
   const int as = a_block_rows == 1 ? 0 : 7, bs = b_block_rows == 1 ? 0 : 7;
   const size_t ob = ftype_bytes(out_t);
+  int lost;
+  unsigned lost_step;
+  lost_wait(&lost, &lost_step);
   const MatmulArgs p{(const unsigned char*)a_d, (const unsigned char*)b_d, sa_d, sb_d, bias_d, out_d, (float*)workspace_d,
                      lda, ldb, ldo, as ? (m + 127) / 128 : m, bs ? (n + 127) / 128 : n, (int)m, (int)n, (int)k, as, bs,
                      pl.m_tiles, pl.n_tiles, pl.k_blocks, (long long)pl.m_tiles * pl.n_tiles * pl.k_blocks, pl.per_cta,
-                     aligned_to(out_d, 32) && (ldo * ob) % 32 == 0, g_lost_warp.load(), g_lost_step.load()};
+                     aligned_to(out_d, 32) && (ldo * ob) % 32 == 0, lost < 0 ? -1 : kLostWarps[lost], lost_step};
   CUtensorMap ma{}, mb{};
   if (pl.bn && (!make_map(&ma, a_d, m, k, lda, kBM) || !make_map(&mb, b_d, n, k, ldb, pl.bn)))
     return fail(EMB_ERR_CUDA, "cuTensorMapEncodeTiled failed or is not available");
@@ -925,9 +647,8 @@ extern "C" emb_status emb_fp8_matmul(const void* a_d, int64_t lda, const float* 
 
 extern "C" emb_status emb_debug_lose_op_wait(int32_t role, int64_t step) {
   if (role < -1 || role > 3 || step < 0 || step > 0x7fffffffLL) return fail(EMB_ERR_INVALID_ARG, "role must be -1 to 3, step 0 to 2^31 - 1");
-  const int warps[4] = {kTmaWarp, kMmaWarp, kFetchWarp, kAfterLoads};
   g_lost_step.store((unsigned)step);
-  g_lost_warp.store(role < 0 ? -1 : warps[role]);
+  g_lost_role.store(role);
   return EMB_OK;
 }
 
