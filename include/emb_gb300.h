@@ -734,6 +734,47 @@ EMB_API emb_status emb_adamw_step(const emb_adamw_tensor* tensors, const void* c
                                   const emb_adamw_params* params, void* stream);
 
 /*
+ * emb_muon_step -- one step of Muon (Jordan et al., "Muon: An optimizer for hidden layers in
+ * neural networks", 2024) over many matrices at once: the tower's optimizer for
+ * its matrices, beside emb_adamw_step for vectors and embeddings.  With beta the momentum:
+ *   g = grad * grad_scale;  m = beta m + (1-beta) g;  u = (1-beta) g + beta m (nesterov) or m
+ *   X = u / (|u| + 1e-7)  (the root of the sum of squares), transposed if it has more rows than columns
+ *   five times:  A = X X^T;  B = -4.7750 A + 2.0315 A A;  X = 3.4445 X + B X
+ *   w = w (1 - lr wd) - lr scale X
+ * X ends with singular values near 1.  Products are of float16 values with float32 sums:
+ * EMB_MUON_HALF of one each (an update's error is about 2^-9 of it; more where u has a
+ * low rank, whose other directions the steps raise from rounding noise), EMB_MUON_SPLIT
+ * of two each (float32's accuracy, at a third of the rate).  The rest is float32; w is
+ * rounded to nearest-even in its own type.  A matrix whose u has a value that is not
+ * finite, or squares that sum past float32, becomes NaN.
+ */
+typedef enum { EMB_MUON_HALF = 0, EMB_MUON_SPLIT = 1 } emb_muon_products;
+#define EMB_MUON_MAX_DIM 65536
+typedef struct {
+  void* param_d;  /* param_t[rows, cols], contiguous, updated in place */
+  float* m_d;     /* float32[rows, cols] */
+  int64_t rows, cols; /* up to EMB_MUON_MAX_DIM (UNSUPPORTED beyond); 0 is allowed */
+  emb_ftype param_t, grad_t;
+  float scale;    /* of this matrix's update, e.g. 0.2 sqrt(max(rows, cols)): a root mean square of 0.2, as AdamW's */
+} emb_muon_tensor;
+typedef struct {
+  double lr, momentum, weight_decay; /* lr, weight_decay >= 0, 0 <= momentum < 1 */
+  int32_t nesterov;
+  emb_muon_products products;
+  const float* grad_scale_d; /* device float32[1] or NULL: multiplies every gradient */
+} emb_muon_params;
+/* tensors and grads (device pointers grad_t[rows, cols], one per matrix) are host arrays,
+ * read before the call returns.  Matrices must not overlap.  workspace_d:
+ * emb_muon_workspace_size() bytes, 256-byte aligned (about 4 bytes an element, 8 with
+ * EMB_MUON_SPLIT, and as much for the short sides' squares); calls that share it must be
+ * ordered.  Results repeat bitwise.  Where a bounded wait runs out before the last
+ * products, the weights are left as they were. */
+EMB_API emb_status emb_muon_workspace_size(const emb_muon_tensor* tensors, int32_t n_tensors, emb_muon_products products,
+                                           size_t* bytes);
+EMB_API emb_status emb_muon_step(const emb_muon_tensor* tensors, const void* const* grads, int32_t n_tensors,
+                                 const emb_muon_params* params, void* workspace_d, size_t ws_bytes, void* stream);
+
+/*
  * emb_check_op_flag -- read and clear the flag word of the dense operators on the
  * current device, in one step after the work before it on `stream`, and synchronise
  * `stream`.  A bit that work of another stream raises meanwhile is reported by this

@@ -34,6 +34,7 @@ __all__ = [
     "emb_fp8_quantize", "emb_fp8_matmul", "emb_fp8_matmul_workspace_size", "emb_norm_gate_fwd", "emb_norm_gate_bwd",
     "emb_norm_gate_bwd_workspace_size", "emb_adamw_step", "AdamW", "emb_check_op_flag",
     "emb_fp4_quantize", "emb_fp4_dequantize", "emb_fp4_matmul", "emb_fp4_matmul_workspace_size",
+    "emb_muon_step", "emb_muon_workspace_size", "Muon", "EMB_MUON_MAX_DIM",
     "EMB_FLAG_OP_TIMEOUT", "EMB_FP8_BLOCK", "EMB_FP4_BLOCK", "EMB_ADAM_BLOCK", "EMB_NORM_MAX_DIM",
 ]
 
@@ -49,6 +50,7 @@ EMB_FP8_BLOCK = 128
 EMB_FP4_BLOCK = 32
 EMB_ADAM_BLOCK = 256
 EMB_NORM_MAX_DIM = 8192
+EMB_MUON_MAX_DIM = 65536
 BWD_PHASES = ("expand", "sort", "reduce", "fixup")
 _DTYPE = {"f32": 0, "f16": 1, "f16m": 2}   # f16m: f32 master rows + the f16 copy the forward reads
 _POOL = {"sum": 0, "mean": 1}
@@ -57,6 +59,7 @@ _FTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _NORM = {"rms": 0, "layer": 1}
 _ACT = {"identity": 0, "sigmoid": 1}
 _ADAM_STATE = {"f32": 0, "q8": 1}
+_MUON_PRODUCTS = {"half": 0, "split": 1}
 
 
 class LibraryNotBuilt(ImportError):
@@ -110,6 +113,16 @@ class _AdamwParams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
                 ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64), ("state", ctypes.c_int),
                 ("seed", ctypes.c_uint32), ("grad_scale", ctypes.c_void_p)]
+
+
+class _MuonTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("m", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("param_t", ctypes.c_int), ("grad_t", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class _MuonParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("nesterov", ctypes.c_int32), ("products", ctypes.c_int), ("grad_scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -178,6 +191,8 @@ def lib():
             "emb_norm_gate_bwd_workspace_size": [ctypes.POINTER(_NormGate), ctypes.POINTER(ctypes.c_size_t)],
             "emb_norm_gate_bwd": [ctypes.POINTER(_NormGate)] + [_vp] * 17 + [ctypes.c_size_t, _vp],
             "emb_adamw_step": [_vp, _vp, ctypes.c_int32, ctypes.POINTER(_AdamwParams), _vp],
+            "emb_muon_workspace_size": [_vp, ctypes.c_int32, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)],
+            "emb_muon_step": [_vp, _vp, ctypes.c_int32, ctypes.POINTER(_MuonParams), _vp, ctypes.c_size_t, _vp],
             "emb_check_op_flag": [_vp, ctypes.POINTER(ctypes.c_uint32)],
         }
         for name, args in sig.items():
@@ -1121,6 +1136,116 @@ class AdamW:
         p.step, p.grad_scale = self.step_count + 1, _dense(grad_scale, _F32, "grad_scale", self._dev)
         emb_adamw_step(self._tensors, ptrs.buffer_info()[0], p, stream, self._dev)
         self.step_count += 1
+
+
+def emb_muon_workspace_size(tensors, products: str = "half") -> int:
+    """Bytes of workspace for a ctypes array of _MuonTensor (Muon makes both)."""
+    b = ctypes.c_size_t()
+    _check(lib().emb_muon_workspace_size(tensors, len(tensors), _MUON_PRODUCTS[products], ctypes.byref(b)))
+    return b.value
+
+
+def emb_muon_step(tensors, grads, params: _MuonParams, workspace: torch.Tensor, stream=None, dev: Optional[int] = None) -> None:
+    """One step over a ctypes array of _MuonTensor and the address of an array of gradient pointers (Muon makes both)."""
+    _check(lib().emb_muon_step(tensors, grads, len(tensors), ctypes.byref(params), workspace.data_ptr(), workspace.nbytes,
+                               _raw_stream(stream, dev)))
+
+
+class Muon:
+    """Muon over a list of matrices: the momentum, orthogonalised by five
+    Newton-Schulz steps, is the update (emb_muon_step).  params: contiguous CUDA
+    matrices (float32, bfloat16 or float16), updated in place.  scale: of each update,
+    "rms" (0.2 sqrt(max(rows, cols)): a root mean square of 0.2, the size of AdamW's, so
+    its learning rates serve), "spectral" (sqrt(max(1, rows / cols))), or one number per
+    matrix.  products "half" (one float16 product each) or "split" (float32's accuracy,
+    three of them).  The momenta `m` (float32, one per matrix) are the
+    checkpoint; load_state sets them.  A parameter or momentum that is given other
+    storage is found by its address at the next step and described anew (the old storage
+    is held until then).  `workspace` is used by every step: steps must be ordered.  A
+    CUDA graph replays the rates and the addresses it was captured with."""
+
+    def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, momentum: float = 0.95, weight_decay: float = 0.0,
+                 nesterov: bool = True, scale="rms", products: str = "half"):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("params is empty")
+        for i, p in enumerate(self.params):
+            if p.dim() != 2:
+                raise ValueError(f"parameter {i} is not a matrix")
+        self.lr, self.momentum, self.weight_decay, self.nesterov, self.products = lr, momentum, weight_decay, nesterov, products
+        _MUON_PRODUCTS[products]
+        self._shapes = [tuple(p.shape) for p in self.params]
+        if scale == "rms":
+            self.scale = [0.2 * max(s) ** 0.5 for s in self._shapes]
+        elif scale == "spectral":
+            self.scale = [max(1.0, r / max(c, 1)) ** 0.5 for r, c in self._shapes]
+        else:
+            self.scale = [float(v) for v in scale]
+            if len(self.scale) != len(self.params):
+                raise ValueError("scale must have one entry per parameter")
+        self._dev = self.params[0].get_device()
+        if self._dev < 0:
+            raise ValueError("param must be a contiguous CUDA tensor")
+        self.device = self.params[0].device
+        self.m = [torch.zeros(s, dtype=_F32, device=self.device) for s in self._shapes]
+        self._devs = [self._dev] * len(self.params)
+        self._grad_dtypes = [p.dtype for p in self.params]
+        self.workspace = None
+        self._bind()
+
+    def _bind(self) -> None:
+        """Describes parameters and momenta to the library, as they are now.  An alias of each
+        is kept: as long as it lives no other tensor can come to lie at its address."""
+        if len(self.params) != len(self._shapes) or len(self.m) != len(self._shapes):
+            raise ValueError("the number of parameters or momenta has changed")
+        tensors = (_MuonTensor * len(self.params))()
+        for i, (p, m, s) in enumerate(zip(self.params, self.m, self._shapes)):
+            if tuple(p.shape) != s or tuple(m.shape) != s:
+                raise ValueError(f"parameter {i} was {list(s)}: it or its momentum has another shape")
+            tensors[i] = _MuonTensor(_dense(p, p.dtype, "param", self._dev), _dense(m, _F32, "m", self._dev), *s,
+                                     _ftype(p.dtype, "param"), _ftype(self._grad_dtypes[i], "grad"), self.scale[i])
+        used = [*self.params, *self.m]
+        for t in used:
+            if (t.storage_offset() + t.numel()) * t.itemsize > t.untyped_storage().nbytes():
+                raise ValueError("a parameter or momentum has lost its storage")
+        if self.workspace is None:
+            self.workspace = torch.empty(emb_muon_workspace_size(tensors, self.products), dtype=_U8, device=self.device)
+        self._tensors, self._addresses, self._aliases = tensors, list(map(torch.Tensor.data_ptr, used)), [t.detach() for t in used]
+
+    def load_state(self, m: Sequence[torch.Tensor]) -> None:
+        """Sets the momenta from one float32 tensor per parameter: all of them, or none if one does not fit."""
+        m = list(m)
+        if len(m) != len(self.params):
+            raise ValueError(f"m: expected {len(self.params)} tensors")
+        for part, s in zip(m, self._shapes):
+            if tuple(part.shape) != s or part.dtype is not _F32:
+                raise ValueError(f"m: expected float32 {list(s)}")
+        torch._foreach_copy_(self.m, m)
+
+    def step(self, grads: Sequence[torch.Tensor], grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+        """One step.  grads: one contiguous tensor per parameter, of its shape (float32,
+        bfloat16 or float16); grad_scale: device float32 scalar that multiplies them."""
+        T = torch.Tensor
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(self.params)} gradients are needed, got {len(grads)}")
+        if [tuple(g.shape) for g in grads] != self._shapes or not all(map(T.is_contiguous, grads)) or list(map(T.get_device, grads)) != self._devs:
+            raise ValueError(f"each gradient must be a contiguous tensor on cuda:{self._dev} of its parameter's shape")
+        if _current_device() != self._dev:
+            raise ValueError(f"the parameters are on cuda:{self._dev}, the current device is cuda:{_current_device()}")
+        if list(map(T.data_ptr, self.params)) + list(map(T.data_ptr, self.m)) != self._addresses:
+            self._bind()                    # a parameter or momentum has moved
+        dtypes = list(map(_dtype_of, grads))
+        if dtypes != self._grad_dtypes:
+            kinds = [_ftype(g, "grad") for g in dtypes]
+            for t, kind in zip(self._tensors, kinds):
+                t.grad_t = kind
+            self._grad_dtypes = dtypes
+        if grad_scale is not None and grad_scale.numel() != 1:
+            raise ValueError(f"grad_scale must have one element, got {grad_scale.numel()}")
+        ptrs = array.array("Q", map(T.data_ptr, grads))
+        params = _MuonParams(self.lr, self.momentum, self.weight_decay, int(self.nesterov), _MUON_PRODUCTS[self.products],
+                             _dense(grad_scale, _F32, "grad_scale", self._dev))
+        emb_muon_step(self._tensors, ptrs.buffer_info()[0], params, self.workspace, stream, self._dev)
 
 
 def emb_check_op_flag(stream=None) -> int:
