@@ -775,14 +775,44 @@ EMB_API emb_status emb_muon_step(const emb_muon_tensor* tensors, const void* con
                                  const emb_muon_params* params, void* workspace_d, size_t ws_bytes, void* stream);
 
 /*
+ * emb_token_fwd / emb_token_bwd -- rows of a plain embedding matrix W[vocab, dim] by
+ * token, without pooling, and the gradient of the matrix: for features of few values
+ * (position, hour, device) and for item sequences, which the dense optimizer trains
+ * (the table's lookup pools, and its backward updates without giving a gradient).
+ *   out[i] = scale * W[t_i]                       float32, rounded once to out_t
+ *   dW[v]  = scale * (sum over i with t_i = v of grad[i])     float32, rounded once to weight_t
+ * Rows that no token names get a gradient of zero; with accumulate != 0 the sums are added to what
+ * dW holds and the other rows are left alone.  A row's gradients are summed in float32 in an order
+ * that depends on the tokens alone, so results repeat bitwise.
+ *   tokens_d   token_t[n].  A token equal to `padding` (any number; -1 is usual) reads as zeros
+ *              and has no gradient.  Any other outside [0, vocab) does the same and raises EMB_FLAG_BAD_TOKEN
+ *              (emb_check_op_flag).
+ *   weight_d, dweight_d  rows ldw elements apart; out_d, grad_d rows ldo / ldg apart.
+ *   workspace_d  emb_token_bwd_workspace_size() bytes, 256-byte aligned; calls that share it
+ *              must be ordered.
+ * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED (n above EMB_MAX_TOKENS, vocab above 2^31 - 1, dim above 65,536), CUDA.
+ */
+typedef enum { EMB_I32 = 0, EMB_I64 = 1 } emb_itype;
+#define EMB_MAX_TOKENS 1073741823
+EMB_API emb_status emb_token_fwd(const void* weight_d, emb_ftype weight_t, int64_t vocab, int64_t dim, int64_t ldw,
+                                 const void* tokens_d, emb_itype token_t, int64_t n, int64_t padding, float scale,
+                                 void* out_d, emb_ftype out_t, int64_t ldo, void* stream);
+EMB_API emb_status emb_token_bwd_workspace_size(int64_t n, int64_t vocab, int64_t dim, size_t* bytes);
+EMB_API emb_status emb_token_bwd(const void* grad_d, emb_ftype grad_t, int64_t ldg, const void* tokens_d, emb_itype token_t,
+                                 int64_t n, int64_t padding, int64_t vocab, int64_t dim, float scale, int32_t accumulate,
+                                 void* dweight_d, emb_ftype weight_t, int64_t ldw, void* workspace_d, size_t ws_bytes,
+                                 void* stream);
+
+/*
  * emb_check_op_flag -- read and clear the flag word of the dense operators on the
  * current device, in one step after the work before it on `stream`, and synchronise
  * `stream`.  A bit that work of another stream raises meanwhile is reported by this
  * check or the next.  EMB_ERR_DEVICE_FLAG if a bit was
  * set since the last check: EMB_FLAG_OP_TIMEOUT, a kernel's bounded wait ran
- * out and its output is not valid.
+ * out and its output is not valid; EMB_FLAG_BAD_TOKEN, a token was neither a row nor the padding.
  */
 #define EMB_FLAG_OP_TIMEOUT 16u
+#define EMB_FLAG_BAD_TOKEN 32u
 EMB_API emb_status emb_check_op_flag(void* stream, uint32_t* flags_out);
 
 /*

@@ -35,6 +35,7 @@ __all__ = [
     "emb_norm_gate_bwd_workspace_size", "emb_adamw_step", "AdamW", "emb_check_op_flag",
     "emb_fp4_quantize", "emb_fp4_dequantize", "emb_fp4_matmul", "emb_fp4_matmul_workspace_size",
     "emb_muon_step", "emb_muon_workspace_size", "Muon", "EMB_MUON_MAX_DIM",
+    "emb_token_fwd", "emb_token_bwd", "emb_token_bwd_workspace_size", "EMB_FLAG_BAD_TOKEN", "EMB_MAX_TOKENS",
     "EMB_FLAG_OP_TIMEOUT", "EMB_FP8_BLOCK", "EMB_FP4_BLOCK", "EMB_ADAM_BLOCK", "EMB_NORM_MAX_DIM",
 ]
 
@@ -46,6 +47,8 @@ EMB_FLAG_PROBE_BOUND, EMB_FLAG_BAD_OFFSETS, EMB_FLAG_SLOT_MISMATCH, EMB_FLAG_BAD
 EMB_NOALLOC_SCRATCH_BYTES = 64 << 20
 EMB_SORT_DIGIT_BITS = 7
 EMB_FLAG_OP_TIMEOUT = 16
+EMB_FLAG_BAD_TOKEN = 32
+EMB_MAX_TOKENS = (1 << 30) - 1
 EMB_FP8_BLOCK = 128
 EMB_FP4_BLOCK = 32
 EMB_ADAM_BLOCK = 256
@@ -60,6 +63,7 @@ _NORM = {"rms": 0, "layer": 1}
 _ACT = {"identity": 0, "sigmoid": 1}
 _ADAM_STATE = {"f32": 0, "q8": 1}
 _MUON_PRODUCTS = {"half": 0, "split": 1}
+_ITYPE = {torch.int32: 0, torch.int64: 1}
 
 
 class LibraryNotBuilt(ImportError):
@@ -193,6 +197,11 @@ def lib():
             "emb_adamw_step": [_vp, _vp, ctypes.c_int32, ctypes.POINTER(_AdamwParams), _vp],
             "emb_muon_workspace_size": [_vp, ctypes.c_int32, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)],
             "emb_muon_step": [_vp, _vp, ctypes.c_int32, ctypes.POINTER(_MuonParams), _vp, ctypes.c_size_t, _vp],
+            "emb_token_fwd": [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, ctypes.c_int, _i64, _i64, ctypes.c_float, _vp, ctypes.c_int,
+                              _i64, _vp],
+            "emb_token_bwd_workspace_size": [_i64, _i64, _i64, ctypes.POINTER(ctypes.c_size_t)],
+            "emb_token_bwd": [_vp, ctypes.c_int, _i64, _vp, ctypes.c_int, _i64, _i64, _i64, _i64, ctypes.c_float, ctypes.c_int32,
+                              _vp, ctypes.c_int, _i64, _vp, ctypes.c_size_t, _vp],
             "emb_check_op_flag": [_vp, ctypes.POINTER(ctypes.c_uint32)],
         }
         for name, args in sig.items():
@@ -1246,6 +1255,82 @@ class Muon:
         params = _MuonParams(self.lr, self.momentum, self.weight_decay, int(self.nesterov), _MUON_PRODUCTS[self.products],
                              _dense(grad_scale, _F32, "grad_scale", self._dev))
         emb_muon_step(self._tensors, ptrs.buffer_info()[0], params, self.workspace, stream, self._dev)
+
+
+def _tokens(t: torch.Tensor, dev: int) -> Tuple[int, int]:
+    kind = _ITYPE.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"tokens must be int32 or int64, got {t.dtype}")
+    return _dense(t, t.dtype, "tokens", dev), kind
+
+
+def emb_token_fwd(weight: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0, padding: int = -1,
+                  out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """scale * weight[tokens], not pooled: out[*tokens.shape, dim] from weight[vocab, dim]
+    (rows may be strided) and contiguous int32 or int64 tokens.  A token equal to `padding`
+    reads as zeros; another one outside the matrix too, and raises EMB_FLAG_BAD_TOKEN
+    (emb_check_op_flag).  out: [tokens, dim] rows, may be strided."""
+    dev = _launch_device(weight, "weight")
+    ldw = _row_stride(weight, "weight", dev)
+    vocab, dim = weight.shape
+    tp, kind = _tokens(tokens, dev)
+    n = tokens.numel()
+    if out is None:
+        out = _empty(stream, weight, (*tokens.shape, dim), out_dtype or weight.dtype)
+        ldo = dim
+    else:
+        if out.shape != (n, dim):
+            raise ValueError(f"out must be [{n}, {dim}]")
+        ldo = _row_stride(out, "out", dev)
+    _check(lib().emb_token_fwd(weight.data_ptr(), _ftype(weight.dtype, "weight"), vocab, dim, ldw, tp, kind, n, padding, scale,
+                               out.data_ptr(), _ftype(out.dtype, "out"), ldo, _raw_stream(stream, dev)))
+    return out
+
+
+def emb_token_bwd_workspace_size(n: int, vocab: int, dim: int) -> int:
+    b = ctypes.c_size_t()
+    _check(lib().emb_token_bwd_workspace_size(n, vocab, dim, ctypes.byref(b)))
+    return b.value
+
+
+def emb_token_bwd(grad: torch.Tensor, tokens: torch.Tensor, vocab: int, scale: float = 1.0, padding: int = -1,
+                  dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient [vocab, dim] of emb_token_fwd's weight from grad, that of its output
+    ([*tokens.shape, dim], or [tokens, dim] with strided rows): sums over equal tokens,
+    bitwise repeatable, zeros for the other rows.  accumulate=True adds them to `out` and leaves
+    the other rows alone.  workspace: emb_token_bwd_workspace_size(tokens, vocab, dim) bytes that
+    the caller keeps; made for the call if None."""
+    dev = _launch_device(grad, "grad")
+    tp, kind = _tokens(tokens, dev)
+    n, dim = tokens.numel(), grad.shape[-1]
+    if grad.shape != (n, dim):
+        if grad.shape[:-1] != tokens.shape or not grad.is_contiguous():
+            raise ValueError(f"grad must be [{n}, dim], or contiguous {[*tokens.shape, 'dim']}")
+        grad = grad.view(n, dim)
+    ldg = _row_stride(grad, "grad", dev)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = _empty(stream, grad, (vocab, dim), dtype)
+        ldw = dim
+    else:
+        if out.shape != (vocab, dim):
+            raise ValueError(f"out must be [{vocab}, {dim}]")
+        ldw = _row_stride(out, "out", dev)
+    wp, ws_bytes = None, 0
+    if workspace is None:
+        ws_bytes = emb_token_bwd_workspace_size(n, vocab, dim)
+        if ws_bytes:
+            workspace = _empty(stream, grad, ws_bytes, _U8)
+            wp = workspace.data_ptr()
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{dev}")
+    else:
+        wp, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    _check(lib().emb_token_bwd(grad.data_ptr(), _ftype(grad.dtype, "grad"), ldg, tp, kind, n, padding, vocab, dim, scale, int(accumulate),
+                               out.data_ptr(), _ftype(out.dtype, "out"), ldw, wp, ws_bytes, _raw_stream(stream, dev)))
+    return out
 
 
 def emb_check_op_flag(stream=None) -> int:

@@ -675,6 +675,7 @@ extern "C" emb_status emb_check_op_flag(void* stream, uint32_t* flags_out) {
   EMB_CUDA(cudaMemcpyFromSymbolAsync(&f, g_op_taken, sizeof f, 0, cudaMemcpyDeviceToHost, st));
   EMB_CUDA(cudaStreamSynchronize(st));
   if (flags_out) *flags_out = f;
-  if (f) return fail(EMB_ERR_DEVICE_FLAG, "a dense operator's bounded wait ran out: its output is not valid");
+  if (f & EMB_FLAG_OP_TIMEOUT) return fail(EMB_ERR_DEVICE_FLAG, "a dense operator's bounded wait ran out: its output is not valid");
+  if (f) return fail(EMB_ERR_DEVICE_FLAG, "a token was neither a row of the matrix nor the padding");
   return EMB_OK;
 }
