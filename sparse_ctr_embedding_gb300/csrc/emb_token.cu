@@ -5,14 +5,13 @@
 //
 // The gradient.  The tokens are sorted by value, stably, so that a row's gradients are
 // summed in the order in which they came: results repeat bitwise and do not depend on
-// atomics.  Launches: a histogram of every digit (and a bit for each row that
-// occurs); one pass a digit, which ranks 4096 tokens a block and learns from the blocks
-// before it where its digits go; zeros into the rows that do not occur; the sums;
-// the joining of runs.
+// atomics.  Launches: a histogram of every digit; one pass a digit, which ranks 4096 tokens a
+// block and learns from the blocks before it where its digits go; other blocks of these
+// launches write zeros into dW meanwhile; the sums; the joining of runs.
 //
 // Sums.  Sorted positions are cut into chunks of equal length, so that a token which
 // occurs a hundred thousand times costs no block more than another.  A thread walks one
-// chunk for V neighbouring columns, eight rows of g on their way at a time.  A run of equal
+// chunk for V neighbouring columns, eight rows of g (four of 32 bytes) on their way at a time.  A run of equal
 // tokens inside a chunk is written at once; the piece of a run that began before the
 // chunk, and the piece of one that goes on after it, are left as float32 and joined, in order.
 #include <algorithm>
@@ -87,6 +86,31 @@ __device__ __forceinline__ void store_v(T* p, const float* v) {
   }
 }
 
+// V neighbouring elements as they lie in memory.
+template <typename T, int V>
+struct RawV {
+  T v[V];
+  __device__ __forceinline__ void load(const T* p) { v[0] = *p; }
+  __device__ __forceinline__ float get(int i) const { return to_f32<T>(v[i]); }
+};
+template <typename T>
+struct RawV<T, 8> : Raw8<T> {};
+template <typename T>
+struct RawV<T, 4> {
+  static constexpr int kWords = sizeof(T);
+  unsigned w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords == 4) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = u.x, w[1] = u.y;
+    }
+  }
+  __device__ __forceinline__ float get(int i) const { return to_f32<T>(reinterpret_cast<const T*>(w)[i]); }
+};
+
 // ------------------------------------------------------------------ lookup
 
 struct LookupArgs {
@@ -124,22 +148,62 @@ struct SortArgs {
   unsigned *hist;        // [kMaxPasses][kDigits]
   unsigned *next;        // [kMaxPasses]: the next tile of each pass
   unsigned *status;      // [passes][tiles][kDigits]: a tile's counts, alone or with all before it
-  unsigned *seen;        // a bit for each row
+  unsigned *valid;       // tokens that name rows
   unsigned *key[2], *val[2];
   int passes, bits, tiles;
 };
 
-__global__ void __launch_bounds__(256) histogram_kernel(const __grid_constant__ SortArgs a) {
+// Zeros into dW, before the sums are written.  The sort is a chain of latencies that leaves the memory
+// idle, so each of its launches has further blocks that write a share of them: one an SM, and
+// the first ones, as the sort's fill what they leave (behind those, the two took turns).
+struct ZeroArgs {
+  void* dw;
+  long long ldw, rows_a_launch, vocab;
+  int pieces, w_t, blocks;   // pieces of V elements, in a row; blocks 0: nothing to do
+};
+template <int V>
+__device__ __forceinline__ void zero_rows(const ZeroArgs& z, int launch, int block) {
+  const int lane = threadIdx.x & 31, more = 32 / z.pieces, rest = 32 - more * z.pieces, warps = z.blocks * (kSortThreads / 32);
+  const long long from = launch * z.rows_a_launch, to = min(z.vocab, from + z.rows_a_launch);
+  float zero[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) zero[j] = 0.0f;
+  for (long long w = from + (block * (kSortThreads / 32) + (threadIdx.x >> 5)) * 32LL; w < to; w += warps * 32LL) {  // 32 rows a warp
+    const int rows = (int)min(32LL, to - w);
+    int r = lane / z.pieces, p = lane - r * z.pieces;
+    while (r < rows) {
+      const long long e = (w + r) * z.ldw + p * V;
+      if (z.w_t == EMB_T_F32) store_v<float, V>((float*)z.dw + e, zero);
+      else if (z.w_t == EMB_T_BF16) store_v<__nv_bfloat16, V>((__nv_bfloat16*)z.dw + e, zero);
+      else store_v<__half, V>((__half*)z.dw + e, zero);
+      r += more;
+      p += rest;
+      if (p >= z.pieces) p -= z.pieces, ++r;
+    }
+  }
+}
+
+// Eight tokens a thread at a time, all loads before any use.
+template <int V>
+__global__ void __launch_bounds__(256) histogram_kernel(const __grid_constant__ SortArgs a, const __grid_constant__ ZeroArgs z, int blocks) {
+  constexpr int kBatch = 8;
   __shared__ unsigned h[kMaxPasses * kDigits];
+  if ((int)blockIdx.x < z.blocks) {
+    zero_rows<V>(z, a.passes, blockIdx.x);
+    return;
+  }
   for (int i = threadIdx.x; i < a.passes * kDigits; i += 256) h[i] = 0;
   __syncthreads();
   const unsigned mask = (1u << a.bits) - 1;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < a.t.n; i += (long long)gridDim.x * 256) {
-    const long long t = token_at(a.t, i);
-    if (!names_row(a.t, t)) continue;
-    const unsigned k = (unsigned)t;
-    for (int p = 0; p < a.passes; ++p) atomicAdd(&h[p * kDigits + ((k >> (p * a.bits)) & mask)], 1u);
-    if (!((*(volatile unsigned*)(a.seen + (k >> 5)) >> (k & 31)) & 1u)) atomicOr(a.seen + (k >> 5), 1u << (k & 31));
+  for (long long i = (long long)(blockIdx.x - z.blocks) * 256 * kBatch + threadIdx.x; i < a.t.n; i += (long long)blocks * 256 * kBatch) {
+    long long t[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) t[q] = i + q * 256 < a.t.n ? token_at(a.t, i + q * 256) : a.t.padding;
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      if (!names_row(a.t, t[q])) continue;
+      for (int p = 0; p < a.passes; ++p) atomicAdd(&h[p * kDigits + (((unsigned)t[q] >> (p * a.bits)) & mask)], 1u);
+    }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < a.passes * kDigits; i += 256)
@@ -169,9 +233,14 @@ __device__ __forceinline__ unsigned scan256(unsigned v, unsigned* warp_sums, uns
 
 // One stable pass.  Tiles are numbered as they start, so those before one are at work or
 // done, and what it waits for comes; the wait is bounded all the same.
-template <bool FIRST>
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ SortArgs a, int pass) {
+template <bool FIRST, int V>
+__global__ void __launch_bounds__(kSortThreads, 4) sort_kernel(const __grid_constant__ SortArgs a, const __grid_constant__ ZeroArgs z, int pass) {
+  if ((int)blockIdx.x < z.blocks) {
+    zero_rows<V>(z, pass, blockIdx.x);
+    return;
+  }
   __shared__ unsigned count[8][kDigits], base[kDigits], sums[8];
+  __shared__ uint2 held[kSortTile];
   __shared__ int tile_slot;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, d = threadIdx.x;
   if (threadIdx.x == 0) tile_slot = (int)atomicAdd(a.next + pass, 1u);
@@ -185,7 +254,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
   const unsigned *key = a.key[(pass & 1) ^ 1], *val = a.val[(pass & 1) ^ 1];
   const int shift = pass * a.bits;
   const unsigned mask = (1u << a.bits) - 1;
-  unsigned k[kSortItems], v[kSortItems], rank[kSortItems];
+  unsigned k[kSortItems], v[kSortItems], rank[kSortItems / 2];   // ranks: two to a word
   unsigned in = 0;
 #pragma unroll
   for (int q = 0; q < kSortItems; ++q) {
@@ -216,7 +285,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     __syncwarp();
     if (ok && below == 0) count[w][digit] = old + __popc(same);
     __syncwarp();
-    rank[q] = old + below;
+    if (q & 1) rank[q / 2] |= (old + below) << 16;
+    else rank[q / 2] = old + below;
   }
   __syncthreads();
   unsigned mine = 0;
@@ -227,33 +297,56 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     mine += c;
   }
   unsigned* st = a.status + ((long long)pass * a.tiles + tile) * kDigits + d;
-  unsigned before = 0;
-  if (d <= mask) {
-    *(volatile unsigned*)st = mine | (tile == 0 ? kInclusive : kAggregate);
-    for (int j = tile - 1; j >= 0; --j) {
-      const volatile unsigned* s = st - (long long)(tile - j) * kDigits;
-      unsigned word = *s;
-      for (unsigned i = 0; word < kAggregate && i < kWaitLimit; ++i) word = *s;
-      if (word < kAggregate) {  // the wait ran out
-        atomicOr(a.t.flags, EMB_FLAG_OP_TIMEOUT);
-        break;
-      }
-      before += word & kCount;
-      if (word >= kInclusive) break;
-    }
-    if (tile) *(volatile unsigned*)st = (before + mine) | kInclusive;
-  }
-  base[d] = first + before;
+  if (d <= mask) *(volatile unsigned*)st = mine | (tile == 0 ? kInclusive : kAggregate);
+  // The tile in the order of its digits, in shared memory: a digit's items then leave as
+  // neighbours (each from its own lane, a sector an item: twice the time).
+  unsigned all;
+  const unsigned local = scan256(mine, sums, &all);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) count[j][d] += local;
   __syncthreads();
-  unsigned *ok_ = a.key[pass & 1], *ov = a.val[pass & 1];
 #pragma unroll
   for (int q = 0; q < kSortItems; ++q) {
     if ((in >> q) & 1u) {
-      const unsigned digit = (k[q] >> shift) & mask, to = base[digit] + count[w][digit] + rank[q];
-      if (to < valid) {  // always, unless a wait ran out
-        ok_[to] = k[q];
-        ov[to] = v[q];
+      const unsigned to = count[w][(k[q] >> shift) & mask] + (q & 1 ? rank[q / 2] >> 16 : rank[q / 2] & 0xffffu);
+      held[to] = make_uint2(k[q], v[q]);
+    }
+  }
+  unsigned before = 0;
+  if (d <= mask) {
+    // 16 tiles' words at a time: one after the other, each a round trip to L2, they took
+    // most of a pass.  A word that is not there yet is asked for again, from it on.
+    constexpr int kLook = 16;
+    int j = tile - 1;
+    for (unsigned i = 0; j >= 0 && i < kWaitLimit; ++i) {
+      unsigned word[kLook];
+#pragma unroll
+      for (int q = 0; q < kLook; ++q)
+        word[q] = q <= j ? *(volatile unsigned*)(st - (long long)(tile - j + q) * kDigits) : (unsigned)kInclusive;
+      bool more = true;
+#pragma unroll
+      for (int q = 0; q < kLook; ++q) {
+        if (more && word[q] >= kAggregate) {
+          before += word[q] & kCount;
+          --j;
+          if (word[q] >= kInclusive) j = -1;
+        }
+        more = more && word[q] >= kAggregate && word[q] < kInclusive;
       }
+    }
+    if (j >= 0) atomicOr(a.t.flags, EMB_FLAG_OP_TIMEOUT);     // the wait ran out
+    if (tile) *(volatile unsigned*)st = (before + mine) | kInclusive;
+  }
+  base[d] = first + before - local;                           // less the item's place in the tile
+  if (FIRST && tile == 0 && d == 0) *a.valid = valid;
+  __syncthreads();
+  unsigned *to_key = a.key[pass & 1], *to_val = a.val[pass & 1];
+  for (unsigned i = threadIdx.x; i < all; i += kSortThreads) {
+    const uint2 item = held[i];
+    const unsigned to = base[(item.x >> shift) & mask] + i;
+    if (to < valid) {  // always, unless a wait ran out
+      to_key[to] = item.x;
+      to_val[to] = item.y;
     }
   }
 }
@@ -261,25 +354,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
 // ------------------------------------------------------------------ sums
 
 struct SumArgs {
-  const unsigned *key, *val, *hist, *seen;
+  const unsigned *key, *val, *valid;
   const void* g;
   void* dw;
   float *head, *tail;    // [chunks][dim]
-  long long ldg, ldw, vocab;
+  long long ldg, ldw, n;   // n: all tokens
   int dim, pieces, w_t, accumulate;
   float scale;
 };
-
-__device__ __forceinline__ unsigned valid_of(const unsigned* hist) {
-  __shared__ unsigned all;
-  if (threadIdx.x == 0) all = 0;
-  __syncthreads();
-  unsigned v = threadIdx.x < kDigits ? hist[threadIdx.x] : 0;
-  v = __reduce_add_sync(0xffffffffu, v);
-  if ((threadIdx.x & 31) == 0) atomicAdd(&all, v);
-  __syncthreads();
-  return all;
-}
 
 template <int V>
 __device__ __forceinline__ void write_row(const SumArgs& a, unsigned row, int piece, float* acc) {
@@ -304,7 +386,7 @@ __device__ __forceinline__ void write_row(const SumArgs& a, unsigned row, int pi
 
 template <typename GT, int V>
 __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArgs a) {
-  const unsigned n = valid_of(a.hist);
+  const unsigned n = *a.valid;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const long long chunk = i / a.pieces;
   const int piece = (int)(i - chunk * a.pieces);
@@ -316,34 +398,40 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArg
 #pragma unroll
   for (int j = 0; j < V; ++j) acc[j] = 0.0f;
   float* const hp = a.head + chunk * a.dim + piece * V;
-  auto flush = [&](float* to) {
+  auto flush = [&](float* to) { store_v<float, V>(to, acc); };
+  constexpr int kRows = V * sizeof(GT) > 16 ? 4 : 8;   // on their way at a time
+  unsigned k[kRows], v[kRows];
+  auto ask = [&](unsigned b) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) to[j] = acc[j];
-  };
-  for (unsigned b = s; b < e; b += 8) {
-    unsigned k[8], v[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < kRows; ++q) {
       const unsigned at = min(b + q, e - 1);
       k[q] = __ldg(a.key + at);
       v[q] = __ldg(a.val + at);
     }
-    float x[8][V];
+  };
+  ask(s);
+  for (unsigned b = s; b < e; b += kRows) {
+    RawV<GT, V> x[kRows];
+    unsigned now[kRows];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) load_v<GT, V>((const GT*)a.g + v[q] * a.ldg + piece * V, x[q]);
+    for (int q = 0; q < kRows; ++q) {
+      x[q].load((const GT*)a.g + v[q] * a.ldg + piece * V);
+      now[q] = k[q];
+    }
+    if (b + kRows < e) ask(b + kRows);                  // the next ones' places, while these are on their way
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < kRows; ++q) {
       if (b + q < e) {
-        if (k[q] != cur) {
+        if (now[q] != cur) {
           if (head) flush(hp);
           else write_row<V>(a, cur, piece, acc);
           head = false;
-          cur = k[q];
+          cur = now[q];
 #pragma unroll
           for (int j = 0; j < V; ++j) acc[j] = 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] += x[q][j];
+        for (int j = 0; j < V; ++j) acc[j] += x[q].get(j);
       }
     }
   }
@@ -352,73 +440,97 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArg
   else write_row<V>(a, cur, piece, acc);
 }
 
-// Runs that pass a chunk's end: a block takes the one that begins in its chunk, if there
-// is one.  Groups of threads add consecutive shares of its pieces, and then the shares.
-template <int V>
-__global__ void __launch_bounds__(256) join_runs_kernel(const __grid_constant__ SumArgs a) {
-  extern __shared__ float share[];   // [groups][columns of this block]
-  const unsigned n = valid_of(a.hist);
-  const long long chunk = blockIdx.x;
-  const long long e = (chunk + 1) * kChunk;
-  if (e >= n) return;
-  const unsigned cur = a.key[e];
-  if (a.key[e - 1] != cur) return;                                       // no run passes the end
-  if (a.key[e - kChunk] == cur && chunk > 0 && a.key[e - kChunk - 1] == cur) return;  // it began before
-  // the last chunk whose first token is `cur`
-  const long long chunks = (n + kChunk - 1) / kChunk;
-  long long lo = chunk + 1, hi = chunks - 1;
-  while (lo < hi) {
-    const long long mid = (lo + hi + 1) >> 1;
-    if (a.key[mid * kChunk] == cur) lo = mid;
-    else hi = mid - 1;
-  }
-  const int last = (int)lo, heads = last - (int)chunk;
-  for (int p0 = 0; p0 < a.pieces; p0 += 256) {
-    const int width = min(256, a.pieces - p0), groups = min(256 / width, heads), g = threadIdx.x / width, piece = p0 + threadIdx.x % width;
+// Joins the run that passes the end of `chunk` and begins in it: its tail here and the heads of the
+// chunks up to `last`.  `threads` threads (this one is the `me`-th) take columns, and where
+// those are fewer, groups of them take consecutive shares of the heads, added in order.
+template <int V, typename Sync>
+__device__ __forceinline__ void join_run(const SumArgs& a, unsigned row, long long chunk, int last, int threads, int me, float* share, Sync sync) {
+  const int heads = last - (int)chunk;
+  for (int p0 = 0; p0 < a.pieces; p0 += threads) {
+    const int width = min(threads, a.pieces - p0), groups = min(threads / width, heads), g = me / width, piece = p0 + me % width;
     float acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.0f;
     if (g < groups) {
       const int from = (int)chunk + 1 + (int)((long long)heads * g / groups), to = (int)chunk + 1 + (int)((long long)heads * (g + 1) / groups);
-      if (g == 0) {
+      if (g == 0) load_v<float, V>(a.tail + chunk * a.dim + piece * V, acc);
+      int c = from;
+      for (; c + 4 <= to; c += 4) {
+        float x[4][V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] = a.tail[chunk * a.dim + piece * V + j];
+        for (int q = 0; q < 4; ++q) load_v<float, V>(a.head + (long long)(c + q) * a.dim + piece * V, x[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int j = 0; j < V; ++j) acc[j] += x[q][j];
       }
-#pragma unroll 8
-      for (int c = from; c < to; ++c) {
+      for (; c < to; ++c) {
+        float x[V];
+        load_v<float, V>(a.head + (long long)c * a.dim + piece * V, x);
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] += a.head[(long long)c * a.dim + piece * V + j];
+        for (int j = 0; j < V; ++j) acc[j] += x[j];
       }
 #pragma unroll
-      for (int j = 0; j < V; ++j) share[(g * width + threadIdx.x % width) * V + j] = acc[j];
+      for (int j = 0; j < V; ++j) share[me * V + j] = acc[j];
     }
-    __syncthreads();
-    if (threadIdx.x < width) {
+    sync();
+    if (me < width) {
 #pragma unroll
       for (int j = 0; j < V; ++j) acc[j] = 0.0f;
       for (int q = 0; q < groups; ++q)
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] += share[(q * width + threadIdx.x) * V + j];
-      write_row<V>(a, cur, piece, acc);
+        for (int j = 0; j < V; ++j) acc[j] += share[(q * width + me) * V + j];
+      write_row<V>(a, row, piece, acc);
     }
-    __syncthreads();
+    sync();
   }
 }
 
-// Zeros into the rows that no token names.
+// Runs that pass a chunk's end.  A warp takes the one that begins in its chunk, if there is
+// one; a run of many chunks is left to the whole block.
 template <int V>
-__global__ void __launch_bounds__(256) zero_rows_kernel(const __grid_constant__ SumArgs a) {
-  const long long total = a.vocab * a.pieces;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
-    const long long row = total <= 0xffffffffLL ? (unsigned)i / (unsigned)a.pieces : i / a.pieces;
-    const long long e = row * a.ldw + (i - row * a.pieces) * V;
-    if ((__ldg(a.seen + (row >> 5)) >> (row & 31)) & 1u) continue;
-    float z[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) z[j] = 0.0f;
-    if (a.w_t == EMB_T_F32) store_v<float, V>((float*)a.dw + e, z);
-    else if (a.w_t == EMB_T_BF16) store_v<__nv_bfloat16, V>((__nv_bfloat16*)a.dw + e, z);
-    else store_v<__half, V>((__half*)a.dw + e, z);
+__global__ void __launch_bounds__(256, 5) join_runs_kernel(const __grid_constant__ SumArgs a) {
+  constexpr int kLong = 64;             // chunks
+  __shared__ float share[256 * V];
+  __shared__ int last_of[8];            // of a warp's run that is long, else -1
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long chunk = blockIdx.x * 8LL + warp, e = (chunk + 1) * kChunk;
+  // All that the usual run needs is asked for at once: keys past the valid ones are there, but mean nothing.
+  const unsigned n = *a.valid;
+  const long long ahead = e + lane * (long long)kChunk;
+  const unsigned start = ahead < a.n ? a.key[ahead] : 0;                // of the chunks that follow, one a lane
+  unsigned here = 0, first = 0, before = 0;
+  if (e < a.n) {
+    here = a.key[e - 1];
+    first = a.key[e - kChunk];
+    before = chunk > 0 ? a.key[e - kChunk - 1] : ~0u;
+  }
+  const int chunks = (int)((n + kChunk - 1LL) / kChunk);
+  if (blockIdx.x * 8LL >= chunks) return;
+  const unsigned cur = __shfl_sync(0xffffffffu, start, 0);
+  // a run passes the end, and it began here
+  const bool have = e < n && here == cur && !(first == cur && before == cur);
+  int lo = (int)chunk + 1;
+  if (have) {  // the last chunk whose first token is `cur`
+    int hi = chunks - 1;
+    const unsigned same = __ballot_sync(0xffffffffu, ahead < n && start == cur);
+    lo += __popc(same) - 1;
+    if (same != ~0u) hi = lo;
+    while (lo < hi) {  // 32 places at a time
+      const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+      const unsigned more = __ballot_sync(0xffffffffu, at <= hi && a.key[(long long)at * kChunk] == cur);
+      lo += __popc(more) * step;
+      hi = min(hi, lo + step - 1);
+    }
+  }
+  const bool is_long = have && lo - (int)chunk > kLong;
+  if (lane == 0) last_of[warp] = is_long ? lo : -1;
+  if (have && !is_long) join_run<V>(a, cur, chunk, lo, 32, lane, share + warp * 32 * V, [] { __syncwarp(); });
+  __syncthreads();
+  for (int w = 0; w < 8; ++w) {
+    if (last_of[w] < 0) continue;       // the same for the block
+    const long long c = blockIdx.x * 8LL + w;
+    join_run<V>(a, a.key[(c + 1) * kChunk], c, last_of[w], 256, threadIdx.x, share, [] { __syncthreads(); });
   }
 }
 
@@ -427,8 +539,8 @@ __global__ void __launch_bounds__(256) zero_rows_kernel(const __grid_constant__ 
 struct TokenPlan {
   int passes = 0, bits = 0, tiles = 0;
   long long chunks = 0;
-  size_t zero_bytes = 0;  // hist, next, status, seen, from the start on
-  size_t next = 0, status = 0, seen = 0, key[2] = {}, val[2] = {}, head = 0, tail = 0, bytes = 0;
+  size_t zero_bytes = 0;  // hist, next, status, from the start on
+  size_t next = 0, status = 0, key[2] = {}, val[2] = {}, head = 0, tail = 0, bytes = 0;
 };
 
 TokenPlan plan_tokens(long long n, long long vocab, long long dim) {
@@ -443,8 +555,7 @@ TokenPlan plan_tokens(long long n, long long vocab, long long dim) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   pl.next = kMaxPasses * kDigits * 4;
   pl.status = pl.next + 256;
-  pl.seen = pl.status + (size_t)pl.passes * pl.tiles * kDigits * 4;
-  pl.zero_bytes = pl.seen + up((size_t)(vocab + 31) / 32 * 4);
+  pl.zero_bytes = pl.status + (size_t)pl.passes * pl.tiles * kDigits * 4;
   size_t at = pl.zero_bytes;
   for (int j = 0; j < 2; ++j) {
     pl.key[j] = at;
@@ -507,15 +618,19 @@ cudaError_t launch_sums(const SumArgs& a, long long chunks, cudaStream_t st) {
   sum_kernel<GT, V><<<(unsigned)blocks, 256, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (chunks > 1) join_runs_kernel<V><<<(unsigned)(chunks - 1), 256, 256 * V * 4, st>>>(a);
+  if (chunks > 1) join_runs_kernel<V><<<(unsigned)((chunks + 7) / 8), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 template <int V>
-cudaError_t launch_grad(const SumArgs& a, emb_ftype g_t, long long chunks, cudaStream_t st) {
-  if (!a.accumulate) {
-    const int grid = (int)std::min<long long>((a.vocab * a.pieces + 255) / 256, 32LL * sm_count());
-    zero_rows_kernel<V><<<grid, 256, 0, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
+cudaError_t launch_grad(const SortArgs& s, const ZeroArgs& z, const SumArgs& a, emb_ftype g_t, long long chunks, cudaStream_t st) {
+  const int blocks = (int)std::min<long long>((a.n + 2047) / 2048, 8LL * sm_count());
+  histogram_kernel<V><<<blocks + z.blocks, 256, 0, st>>>(s, z, blocks);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  for (int p = 0; p < s.passes; ++p) {
+    if (p == 0) sort_kernel<true, V><<<s.tiles + z.blocks, kSortThreads, 0, st>>>(s, z, p);
+    else sort_kernel<false, V><<<s.tiles + z.blocks, kSortThreads, 0, st>>>(s, z, p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   if (g_t == EMB_T_F32) return launch_sums<float, V>(a, chunks, st);
@@ -588,24 +703,21 @@ extern "C" emb_status emb_token_bwd(const void* grad_d, emb_ftype grad_t, int64_
   if ((pl.chunks * (dim / v) + 255) / 256 > 0x7fffffffLL) return fail(EMB_ERR_UNSUPPORTED, "n * dim too large");
   unsigned char* ws = (unsigned char*)workspace_d;
   SortArgs s{{tokens_d, n, vocab, padding, token_t == EMB_I64, flags},
-             (unsigned*)ws, (unsigned*)(ws + pl.next), (unsigned*)(ws + pl.status), (unsigned*)(ws + pl.seen), {}, {}, pl.passes, pl.bits, pl.tiles};
+             (unsigned*)ws, (unsigned*)(ws + pl.next), (unsigned*)(ws + pl.status), (unsigned*)(ws + pl.next) + kMaxPasses, {}, {}, pl.passes, pl.bits, pl.tiles};
   for (int j = 0; j < 2; ++j) {
     s.key[j] = (unsigned*)(ws + pl.key[j]);
     s.val[j] = (unsigned*)(ws + pl.val[j]);
   }
   EMB_CUDA(cudaMemsetAsync(ws, 0, pl.zero_bytes, st));
-  histogram_kernel<<<(int)std::min<long long>((n + 2047) / 2048, 4LL * sm_count()), 256, 0, st>>>(s);
-  EMB_CUDA(cudaGetLastError());
-  for (int p = 0; p < pl.passes; ++p) {
-    if (p == 0) sort_kernel<true><<<pl.tiles, kSortThreads, 0, st>>>(s, p);
-    else sort_kernel<false><<<pl.tiles, kSortThreads, 0, st>>>(s, p);
-    EMB_CUDA(cudaGetLastError());
-  }
   const int end = (pl.passes - 1) & 1;
-  const SumArgs a{s.key[end], s.val[end], s.hist, s.seen, grad_d, dweight_d, (float*)(ws + pl.head), (float*)(ws + pl.tail),
-                  ldg, ldw, vocab, (int)dim, (int)dim / v, weight_t, accumulate != 0, scale};
-  const cudaError_t e = v == 8 ? launch_grad<8>(a, grad_t, pl.chunks, st) : v == 4 ? launch_grad<4>(a, grad_t, pl.chunks, st)
-                                                                                   : launch_grad<1>(a, grad_t, pl.chunks, st);
+  const SumArgs a{s.key[end], s.val[end], s.valid, grad_d, dweight_d, (float*)(ws + pl.head), (float*)(ws + pl.tail),
+                  ldg, ldw, n, (int)dim, (int)dim / v, weight_t, accumulate != 0, scale};
+  // blocks that write zeros: 32 rows a warp, one block an SM at most
+  const long long share = (vocab + pl.passes) / (pl.passes + 1);
+  const ZeroArgs z{dweight_d, ldw, share, vocab, (int)dim / v, weight_t,
+                   accumulate ? 0 : (int)std::min<long long>((share + kSortThreads - 1) / kSortThreads, sm_count())};
+  const cudaError_t e = v == 8 ? launch_grad<8>(s, z, a, grad_t, pl.chunks, st) : v == 4 ? launch_grad<4>(s, z, a, grad_t, pl.chunks, st)
+                                                                                         : launch_grad<1>(s, z, a, grad_t, pl.chunks, st);
   if (e != cudaSuccess) return cuda_fail(e, "emb_token_bwd launch");
   return EMB_OK;
 }
