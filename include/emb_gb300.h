@@ -828,22 +828,25 @@ EMB_API emb_status emb_check_op_flag(void* stream, uint32_t* flags_out);
  *    1 <= bound <= max_cluster + 1, as a corrupted table would have it: a key
  *    further than `bound` slots from its home then misses and raises
  *    EMB_FLAG_PROBE_BOUND, and no probe inspects more than `bound` slots.
- *  - emb_debug_lose_op_wait(role, step): in the tiled products of emb_fp8_matmul
- *    launched from now on, a wait of each block counts as run out at this step
+ *  - emb_debug_lose_op_wait(role, step): in the tiled products of emb_fp8_matmul, emb_fp4_matmul and
+ *    emb_muon_step launched from now on, a wait of each block counts as run out at this step
  *    (from 0; a step is 128 k's of one tile): role 0 that of the warp that loads
  *    the operands, 1 of the one that issues the products, 2 of the one that loads
- *    the scales; role 3, whatever the step: another one, when the last loads are
+ *    the scales (emb_fp8_matmul only); role 3, whatever the step: another one, when the last loads are
  *    on their way.  The products then end early and raise EMB_FLAG_OP_TIMEOUT.
  *    role -1: none (the default).  Process-wide.
  *  - emb_debug_fp8_matmul_plan(m, n, k, plan): how emb_fp8_matmul splits a
  *    product on the current device: plan[0] columns of a tile (0: no tiles), [1]
  *    tiles, [2] blocks, [3] steps of a block (0: whole tiles, in turn).
+ *  - emb_debug_fp4_matmul_plan(m, n, k, plan): the same of emb_fp4_matmul; plan[2] counts
+ *    workers and plan[4] is the blocks of a worker (2: a pair of SMs, tiles of 256 rows).
  */
 EMB_API emb_status emb_debug_fail_device_alloc(int64_t after);
 EMB_API int64_t emb_debug_live_device_allocs(void);
 EMB_API emb_status emb_debug_set_probe_bound(emb_table* table, int64_t bound);
 EMB_API emb_status emb_debug_lose_op_wait(int32_t role, int64_t step);
 EMB_API emb_status emb_debug_fp8_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t* plan);
+EMB_API emb_status emb_debug_fp4_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t* plan);
 
 /* Human-readable status name, and the calling thread's last error message
  * (no counterpart in the pages). */

@@ -26,7 +26,7 @@ __all__ = [
     "emb_lookup_fwd", "emb_lookup_fwd_record", "emb_lookup_fwd_dedup", "emb_bwd_adagrad_recorded", "emb_bwd_workspace_size", "emb_bwd_adagrad", "emb_bwd_adagrad_noalloc",
     "emb_bwd_ftrl", "emb_bwd_ftrl_recorded", "emb_table_export_z", "emb_table_import_z",
     "emb_debug_fail_device_alloc", "emb_debug_live_device_allocs", "emb_debug_set_probe_bound", "emb_debug_lose_op_wait",
-    "emb_debug_fp8_matmul_plan", "Pipeline",
+    "emb_debug_fp8_matmul_plan", "emb_debug_fp4_matmul_plan", "Pipeline",
     "emb_bwd_unique_keys", "emb_bwd_phase_events", "EMB_NOALLOC_SCRATCH_BYTES", "EMB_SORT_DIGIT_BITS", "BWD_PHASES",
     "emb_resolve", "emb_table_export", "emb_table_export_rows", "emb_table_slots", "emb_check_device_flag",
     "emb_status_string", "emb_last_error",
@@ -176,6 +176,7 @@ def lib():
             "emb_debug_set_probe_bound": [_vp, _i64],
             "emb_debug_lose_op_wait": [ctypes.c_int32, _i64],
             "emb_debug_fp8_matmul_plan": [_i64, _i64, _i64, ctypes.POINTER(_i64)],
+            "emb_debug_fp4_matmul_plan": [_i64, _i64, _i64, ctypes.POINTER(_i64)],
             "emb_table_import_z": [_vp, _vp, _vp],
             "emb_resolve": [_vp, _vp, _i64, _vp, _vp, _vp],
             "emb_table_export": [_vp, _vp, _vp, _vp, _vp],
@@ -558,6 +559,13 @@ def emb_debug_fp8_matmul_plan(m: int, n: int, k: int) -> Tuple[int, int, int, in
     """(columns of a tile or 0, tiles, blocks, steps of a block or 0 for whole tiles) of an emb_fp8_matmul."""
     plan = (_i64 * 4)()
     _check(lib().emb_debug_fp8_matmul_plan(m, n, k, plan))
+    return tuple(plan)
+
+
+def emb_debug_fp4_matmul_plan(m: int, n: int, k: int) -> Tuple[int, int, int, int, int]:
+    """(columns of a tile or 0, tiles, workers, steps of a worker or 0 for whole tiles, blocks of a worker) of an emb_fp4_matmul."""
+    plan = (_i64 * 5)()
+    _check(lib().emb_debug_fp4_matmul_plan(m, n, k, plan))
     return tuple(plan)
 
 

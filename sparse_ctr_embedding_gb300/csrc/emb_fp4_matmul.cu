@@ -64,6 +64,45 @@ __device__ __forceinline__ void tc_copy_scales(unsigned d, unsigned long long de
 __device__ __forceinline__ unsigned long long scale_desc(unsigned addr) {
   return (unsigned long long)((addr >> 4) & 0x3FFF) | (8ull << 32) | (1ull << 46);
 }
+__device__ __forceinline__ void tc_mma4_pair(unsigned d, unsigned long long a, unsigned long long b, unsigned idesc, unsigned sa,
+                                             unsigned sb, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "setp.ne.b32 p, %6, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((unsigned)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_copy_scales_pair(unsigned d, unsigned long long desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(d), "l"(desc) : "memory");
+}
+
+// A step's copies of scales and products, `left` k's of it (a constant for a whole one).  ROWS: tiles
+// of scales of 128 rows, a's and b's; a block of 128 k's has a's scales in four TMEM columns,
+// and b's tiles side by side.
+template <int ROWS, bool PAIR>
+__device__ __forceinline__ void issue_step4(unsigned d, unsigned long long da, unsigned long long db, unsigned idesc, unsigned long long ds,
+                                            unsigned ts, unsigned half_cols, bool add, int left) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (h * 128 < left) {
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        const unsigned to = ts + (j == 0 ? h * 4 : 8 + h * 4 * (ROWS - 1) + (j - 1) * 4);
+        if (PAIR) tc_copy_scales_pair(to, ds + (j * 1024 + h * 512) / 16);
+        else tc_copy_scales(to, ds + (j * 1024 + h * 512) / 16);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kBK / 64; ++j) {
+    if (j * 64 < left) {
+      const unsigned id = (j & 1) * 2u, h = j >> 1, sa = ts + h * 4, sb = ts + 8 + h * 4 * (ROWS - 1) + half_cols;
+      if (PAIR) tc_mma4_pair(d, da + 2 * j, db + 2 * j, idesc | (id << 4) | (id << 29), sa, sb, add || j > 0);
+      else tc_mma4(d, da + 2 * j, db + 2 * j, idesc | (id << 4) | (id << 29), sa, sb, add || j > 0);
+    }
+  }
+}
 __device__ __forceinline__ void bulk_load(unsigned dst, const void* src, unsigned bytes, unsigned bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                "r"(bytes), "r"(bar)
@@ -129,14 +168,14 @@ __global__ void __launch_bounds__(kThreads, 1) tile4_kernel(const __grid_constan
   const unsigned tmem = tmem_slot, tscales = tmem + C::kAccs * BN;
 
   long long pos, end;
-  my_range(p, &pos, &end);
+  my_range(p, &pos, &end, blockIdx.x);
   Unit u;
 
   if (warp == kTmaWarp) {
     unsigned it = 0;
     bool go = true;
     const int last_b = (p.n - 1) >> 7;  // b's last tile of scales
-    while (go && next_unit(p, &pos, end, &u)) {
+    while (go && next_unit(p, &pos, end, &u, gridDim.x)) {
       for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
         const unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
         go = __all_sync(0xffffffffu, p.lost_warp == kTmaWarp && p.lost_step == it ? give_up(stop, p.flags)
@@ -166,44 +205,36 @@ __global__ void __launch_bounds__(kThreads, 1) tile4_kernel(const __grid_constan
     constexpr unsigned idesc = (1u << 7) | (1u << 10) | ((BN >> 3) << 17) | (1u << 23) | ((kBM >> 4) << 24);
     unsigned it = 0, tile = 0;
     bool go = true;
-    while (go && next_unit(p, &pos, end, &u)) {
+    while (go && next_unit(p, &pos, end, &u, gridDim.x)) {
       const unsigned t = tile % C::kAccs, tph = (tile / C::kAccs) & 1;
       go = __all_sync(0xffffffffu, mbar_wait(aempty0 + 8 * t, tph ^ 1, stop, p.flags));
       if (!go) break;
       tc_fence_after();
       // a tile of 64 columns has the scales of half a block of 128 rows of b
       const unsigned half_cols = BN == 64 ? (u.tn & 1) * 2 : 0;
-      for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
-        const unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
-        go = __all_sync(0xffffffffu, p.lost_warp == kMmaWarp && p.lost_step == it ? give_up(stop, p.flags)
-                                                                                 : mbar_wait(full0 + 8 * s, ph, stop, p.flags));
-        if (!go) break;
-        tc_fence_after();
-        const unsigned at = smem + s * C::kSlabBytes, sat = scales0 + s * C::kScaleBytes, ts = tscales + s * C::kScaleCols;
-        const unsigned long long da = smem_desc(at), db = smem_desc(at + kBM * 128), ds = scale_desc(sat);
-        const int left = p.k - kb * kBK;
-        if (elect_one()) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h * 128 < left) {  // the scales of 128 k's: a's, then b's blocks of rows side by side
-#pragma unroll
-              for (int j = 0; j < C::kRowBlocks; ++j)
-                tc_copy_scales(ts + (j == 0 ? h * 4 : 8 + h * 4 * (C::kRowBlocks - 1) + (j - 1) * 4), ds + (j * 1024 + h * 512) / 16);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < kBK / 64; ++j) {
-            if (j * 64 < left) {
-              const unsigned id = (j & 1) * 2u, h = j >> 1;
-              tc_mma4(tmem + t * BN, da + 2 * j, db + 2 * j, idesc | (id << 4) | (id << 29), ts + h * 4,
-                      ts + 8 + h * 4 * (C::kRowBlocks - 1) + half_cols, kb > u.kb0 || j > 0);
-            }
-          }
+      // One thread for the whole unit: with the warp meeting at every step, a step took 50 to 100 cycles more.
+      bool fine = true;
+      unsigned did = 0;
+      if (elect_one()) {
+        unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
+        for (int kb = u.kb0; kb < u.kb1; ++kb, ++did) {
+          fine = p.lost_warp == kMmaWarp && p.lost_step == it + did ? give_up(stop, p.flags) : mbar_wait(full0 + 8 * s, ph, stop, p.flags);
+          if (!fine) break;
+          tc_fence_after();
+          const unsigned at = smem + s * C::kSlabBytes, ts = tscales + s * C::kScaleCols, d = tmem + t * BN;
+          const unsigned long long da = smem_desc(at), db = smem_desc(at + kBM * 128), ds = scale_desc(scales0 + s * C::kScaleBytes);
+          const int left = p.k - kb * kBK;
+          if (left >= kBK) issue_step4<C::kRowBlocks, false>(d, da, db, idesc, ds, ts, half_cols, kb > u.kb0, kBK);
+          else issue_step4<C::kRowBlocks, false>(d, da, db, idesc, ds, ts, half_cols, kb > u.kb0, left);
           tc_commit(done0 + 8 * s);
-          if (kb + 1 == u.kb1) tc_commit(afull0 + 8 * t);
+          if (++s == C::kStages) s = 0, ph ^= 1;
         }
-        __syncwarp();
+        if (fine) tc_commit(afull0 + 8 * t);
       }
+      __syncwarp();
+      it += __reduce_max_sync(0xffffffffu, did);
+      go = __all_sync(0xffffffffu, fine);
+      if (!go) break;
       ++tile;
     }
     issued[1] = it;
@@ -212,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile4_kernel(const __grid_constan
     const int half = warp >> 2, quarter = warp & 3;
     float* const stage = reinterpret_cast<float*>(raw + (smem - smem_u32(raw)) + C::kStages * (C::kSlabBytes + C::kScaleBytes)) + warp * 32 * 17;
     unsigned tile = 0;
-    while (next_unit(p, &pos, end, &u)) {
+    while (next_unit(p, &pos, end, &u, gridDim.x)) {
       const unsigned t = tile % C::kAccs, tph = (tile / C::kAccs) & 1;
       const int row = u.tm * kBM + quarter * 32 + lane;
       const int col0 = u.tn * BN + half * kHalf;
@@ -248,6 +279,168 @@ __global__ void __launch_bounds__(kThreads, 1) tile4_kernel(const __grid_constan
   if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+  }
+}
+
+// ------------------------------------------------------------------ pairs of SMs
+
+// A tile of 256 x 256 by two neighbouring SMs: each holds its 128 rows of a, half of b's rows
+// (the tensor cores read both halves), all scales of those 256 and the sums of its own rows.  A step then
+// takes 35 KB a block from L2 where a tile of 128 x 256 takes 51: at 512 cycles of products a
+// step those are 29 TB/s for 152 SMs, more than L2 gives.
+struct PairCfg4 {
+  static constexpr int kSlabBytes = 2 * kBM * 128;
+  static constexpr int kScaleBytes = 3 * 1024;
+  static constexpr int kScaleCols = 24;
+};
+template <bool WIDE>
+struct PairStages4 : PairCfg4 {
+  static constexpr int kStages = WIDE ? 6 : 5;
+  static constexpr int kStoreBytes = WIDE ? 0 : kSumWarps * 32 * 17 * 4;
+  static constexpr int kBytes = kStages * (kSlabBytes + kScaleBytes) + kStoreBytes + 1024;
+  static_assert(256 + kStages * kScaleCols <= 512 && kBytes <= 232448, "TMEM columns, shared memory");
+};
+
+template <typename OT, bool WIDE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    pair4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                 const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb, const __grid_constant__ Matmul4Args p) {
+  using C = PairStages4<WIDE>;
+  constexpr int BN = 256, kHalf = BN / 2;
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) unsigned long long bars[2 * C::kStages + 2];
+  __shared__ unsigned tmem_slot, stop_flag;
+  __shared__ unsigned issued[2];  // steps whose loads and products were issued
+  const unsigned smem = (smem_u32(raw) + 1023u) & ~1023u, stop = smem_u32(&stop_flag);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const unsigned full0 = smem_u32(bars), done0 = full0 + 8 * C::kStages, afull = done0 + 8 * C::kStages, aempty = afull + 8;
+  const unsigned scales0 = smem + C::kStages * C::kSlabBytes;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(done0 + 8 * s, 1);
+    }
+    mbar_init(afull, 1);
+    mbar_init(aempty, 2 * kSumWarps);                          // of both blocks
+    stop_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  pair_sync();
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  pair_sync();
+  tc_fence_after();
+  const unsigned tmem = tmem_slot, tscales = tmem + BN;
+
+  long long pos, end;
+  my_range(p, &pos, &end, pair);
+  Unit u;
+
+  if (warp == kTmaWarp) {
+    unsigned it = 0;
+    bool go = true;
+    const int last_a = (p.m - 1) >> 7, last_b = (p.n - 1) >> 7;  // last tiles of scales: past them, any do
+    while (go && next_unit(p, &pos, end, &u, pairs)) {
+      const int ra = u.tm * 2 + rank;
+      for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
+        const unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
+        go = __all_sync(0xffffffffu, p.lost_warp == kTmaWarp && p.lost_step == it ? pair_give_up(stop, p.flags)
+                                                                                 : pair_wait(done0 + 8 * s, ph ^ 1, stop, p.flags));
+        if (!go) break;
+        if (elect_one()) {
+          const unsigned dst = smem + s * C::kSlabBytes, sdst = scales0 + s * C::kScaleBytes, bar = peer_addr(full0 + 8 * s, 0);
+          if (rank == 0) mbar_expect_tx(full0 + 8 * s, 2 * (C::kSlabBytes + C::kScaleBytes));
+          tma_load_pair(dst, &map_a, kb * 128, ra * kBM, bar);
+          tma_load_pair(dst + kBM * 128, &map_b, kb * 128, u.tn * BN + rank * kBM, bar);
+          tma_load_pair(sdst, &map_sa, 0, min(ra, last_a) * p.s_blocks + 2 * kb, bar);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) tma_load_pair(sdst + 1024 * (1 + j), &map_sb, 0, min(u.tn * 2 + j, last_b) * p.s_blocks + 2 * kb, bar);
+        }
+        __syncwarp();
+      }
+    }
+    if (p.lost_warp == kAfterLoads) pair_give_up(stop, p.flags);
+    issued[0] = it;
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    constexpr unsigned idesc = (1u << 7) | (1u << 10) | ((BN >> 3) << 17) | (1u << 23) | ((2 * kBM >> 4) << 24);
+    unsigned it = 0, tile = 0;
+    bool go = rank == 0;
+    while (go && next_unit(p, &pos, end, &u, pairs)) {
+      go = __all_sync(0xffffffffu, pair_wait(aempty, (tile & 1) ^ 1, stop, p.flags));
+      if (!go) break;
+      bool fine = true;
+      unsigned did = 0;
+      if (elect_one()) {
+        unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
+        for (int kb = u.kb0; kb < u.kb1; ++kb, ++did) {
+          fine = p.lost_warp == kMmaWarp && p.lost_step == it + did ? pair_give_up(stop, p.flags) : pair_wait(full0 + 8 * s, ph, stop, p.flags);
+          if (!fine) break;
+          tc_fence_after();
+          const unsigned at = smem + s * C::kSlabBytes, ts = tscales + s * C::kScaleCols;
+          const unsigned long long da = smem_desc(at), db = smem_desc(at + kBM * 128), ds = scale_desc(scales0 + s * C::kScaleBytes);
+          const int left = p.k - kb * kBK;
+          if (left >= kBK) issue_step4<3, true>(tmem, da, db, idesc, ds, ts, 0, kb > u.kb0, kBK);
+          else issue_step4<3, true>(tmem, da, db, idesc, ds, ts, 0, kb > u.kb0, left);
+          commit_both(done0 + 8 * s);
+          if (++s == C::kStages) s = 0, ph ^= 1;
+        }
+        if (fine) commit_both(afull);
+      }
+      __syncwarp();
+      it += __reduce_max_sync(0xffffffffu, did);
+      go = __all_sync(0xffffffffu, fine);
+      if (!go) break;
+      ++tile;
+    }
+    issued[1] = it;
+    __syncwarp();
+  } else {  // TMEM lanes 32 (warp % 4).., columns group (warp / 4)
+    const int half = warp >> 2, quarter = warp & 3;
+    float* const stage = reinterpret_cast<float*>(raw + (smem - smem_u32(raw)) + C::kStages * (C::kSlabBytes + C::kScaleBytes)) + warp * 32 * 17;
+    unsigned tile = 0;
+    while (next_unit(p, &pos, end, &u, pairs)) {
+      const int row = (u.tm * 2 + rank) * kBM + quarter * 32 + lane;
+      const int col0 = u.tn * BN + half * kHalf;
+      if (!__all_sync(0xffffffffu, pair_wait(afull, tile & 1, stop, p.flags))) break;
+      tc_fence_after();
+      const unsigned taddr = tmem + ((unsigned)(quarter * 32) << 16) + half * kHalf;
+      unsigned v[kHalf];
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 32) tc_load32(taddr + c, v + c);
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 32) tc_wait32(v + c);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) pair_arrive(aempty, 0);                   // all sums are in registers
+      float acc[kHalf];
+#pragma unroll
+      for (int c = 0; c < kHalf; ++c) acc[c] = __uint_as_float(v[c]);
+      store_unit<BN, OT, WIDE, 2>(p, u, warp, lane, row, col0, acc, stage);
+      ++tile;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (pair_stopped(stop)) {  // a wait ran out: what is in flight lands before the blocks end
+    const unsigned n = warp >= kSumWarps ? issued[warp - kSumWarps] : 0;
+    if (rank == 0 && warp == kTmaWarp)
+      for (unsigned j = n - min(n, (unsigned)C::kStages); j < n; ++j) mbar_drain(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1);
+    if (rank == 0 && warp == kMmaWarp && n > 0) mbar_drain(done0 + 8 * ((n - 1) % C::kStages), ((n - 1) / C::kStages) & 1);
+    // loads of the other block that the leader no longer expects: they take microseconds
+    for (int i = 0; i < 200; ++i) __nanosleep(1000);
+  }
+  __syncthreads();
+  pair_sync();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
 }
 
@@ -380,7 +573,8 @@ __global__ void __launch_bounds__(256) row4_kernel(const __grid_constant__ Matmu
 // ------------------------------------------------------------------ host side
 
 struct Plan4 {
-  int bn = 0;             // 0: row kernel
+  int bn = 0;             // columns of a tile; 0: row kernel
+  bool pair = false;      // tiles of 256 x 256, by pairs
   int m_tiles = 0, n_tiles = 0, k_blocks = 0;
   long long per_cta = 0;  // steps a block, 0: whole tiles
   int grid = 0;
@@ -393,43 +587,66 @@ Plan4 make_plan4(long long m, long long n, long long k) {
   pl.k_blocks = (int)((k + kBK - 1) / kBK);
   if (m == 1 || (m == kRowMax && (double)n * k <= 8e7)) return pl;
   const int sms = sm_count();
-  const long long mt = (m + kBM - 1) / kBM;
-  // The tile's width, and whole tiles or even shares of the steps: whichever a model of
-  // the time (us) puts first.
+  // The tile's width, or pairs' tiles, and whole tiles or even shares of the steps: whichever a model of
+  // the time (us, fitted to 17 shapes from 64 x 1024 x 8192 to 131,072 x 1024 x 8192, each run in all four
+  // ways; within 20 % of most) puts first.  A step takes 0.33, 0.245 or 0.23 at 256, 128 or 64 columns and 0.284
+  // by pairs, a tile's end 1.4, 0.6, 0.5 and 2.6; sharing costs the second launch and 0.3 a megabyte
+  // of partial tiles.  Measured: 131,072 x 1024 x 8192 311 by pairs and 339 at 256; x 1024 77 at 256 and 90 by
+  // pairs; 1024 x 1664 x 16,384 19 whole at 128 and 22 at 256; 64 x 1024 x 8192 7.6 shared and 10.7 whole.
   double best = 0.0;
-  const double step_us[3] = {0.33, 0.20, 0.15}, end_us[3] = {2.5, 1.5, 1.5};
-  for (int w = 0; w < 3; ++w) {
-    const int bn = 256 >> w;
-    const long long nt = (n + bn - 1) / bn, tiles = mt * nt, steps = tiles * pl.k_blocks;
-    const long long rounds = (tiles + sms - 1) / sms;
+  const double step_us[4] = {0.33, 0.245, 0.23, 0.284}, end_us[4] = {1.4, 0.6, 0.5, 2.6};
+  const bool fits = ((m + 127) / 128) * ((k + 127) / 128) < 0x7fffffffLL && ((n + 127) / 128) * ((k + 127) / 128) < 0x7fffffffLL;
+  for (int w = 0; w < (fits ? 4 : 3); ++w) {
+    const bool pair = w == 3;
+    const int bn = pair ? 256 : 256 >> w, rows = pair ? 2 * kBM : kBM, workers = pair ? std::max(1, sms / 2) : sms;
+    const long long mt = (m + rows - 1) / rows, nt = (n + bn - 1) / bn, tiles = mt * nt, steps = tiles * pl.k_blocks;
+    const long long rounds = (tiles + workers - 1) / workers;
     const double whole = (double)rounds * (pl.k_blocks * step_us[w] + end_us[w]);
-    const long long per = std::max<long long>((steps + sms - 1) / sms, 2);
+    const long long per = std::max<long long>((steps + workers - 1) / workers, 2);
     const long long grid = (steps + per - 1) / per;
-    const double mb = (double)(grid + tiles) * std::min<long long>(m, kBM) * bn * 4e-6;
-    const double shared = per * step_us[w] + end_us[w] + 4.0 + 0.42 * mb;
+    const double mb = (double)(grid + tiles) * std::min<long long>(m, rows) * bn * 4e-6;
+    const double shared = per * step_us[w] + end_us[w] + 2.6 + 0.3 * mb;
     const bool share = pl.k_blocks > 1 && shared < whole;
     const double us = share ? shared : whole;
     if (w > 0 && us >= best) continue;
     best = us;
     pl.bn = bn;
+    pl.pair = pair;
+    pl.m_tiles = (int)mt;
     pl.n_tiles = (int)nt;
     pl.per_cta = share ? per : 0;
-    pl.grid = (int)(share ? grid : std::min<long long>(tiles, sms));
-    pl.ws_bytes = share ? (size_t)(grid + tiles) * kBM * bn * sizeof(float) : 0;
+    pl.grid = (int)(share ? grid : std::min<long long>(tiles, workers));
+    pl.ws_bytes = share ? (size_t)(grid + tiles) * rows * bn * sizeof(float) : 0;
   }
-  pl.m_tiles = (int)mt;
   return pl;
 }
 
+struct Maps4 {
+  CUtensorMap a, b, sa, sb;  // sa, sb: pairs only
+};
+
 template <int BN, typename OT>
-cudaError_t launch_tiles4(const Matmul4Args& p, const Plan4& pl, const CUtensorMap& ma, const CUtensorMap& mb, bool wide, cudaStream_t st) {
+cudaError_t launch_tiles4(const Matmul4Args& p, const Plan4& pl, const Maps4& t, bool wide, cudaStream_t st) {
   auto* k = wide ? tile4_kernel<BN, OT, true> : tile4_kernel<BN, OT, false>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, TileCfg4<BN>::kBytes);
   if (e != cudaSuccess) return e;
-  k<<<pl.grid, kThreads, TileCfg4<BN>::kBytes, st>>>(ma, mb, p);
+  k<<<pl.grid, kThreads, TileCfg4<BN>::kBytes, st>>>(t.a, t.b, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || pl.per_cta == 0) return e;
   join_kernel<BN, OT, Matmul4Args><<<pl.m_tiles * pl.n_tiles * (kBM * BN / 1024), 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename OT>
+cudaError_t launch_pairs4(const Matmul4Args& p, const Plan4& pl, const Maps4& t, bool wide, cudaStream_t st) {
+  auto* k = wide ? pair4_kernel<OT, true> : pair4_kernel<OT, false>;
+  const int bytes = wide ? PairStages4<true>::kBytes : PairStages4<false>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  k<<<2 * pl.grid, kThreads, bytes, st>>>(t.a, t.b, t.sa, t.sb, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || pl.per_cta == 0) return e;
+  join_kernel<256, OT, Matmul4Args, 2><<<pl.m_tiles * pl.n_tiles * 2 * (kBM * 256 / 1024), 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -443,15 +660,16 @@ cudaError_t launch_rows4(const Matmul4Args& p, cudaStream_t st) {
 }
 
 template <typename OT>
-cudaError_t launch4(const Matmul4Args& p, const Plan4& pl, const CUtensorMap& ma, const CUtensorMap& mb, bool wide, cudaStream_t st) {
+cudaError_t launch4(const Matmul4Args& p, const Plan4& pl, const Maps4& t, bool wide, cudaStream_t st) {
   if (p.k == 0) {
     bias_kernel<OT, Matmul4Args><<<(int)std::min<long long>(((long long)p.m * p.n + 255) / 256, 8LL * sm_count()), 256, 0, st>>>(p);
     return cudaGetLastError();
   }
   if (pl.bn == 0) return p.m == 1 ? launch_rows4<1, OT>(p, st) : launch_rows4<2, OT>(p, st);
-  if (pl.bn == 64) return launch_tiles4<64, OT>(p, pl, ma, mb, wide, st);
-  if (pl.bn == 128) return launch_tiles4<128, OT>(p, pl, ma, mb, wide, st);
-  return launch_tiles4<256, OT>(p, pl, ma, mb, wide, st);
+  if (pl.pair) return launch_pairs4<OT>(p, pl, t, wide, st);
+  if (pl.bn == 64) return launch_tiles4<64, OT>(p, pl, t, wide, st);
+  if (pl.bn == 128) return launch_tiles4<128, OT>(p, pl, t, wide, st);
+  return launch_tiles4<256, OT>(p, pl, t, wide, st);
 }
 
 }  // namespace
@@ -498,18 +716,35 @@ extern "C" emb_status emb_fp4_matmul(const void* a_d, int64_t lda, const void* s
                 bias_d, out_d, (float*)workspace_d, lda, ldb, ldo, (int)m, (int)n, (int)k, pl.m_tiles, pl.n_tiles,
                 pl.k_blocks, (int)((k + 127) / 128), (long long)pl.m_tiles * pl.n_tiles * pl.k_blocks, pl.per_cta, nullptr,
                 lost < 0 ? -1 : lost_warps[lost], lost_step};
-  CUtensorMap ma{}, mb{};
+  Maps4 t{};
   if (pl.bn) {
     EMB_CUDA(op_flags(&p.flags));
-    if (!make_map(&ma, a_d, m, kb, lda, kBM) || !make_map(&mb, b_d, n, kb, ldb, pl.bn))
+    bool ok = make_map(&t.a, a_d, m, kb, lda, kBM) && make_map(&t.b, b_d, n, kb, ldb, pl.pair ? kBM : pl.bn);
+    if (pl.pair)
+      ok = ok && make_scale_map(&t.sa, sa_d, (m + 127) / 128 * p.s_blocks) && make_scale_map(&t.sb, sb_d, (n + 127) / 128 * p.s_blocks);
+    if (!ok)
       return fail(EMB_ERR_CUDA, "cuTensorMapEncodeTiled failed or is not available");
   }
   const bool wide = aligned_to(out_d, 32) && (ldo * ftype_bytes(out_t)) % 32 == 0;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
-  if (out_t == EMB_T_F32) e = launch4<float>(p, pl, ma, mb, wide, st);
-  else if (out_t == EMB_T_BF16) e = launch4<__nv_bfloat16>(p, pl, ma, mb, wide, st);
-  else e = launch4<__half>(p, pl, ma, mb, wide, st);
+  if (out_t == EMB_T_F32) e = launch4<float>(p, pl, t, wide, st);
+  else if (out_t == EMB_T_BF16) e = launch4<__nv_bfloat16>(p, pl, t, wide, st);
+  else e = launch4<__half>(p, pl, t, wide, st);
   if (e != cudaSuccess) return cuda_fail(e, "emb_fp4_matmul launch");
+  return EMB_OK;
+}
+
+extern "C" emb_status emb_debug_fp4_matmul_plan(int64_t m, int64_t n, int64_t k, int64_t* plan) {
+  size_t bytes = 0;
+  if (!plan) return fail(EMB_ERR_INVALID_ARG, "plan is NULL");
+  const emb_status rc = emb_fp4_matmul_workspace_size(m, n, k, &bytes);
+  if (rc != EMB_OK) return rc;
+  const Plan4 pl = make_plan4(m, n, k);
+  plan[0] = pl.bn;
+  plan[1] = (int64_t)pl.m_tiles * pl.n_tiles;
+  plan[2] = pl.grid;
+  plan[3] = pl.per_cta;
+  plan[4] = pl.pair ? 2 : 1;
   return EMB_OK;
 }

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
   const unsigned tmem = tmem_slot;
 
   long long pos, end;
-  my_range(p, &pos, &end);
+  my_range(p, &pos, &end, blockIdx.x);
   Unit u;
 
   if (warp >= kScaleWarps) {
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     if (warp == kTmaWarp) {  // TMA: both slabs of each step
       unsigned it = 0;
       bool go = true;
-      while (go && next_unit(p, &pos, end, &u)) {
+      while (go && next_unit(p, &pos, end, &u, gridDim.x)) {
         cut_lost(p, kTmaWarp, it, &u);
         for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
           const unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       constexpr unsigned idesc = (1u << 4) | ((BN >> 3) << 17) | ((kBM >> 4) << 24);
       unsigned it = 0;
       bool go = true;
-      while (go && next_unit(p, &pos, end, &u)) {
+      while (go && next_unit(p, &pos, end, &u, gridDim.x)) {
         cut_lost(p, kMmaWarp, it, &u);
         for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
           const unsigned s = it % C::kStages, ph = (it / C::kStages) & 1;
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
       // alignment), up to kAhead steps early: each is a new cache line.
       unsigned it = 0;
       bool go = true;
-      while (go && next_unit(p, &pos, end, &u)) {
+      while (go && next_unit(p, &pos, end, &u, gridDim.x)) {
         cut_lost(p, kFetchWarp, it, &u);
         const float *sa[kBM / 32], *sb[BCOL ? BN / 32 : 1];
 #pragma unroll
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) tile_kernel(const __grid_constant
     float* const stage = ring + kAhead * C::kSlot + warp * 32 * 17;
     unsigned it = 0;
     bool go = true;
-    while (go && next_unit(p, &pos, end, &u)) {
+    while (go && next_unit(p, &pos, end, &u, gridDim.x)) {
       const int row = u.tm * kBM + quarter * 32 + lane;
       const int col0 = u.tn * BN + half * C::kHalf;
       float acc[C::kHalf];

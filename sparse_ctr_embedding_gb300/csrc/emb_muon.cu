@@ -290,42 +290,18 @@ __device__ __forceinline__ unsigned tiles_before(const Mat& t, const Item& it) {
   return 2u * (unsigned)(it.step * (n0 + n1 + n2) + (it.phase > 0 ? n0 : 0) + (it.phase > 1 ? n1 : 0));
 }
 
-__device__ __forceinline__ unsigned peer_addr(unsigned addr, unsigned rank) {
-  unsigned r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-// What a wait that ran out does: both blocks' other waits end, the weights stay, the host is told.
+// What a wait that ran out does: the pair's other waits end, the weights stay, the host is told.
 __device__ __forceinline__ bool muon_give_up(unsigned stop, const MuonArgs& a) {
-  for (unsigned r = 0; r < 2; ++r)
-    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(peer_addr(stop, r)) : "memory");
   atomicOr(a.failed, 1u);
-  atomicOr(a.flags, EMB_FLAG_OP_TIMEOUT);
-  return false;
-}
-__device__ __forceinline__ bool stopped(unsigned stop) {
-  unsigned v;
-  asm volatile("ld.relaxed.cluster.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(stop) : "memory");
-  return v != 0;
-}
-__device__ __forceinline__ bool cluster_try(unsigned bar, unsigned parity) {
-  unsigned ok;
-  asm volatile(
-      "{\n.reg .pred p;\n"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      "selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
+  return pair_give_up(stop, a.flags);
 }
 // A phase of a large matrix takes a second: the limit on polls is longer than the other products'.
 constexpr unsigned kMuonLimit = 1u << 27;
 __device__ __forceinline__ bool muon_wait(unsigned bar, unsigned parity, unsigned stop, const MuonArgs& a) {
-  if (cluster_try(bar, parity)) return true;
+  if (pair_try(bar, parity)) return true;
   for (unsigned i = 0; i < kMuonLimit; ++i) {
-    if (cluster_try(bar, parity)) return true;
-    if (stopped(stop)) return false;
+    if (pair_try(bar, parity)) return true;
+    if (pair_stopped(stop)) return false;
   }
   return muon_give_up(stop, a);
 }
@@ -335,22 +311,12 @@ __device__ __forceinline__ bool tiles_wait(const unsigned* count, unsigned need,
     unsigned v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
     if (v >= need) return true;
-    if ((i & 15) == 15 && (stopped(stop) || *(volatile unsigned*)a.failed)) return muon_give_up(stop, a);
+    if ((i & 15) == 15 && (pair_stopped(stop) || *(volatile unsigned*)a.failed)) return muon_give_up(stop, a);
   }
   return muon_give_up(stop, a);
 }
 __device__ __forceinline__ void tma_load2(unsigned dst, const CUtensorMap* map, long long at, unsigned bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(0), "r"((int)(at >> 7)), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void commit_both(unsigned bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"((unsigned short)3)
-               : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  tma_load_pair(dst, map, 0, (int)(at >> 7), bar);
 }
 // Whether `go` holds in all warps that hold sums.
 __device__ __forceinline__ bool sums_go(bool go) {
@@ -459,14 +425,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
-  cluster_sync();
+  pair_sync();
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  pair_sync();
   tc_fence_after();
   const unsigned tmem = tmem_slot;
   const int total = kSteps * (a.total[0] + a.total[1] + a.total[2]), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -516,26 +482,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == kMmaWarp && rank == 0) {
       // float32 sums, float16 operands, M = N = 256
       constexpr unsigned idesc0 = (1u << 4) | ((256 >> 3) << 17) | ((256 >> 4) << 24);
+      // One thread for all: with the warp meeting at every slab, a slab took 50 to 100 cycles more.
       unsigned n = 0, tile = 0;
-      bool go = true;
-      for (int at = pair; go && at < total; at += pairs) {
-        item_at(a, at, &it);
-        const bool apply = it.phase == kApply;                            // its right operand has its columns contiguous
-        const unsigned idesc = idesc0 | (apply ? 1u << 16 : 0u), badvance = apply ? 128 : 2;
-        for (int k = it.k0; k < it.k1; ++k, ++n) {
-          const bool first = (k - it.k0) % C::kDrain == 0, last = k + 1 == it.k1 || (k + 1 - it.k0) % C::kDrain == 0;
-          const unsigned t = tile & 1, tph = (tile >> 1) & 1;
-          if (first) {
-            go = __all_sync(0xffffffffu, muon_wait(aempty0 + 8 * t, tph ^ 1, stop, a));
+      if (elect_one()) {
+        bool go = true;
+        unsigned s = 0, ph = 0;
+        for (int at = pair; go && at < total; at += pairs) {
+          item_at(a, at, &it);
+          const bool apply = it.phase == kApply;                          // its right operand has its columns contiguous
+          const unsigned idesc = idesc0 | (apply ? 1u << 16 : 0u), badvance = apply ? 128 : 2;
+          for (int k = it.k0; k < it.k1; ++k, ++n) {
+            const bool first = (k - it.k0) % C::kDrain == 0, last = k + 1 == it.k1 || (k + 1 - it.k0) % C::kDrain == 0;
+            const unsigned t = tile & 1, tph = (tile >> 1) & 1;
+            if (first) {
+              go = muon_wait(aempty0 + 8 * t, tph ^ 1, stop, a);
+              if (!go) break;
+            }
+            tile += last;
+            go = a.lost_warp == kMmaWarp && a.lost_step == n ? muon_give_up(stop, a) : muon_wait(full0 + 8 * s, ph, stop, a);
             if (!go) break;
-          }
-          tile += last;
-          const unsigned s = n % C::kStages, ph = (n / C::kStages) & 1;
-          go = __all_sync(0xffffffffu, a.lost_warp == kMmaWarp && a.lost_step == n ? muon_give_up(stop, a) : muon_wait(full0 + 8 * s, ph, stop, a));
-          if (!go) break;
-          tc_fence_after();
-          const unsigned from = smem + s * C::kStageBytes;
-          if (elect_one()) {
+            tc_fence_after();
+            const unsigned from = smem + s * C::kStageBytes;
 #pragma unroll
             for (int q = 0; q < (PLANES == 2 ? 3 : 1); ++q) {  // hi hi, hi lo, lo hi
               const unsigned long long da = smem_desc(from + (q == 2 ? kTileBytes : 0));
@@ -546,10 +513,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             commit_both(done0 + 8 * s);
             if (last) commit_both(afull0 + 8 * t);
+            if (++s == C::kStages) s = 0, ph ^= 1;
           }
-          __syncwarp();
         }
       }
+      __syncwarp();
+      n = __reduce_max_sync(0xffffffffu, n);
       issued[1] = n;
     }
     __syncwarp();
@@ -562,8 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto release = [&](unsigned which) {                       // an accumulator that has been read
       tc_fence_before();
       __syncwarp();
-      if (lane == 0)
-        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(aempty0 + 8 * which, 0)) : "memory");
+      if (lane == 0) pair_arrive(aempty0 + 8 * which, 0);
     };
     for (int at = pair; at < total; at += pairs) {
       item_at(a, at, &it);
@@ -776,7 +744,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (stopped(stop)) {  // a wait ran out: what is in flight lands before the blocks end
+  if (pair_stopped(stop)) {  // a wait ran out: what is in flight lands before the blocks end
     const unsigned n = warp >= kSumWarps && warp < kSumWarps + 2 ? issued[warp - kSumWarps] : 0;
     if (rank == 0 && warp == kLoadWarp)
       for (unsigned j = n - min(n, (unsigned)C::kStages); j < n; ++j) mbar_drain(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1);
@@ -785,7 +753,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 200; ++i) __nanosleep(1000);
   }
   __syncthreads();
-  cluster_sync();
+  pair_sync();
   if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));

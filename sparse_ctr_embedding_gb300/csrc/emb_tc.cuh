@@ -131,6 +131,64 @@ __device__ __forceinline__ unsigned long long smem_desc(unsigned addr) {
   return (unsigned long long)((addr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// ------------------------------------------------------------------ pairs of SMs (clusters of two blocks)
+//
+// A pair's MMAs are issued by its first block ("leader"); loads of both signal its barriers,
+// completions go to both.  A wait that runs out raises `stop` (a word at the same place of both
+// blocks' shared memory) in both.
+
+__device__ __forceinline__ unsigned peer_addr(unsigned addr, unsigned rank) {
+  unsigned r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ bool pair_give_up(unsigned stop, unsigned* flags) {
+  for (unsigned r = 0; r < 2; ++r)
+    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(peer_addr(stop, r)) : "memory");
+  atomicOr(flags, EMB_FLAG_OP_TIMEOUT);
+  return false;
+}
+__device__ __forceinline__ bool pair_stopped(unsigned stop) {
+  unsigned v;
+  asm volatile("ld.relaxed.cluster.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(stop) : "memory");
+  return v != 0;
+}
+__device__ __forceinline__ bool pair_try(unsigned bar, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool pair_wait(unsigned bar, unsigned parity, unsigned stop, unsigned* flags) {
+  if (pair_try(bar, parity)) return true;
+  for (unsigned i = 0; i < kWaitLimit; ++i) {
+    if (pair_try(bar, parity)) return true;
+    if (pair_stopped(stop)) return false;
+  }
+  return pair_give_up(stop, flags);
+}
+__device__ __forceinline__ void pair_arrive(unsigned bar, unsigned rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(bar, rank)) : "memory");
+}
+// A TMA load that signals the leader's barrier (`bar`: its address in the cluster).
+__device__ __forceinline__ void tma_load_pair(unsigned dst, const CUtensorMap* map, int x, int y, unsigned bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void commit_both(unsigned bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"((unsigned short)3)
+               : "memory");
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 template <typename OT>
 __device__ __forceinline__ void store32(OT* dst, const float* v) {  // 32 bytes
   if constexpr (sizeof(OT) == 4) {

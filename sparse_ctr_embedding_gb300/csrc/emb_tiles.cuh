@@ -33,15 +33,15 @@ __device__ __forceinline__ void tile_at(const P& p, long long t, int* tm, int* t
   *tn = in / rows;
 }
 
-// The block's next unit from its position: a tile number, or a step.
+// A worker's (a block's, or a pair's) next unit from its position: a tile number, or a step.
 template <class P>
-__device__ __forceinline__ bool next_unit(const P& p, long long* pos, long long end, Unit* u) {
+__device__ __forceinline__ bool next_unit(const P& p, long long* pos, long long end, Unit* u, int workers) {
   if (*pos >= end) return false;
   if (p.per_cta == 0) {
     u->tile = *pos;
     u->kb0 = 0;
     u->kb1 = p.k_blocks;
-    *pos += gridDim.x;
+    *pos += workers;
   } else {
     u->tile = *pos / p.k_blocks;
     u->kb0 = (int)(*pos - u->tile * p.k_blocks);
@@ -52,20 +52,21 @@ __device__ __forceinline__ bool next_unit(const P& p, long long* pos, long long 
   return true;
 }
 template <class P>
-__device__ __forceinline__ void my_range(const P& p, long long* pos, long long* end) {
+__device__ __forceinline__ void my_range(const P& p, long long* pos, long long* end, int worker) {
   if (p.per_cta == 0) {
-    *pos = blockIdx.x;
+    *pos = worker;
     *end = (long long)p.m_tiles * p.n_tiles;
   } else {
-    *pos = blockIdx.x * p.per_cta;
+    *pos = worker * p.per_cta;
     *end = min(p.steps, *pos + p.per_cta);
   }
 }
 
 // A unit's sums, from the registers of this lane (`acc`: row `row`, columns col0..), to
 // the output, or to the workspace where the tile has other pieces.  WIDE: rows of out
-// are aligned to 32 bytes; else `stage` is this warp's 32 x 17 floats of shared memory.
-template <int BN, typename OT, bool WIDE, class P>
+// are aligned to 32 bytes; else `stage` is this warp's 32 x 17 floats of shared memory.  BLOCKS:
+// of a worker (a pair has two tiles of 128 rows, one below the other).
+template <int BN, typename OT, bool WIDE, int BLOCKS = 1, class P>
 __device__ __forceinline__ void store_unit(const P& p, const Unit& u, int warp, int lane, int row, int col0, float* acc, float* stage) {
   constexpr int kHalf = BN / 2;
   if (u.kb0 == 0 && u.kb1 == p.k_blocks) {
@@ -107,8 +108,8 @@ __device__ __forceinline__ void store_unit(const P& p, const Unit& u, int warp, 
           if (row - lane + r < p.m && col < p.n) dst[r * p.ldo] = from_f32<OT>(stage[r * 17 + (lane & 15)] + bias);
       }
     }
-  } else if (row < p.m) {  // part of a tile: slot (block + tile) is this piece's alone
-    float* dst = p.partial + (long long)(blockIdx.x + u.tile) * kBM * BN + (warp * kHalf * 4 + lane) * 8;
+  } else if (row < p.m) {  // part of a tile: slot (worker + tile) is this piece's alone
+    float* dst = p.partial + ((blockIdx.x / BLOCKS + u.tile) * BLOCKS + blockIdx.x % BLOCKS) * kBM * BN + (warp * kHalf * 4 + lane) * 8;
 #pragma unroll
     for (int c = 0; c < kHalf; c += 8) store32<float>(dst + c * 32, acc + c);
   }
@@ -118,21 +119,21 @@ __device__ __forceinline__ void store_unit(const P& p, const Unit& u, int warp, 
 // lies as the warps store it, whole kilobytes at a time: by warps, by 8 columns, by
 // rows (the 8-bit product of 1664 x 452 x 30,584 to bf16: 52 us, and 56 with pieces laid
 // out by rows).  One block takes 32 rows x 32 columns, four columns a thread.
-template <int BN, typename OT, class P>
+template <int BN, typename OT, class P, int BLOCKS = 1>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ P p) {
   constexpr int kBlocks = kBM * BN / 1024, kHalf = BN / 2, kWarpBlocks = kHalf / 32;
-  const long long tile = blockIdx.x / kBlocks;
+  const long long sub = blockIdx.x / kBlocks, tile = sub / BLOCKS;
   const int q = (int)(blockIdx.x % kBlocks), warp = q / kWarpBlocks, x = threadIdx.x / 8, y = threadIdx.x % 8;
   const long long first = tile * p.k_blocks / p.per_cta, last = ((tile + 1) * p.k_blocks - 1) / p.per_cta;
   if (first == last) return;  // one block had it whole
   int tm, tn;
   tile_at(p, tile, &tm, &tn);
-  const int row = tm * kBM + (warp & 3) * 32 + x, col = tn * BN + (warp >> 2) * kHalf + q % kWarpBlocks * 32 + y * 4;
+  const int row = (int)(tm * BLOCKS + sub % BLOCKS) * kBM + (warp & 3) * 32 + x, col = tn * BN + (warp >> 2) * kHalf + q % kWarpBlocks * 32 + y * 4;
   if (row >= p.m || col >= p.n) return;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  const float* src = p.partial + (first + tile) * kBM * BN + q * 1024 + y / 2 * 256 + x * 8 + y % 2 * 4;
+  const float* src = p.partial + ((first + tile) * BLOCKS + sub % BLOCKS) * kBM * BN + q * 1024 + y / 2 * 256 + x * 8 + y % 2 * 4;
 #pragma unroll 8
-  for (long long b = first; b <= last; ++b, src += (long long)kBM * BN) {
+  for (long long b = first; b <= last; ++b, src += (long long)BLOCKS * kBM * BN) {
     const float4 w = *reinterpret_cast<const float4*>(src);
     v.x += w.x;
     v.y += w.y;
@@ -178,6 +179,17 @@ inline bool make_map(CUtensorMap* map, const void* base, long long rows, long lo
   const cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, step[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tiles of scales, 512 bytes each, two at a time.
+inline bool make_scale_map(CUtensorMap* map, const void* base, long long tiles) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {128, (cuuint64_t)tiles}, strides[1] = {512};
+  const cuuint32_t box[2] = {128, 2}, step[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -143,7 +143,7 @@ SHAPES = [(1, 1, 1), (1, 64, 128), (1, 333, 1000), (2, 128, 64), (3, 64, 64), (1
           (5, 700, 8192), (8, 96, 200), (9, 40, 300), (16, 256, 512), (17, 129, 130), (64, 64, 64), (100, 512, 4096), (127, 255, 129),
           (128, 128, 1024), (129, 257, 385), (200, 1000, 16384), (256, 512, 256), (1000, 300, 1664), (1024, 1664, 2048), (2500, 96, 333),
           (4096, 640, 768), (40, 2500, 16), (300, 20, 5000), (1, 10001, 300), (1, 9729, 2100), (2, 9800, 1100), (2, 4100, 10000),
-          (10001, 70, 300), (1300, 452, 692), (2500, 1293, 141)]
+          (10001, 70, 300), (1300, 452, 692), (2500, 1293, 141), (20_011, 1100, 8192), (1000, 520, 80_000)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)
@@ -262,7 +262,7 @@ def test_linear_layer_gradients():
     assert float((DT.t() - dy).norm() / dy.norm()) < 0.25 and float((XT.t() - x).norm() / x.norm()) < 0.25
 
 
-@pytest.mark.parametrize("m,n,k", [(300, 512, 5120), (5000, 1100, 640), (20_011, 400, 300), (40_003, 40, 300)])
+@pytest.mark.parametrize("m,n,k", [(300, 512, 5120), (5000, 1100, 640), (20_011, 400, 300), (40_003, 40, 300), (1024, 1664, 16384)])
 def test_a_wait_that_runs_out(m, n, k):
     """Each warp that issues work loses its wait at the first step, while the ring of
     stages fills, and later, or the block is told to stop when the last loads are on
@@ -287,7 +287,7 @@ def test_a_wait_that_runs_out(m, n, k):
 
 
 @pytest.mark.parametrize("out,wide", [(BF16, True), (F32, False)])
-@pytest.mark.parametrize("m,n,k", [(20_011, 1100, 300), (40_011, 400, 640), (40_003, 40, 300), (60_003, 64, 1100), (30_000, 200, 96)])
+@pytest.mark.parametrize("m,n,k", [(20_011, 1100, 300), (66_000, 512, 1000), (100_001, 300, 130), (40_011, 400, 640), (40_003, 40, 300), (60_003, 64, 1100), (30_000, 200, 96)])
 def test_matmul_of_several_tiles_a_block(m, n, k, out, wide):
     """Whole tiles, several to a block: stages and accumulators go on from tile to tile,
     and a tile's output is stored while the next one's products run."""
@@ -298,3 +298,15 @@ def test_matmul_of_several_tiles_a_block(m, n, k, out, wide):
     got = E.emb_fp4_matmul(a, sa, b, sb, bias=bias, out=hold[:, :n])
     check(got, a, sa, b, sb, bias)
     assert bool((hold[:, n:] == 7.0).all())
+
+
+def test_plans():
+    """The sizes above reach every kernel: rows, each width of a tile, pairs, whole and shared tiles."""
+    seen = set()
+    for m, n, k in SHAPES + [(300, 512, 5120), (5000, 1100, 640), (20_011, 400, 300), (40_003, 40, 300), (1024, 1664, 16384), (20_011, 1100, 300),
+                             (66_000, 512, 1000), (100_001, 300, 130), (40_011, 400, 640), (60_003, 64, 1100), (30_000, 200, 96)]:
+        cols, tiles, workers, steps, blocks = E.emb_debug_fp4_matmul_plan(m, n, k)
+        seen.add((cols, blocks, steps > 0))
+        assert workers <= 152 // blocks or cols == 0
+    assert {(0, 1, False), (256, 2, False), (256, 2, True)} <= seen, seen
+    print(seen)
