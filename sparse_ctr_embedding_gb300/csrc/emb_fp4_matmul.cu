@@ -431,10 +431,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (pair_stopped(stop)) {  // a wait ran out: what is in flight lands before the blocks end
     const unsigned n = warp >= kSumWarps ? issued[warp - kSumWarps] : 0;
     if (rank == 0 && warp == kTmaWarp)
-      for (unsigned j = n - min(n, (unsigned)C::kStages); j < n; ++j) mbar_drain(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1);
-    if (rank == 0 && warp == kMmaWarp && n > 0) mbar_drain(done0 + 8 * ((n - 1) % C::kStages), ((n - 1) / C::kStages) & 1);
-    // loads of the other block that the leader no longer expects: they take microseconds
-    for (int i = 0; i < 200; ++i) __nanosleep(1000);
+      for (unsigned j = n - min(n, (unsigned)C::kStages); j < n; ++j) pair_drain(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1);
+    if (rank == 0 && warp == kMmaWarp && n > 0) pair_drain(done0 + 8 * ((n - 1) % C::kStages), ((n - 1) / C::kStages) & 1);
+    pair_settle();
   }
   __syncthreads();
   pair_sync();

@@ -175,6 +175,16 @@ __device__ __forceinline__ bool pair_wait(unsigned bar, unsigned parity, unsigne
 __device__ __forceinline__ void pair_arrive(unsigned bar, unsigned rank) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(bar, rank)) : "memory");
 }
+// After a wait has run out: waits for a barrier of what is still in flight.  Where the other block
+// gave up first the barrier may never complete, so a millisecond at most: loads take microseconds.
+__device__ __forceinline__ void pair_drain(unsigned bar, unsigned parity) {
+  const long long from = clock64();
+  while (!mbar_try(bar, parity) && clock64() - from < 2000000) {}
+}
+// ... and lets loads of the other block land that the leader no longer expects.
+__device__ __forceinline__ void pair_settle() {
+  for (int i = 0; i < 200; ++i) __nanosleep(1000);
+}
 // A TMA load that signals the leader's barrier (`bar`: its address in the cluster).
 __device__ __forceinline__ void tma_load_pair(unsigned dst, const CUtensorMap* map, int x, int y, unsigned bar) {
   asm volatile(
