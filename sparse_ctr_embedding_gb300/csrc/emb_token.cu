@@ -231,6 +231,95 @@ __device__ __forceinline__ unsigned scan256(unsigned v, unsigned* warp_sums, uns
   return before + x - v;
 }
 
+// Ranks of a lane's items among the warp's equal digits, in order; `count`: how many of each the warp has.
+__device__ __forceinline__ void rank_digits(const unsigned* k, unsigned in, int shift, unsigned mask, unsigned* count, unsigned* rank) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int q = 0; q < kSortItems; ++q) {
+    const bool ok = (in >> q) & 1u;
+    const unsigned digit = ok ? (k[q] >> shift) & mask : 0xffffu;
+    const unsigned same = __match_any_sync(0xffffffffu, digit);
+    const unsigned below = __popc(same & ((1u << lane) - 1));
+    unsigned old = 0;
+    if (ok) old = count[digit];
+    __syncwarp();
+    if (ok && below == 0) count[digit] = old + __popc(same);
+    __syncwarp();
+    if (q & 1) rank[q / 2] |= (old + below) << 16;
+    else rank[q / 2] = old + below;
+  }
+}
+__device__ __forceinline__ unsigned rank_of(const unsigned* rank, int q) { return q & 1 ? rank[q / 2] >> 16 : rank[q / 2] & 0xffffu; }
+
+// All passes of one tile's tokens by one block, in shared memory: no histogram, no other
+// launch (50 tokens of 64 columns into 1000 rows: 33 us with them).
+template <int V>
+__global__ void __launch_bounds__(kSortThreads) sort_one_kernel(const __grid_constant__ SortArgs a, const __grid_constant__ ZeroArgs z) {
+  __shared__ unsigned count[8][kDigits], sums[8];
+  __shared__ uint2 held[kSortTile];
+  if ((int)blockIdx.x < z.blocks) {
+    zero_rows<V>(z, 0, blockIdx.x);
+    return;
+  }
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, d = threadIdx.x, at = w * 32 * kSortItems + lane;
+  const unsigned mask = (1u << a.bits) - 1;
+  unsigned k[kSortItems], v[kSortItems], rank[kSortItems / 2], in = 0, all = 0;
+#pragma unroll
+  for (int q = 0; q < kSortItems; ++q) {
+    const int i = at + q * 32;
+    k[q] = v[q] = 0;
+    if (i < a.t.n) {
+      const long long t = token_at(a.t, i);
+      k[q] = (unsigned)t;
+      v[q] = (unsigned)i;
+      in |= names_row(a.t, t) ? 1u << q : 0u;
+    }
+  }
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * a.bits;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) count[j][d] = 0;
+    __syncthreads();
+    rank_digits(k, in, shift, mask, count[w], rank);
+    __syncthreads();
+    unsigned mine = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const unsigned c = count[j][d];
+      count[j][d] = mine;
+      mine += c;
+    }
+    const unsigned first = scan256(mine, sums, &all);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) count[j][d] += first;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kSortItems; ++q)
+      if ((in >> q) & 1u) held[count[w][(k[q] >> shift) & mask] + rank_of(rank, q)] = make_uint2(k[q], v[q]);
+    __syncthreads();
+    in = 0;
+#pragma unroll
+    for (int q = 0; q < kSortItems; ++q) {
+      const unsigned i = at + q * 32;
+      if (i < all) {
+        const uint2 item = held[i];
+        k[q] = item.x;
+        v[q] = item.y;
+        in |= 1u << q;
+      }
+    }
+  }
+  const int end = (a.passes - 1) & 1;
+#pragma unroll
+  for (int q = 0; q < kSortItems; ++q) {
+    if ((in >> q) & 1u) {
+      a.key[end][at + q * 32] = k[q];
+      a.val[end][at + q * 32] = v[q];
+    }
+  }
+  if (threadIdx.x == 0) *a.valid = all;
+}
+
 // One stable pass.  Tiles are numbered as they start, so those before one are at work or
 // done, and what it waits for comes; the wait is bounded all the same.
 template <bool FIRST, int V>
@@ -274,20 +363,7 @@ __global__ void __launch_bounds__(kSortThreads, 4) sort_kernel(const __grid_cons
       }
     }
   }
-#pragma unroll
-  for (int q = 0; q < kSortItems; ++q) {  // rank among the warp's equal digits, in order
-    const bool ok = (in >> q) & 1u;
-    const unsigned digit = ok ? (k[q] >> shift) & mask : 0xffffu;
-    const unsigned same = __match_any_sync(0xffffffffu, digit);
-    const unsigned below = __popc(same & ((1u << lane) - 1));
-    unsigned old = 0;
-    if (ok) old = count[w][digit];
-    __syncwarp();
-    if (ok && below == 0) count[w][digit] = old + __popc(same);
-    __syncwarp();
-    if (q & 1) rank[q / 2] |= (old + below) << 16;
-    else rank[q / 2] = old + below;
-  }
+  rank_digits(k, in, shift, mask, count[w], rank);
   __syncthreads();
   unsigned mine = 0;
 #pragma unroll
@@ -308,7 +384,7 @@ __global__ void __launch_bounds__(kSortThreads, 4) sort_kernel(const __grid_cons
 #pragma unroll
   for (int q = 0; q < kSortItems; ++q) {
     if ((in >> q) & 1u) {
-      const unsigned to = count[w][(k[q] >> shift) & mask] + (q & 1 ? rank[q / 2] >> 16 : rank[q / 2] & 0xffffu);
+      const unsigned to = count[w][(k[q] >> shift) & mask] + rank_of(rank, q);
       held[to] = make_uint2(k[q], v[q]);
     }
   }
@@ -622,10 +698,24 @@ cudaError_t launch_sums(const SumArgs& a, long long chunks, cudaStream_t st) {
   return cudaGetLastError();
 }
 template <int V>
-cudaError_t launch_grad(const SortArgs& s, const ZeroArgs& z, const SumArgs& a, emb_ftype g_t, long long chunks, cudaStream_t st) {
+cudaError_t launch_sums_of(const SumArgs& a, emb_ftype g_t, long long chunks, cudaStream_t st) {
+  if (g_t == EMB_T_F32) return launch_sums<float, V>(a, chunks, st);
+  if (g_t == EMB_T_BF16) return launch_sums<__nv_bfloat16, V>(a, chunks, st);
+  return launch_sums<__half, V>(a, chunks, st);
+}
+template <int V>
+cudaError_t launch_grad(const SortArgs& s, const ZeroArgs& z, const SumArgs& a, emb_ftype g_t, long long chunks, size_t zero_bytes, cudaStream_t st) {
+  cudaError_t e;
+  if (s.tiles == 1) {
+    sort_one_kernel<V><<<1 + z.blocks, kSortThreads, 0, st>>>(s, z);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_sums_of<V>(a, g_t, chunks, st) : e;
+  }
+  e = cudaMemsetAsync(s.hist, 0, zero_bytes, st);
+  if (e != cudaSuccess) return e;
   const int blocks = (int)std::min<long long>((a.n + 2047) / 2048, 8LL * sm_count());
   histogram_kernel<V><<<blocks + z.blocks, 256, 0, st>>>(s, z, blocks);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   for (int p = 0; p < s.passes; ++p) {
     if (p == 0) sort_kernel<true, V><<<s.tiles + z.blocks, kSortThreads, 0, st>>>(s, z, p);
@@ -633,9 +723,7 @@ cudaError_t launch_grad(const SortArgs& s, const ZeroArgs& z, const SumArgs& a, 
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (g_t == EMB_T_F32) return launch_sums<float, V>(a, chunks, st);
-  if (g_t == EMB_T_BF16) return launch_sums<__nv_bfloat16, V>(a, chunks, st);
-  return launch_sums<__half, V>(a, chunks, st);
+  return launch_sums_of<V>(a, g_t, chunks, st);
 }
 
 }  // namespace
@@ -708,16 +796,16 @@ extern "C" emb_status emb_token_bwd(const void* grad_d, emb_ftype grad_t, int64_
     s.key[j] = (unsigned*)(ws + pl.key[j]);
     s.val[j] = (unsigned*)(ws + pl.val[j]);
   }
-  EMB_CUDA(cudaMemsetAsync(ws, 0, pl.zero_bytes, st));
   const int end = (pl.passes - 1) & 1;
   const SumArgs a{s.key[end], s.val[end], s.valid, grad_d, dweight_d, (float*)(ws + pl.head), (float*)(ws + pl.tail),
                   ldg, ldw, n, (int)dim, (int)dim / v, weight_t, accumulate != 0, scale};
   // blocks that write zeros: 32 rows a warp, one block an SM at most
-  const long long share = (vocab + pl.passes) / (pl.passes + 1);
+  const long long share = pl.tiles == 1 ? vocab : (vocab + pl.passes) / (pl.passes + 1);   // of a launch's
   const ZeroArgs z{dweight_d, ldw, share, vocab, (int)dim / v, weight_t,
                    accumulate ? 0 : (int)std::min<long long>((share + kSortThreads - 1) / kSortThreads, sm_count())};
-  const cudaError_t e = v == 8 ? launch_grad<8>(s, z, a, grad_t, pl.chunks, st) : v == 4 ? launch_grad<4>(s, z, a, grad_t, pl.chunks, st)
-                                                                                         : launch_grad<1>(s, z, a, grad_t, pl.chunks, st);
+  const cudaError_t e = v == 8 ? launch_grad<8>(s, z, a, grad_t, pl.chunks, pl.zero_bytes, st)
+                        : v == 4 ? launch_grad<4>(s, z, a, grad_t, pl.chunks, pl.zero_bytes, st)
+                                 : launch_grad<1>(s, z, a, grad_t, pl.chunks, pl.zero_bytes, st);
   if (e != cudaSuccess) return cuda_fail(e, "emb_token_bwd launch");
   return EMB_OK;
 }
