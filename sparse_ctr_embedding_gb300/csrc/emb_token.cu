@@ -799,10 +799,10 @@ extern "C" emb_status emb_token_bwd(const void* grad_d, emb_ftype grad_t, int64_
   const int end = (pl.passes - 1) & 1;
   const SumArgs a{s.key[end], s.val[end], s.valid, grad_d, dweight_d, (float*)(ws + pl.head), (float*)(ws + pl.tail),
                   ldg, ldw, n, (int)dim, (int)dim / v, weight_t, accumulate != 0, scale};
-  // blocks that write zeros: 32 rows a warp, one block an SM at most
+  // blocks that write zeros: 32 rows a warp; one an SM beside a sort's, four beside one block
   const long long share = pl.tiles == 1 ? vocab : (vocab + pl.passes) / (pl.passes + 1);   // of a launch's
   const ZeroArgs z{dweight_d, ldw, share, vocab, (int)dim / v, weight_t,
-                   accumulate ? 0 : (int)std::min<long long>((share + kSortThreads - 1) / kSortThreads, sm_count())};
+                   accumulate ? 0 : (int)std::min<long long>((share + kSortThreads - 1) / kSortThreads, (pl.tiles == 1 ? 4LL : 1LL) * sm_count())};
   const cudaError_t e = v == 8 ? launch_grad<8>(s, z, a, grad_t, pl.chunks, pl.zero_bytes, st)
                         : v == 4 ? launch_grad<4>(s, z, a, grad_t, pl.chunks, pl.zero_bytes, st)
                                  : launch_grad<1>(s, z, a, grad_t, pl.chunks, pl.zero_bytes, st);
