@@ -28,7 +28,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <cstring>
+#include <type_traits>
 
 #include "emb_tiles.cuh"
 
@@ -64,6 +64,7 @@ struct Mat {
   int first[5];             // of this matrix among all: items of the three phases, chunks, tiles of X
   int param_t, grad_t;
   int wide;                 // rows of the parameter are aligned to four elements
+  int vec;                  // momentum and gradient are aligned to eight
   float scale;
 };
 
@@ -93,6 +94,17 @@ __device__ __forceinline__ float load_f32(const void* p, int t, long long i) {
   if (t == EMB_T_BF16) return to_f32<__nv_bfloat16>(((const __nv_bfloat16*)p)[i]);
   return to_f32<__half>(((const __half*)p)[i]);
 }
+__device__ __forceinline__ void load8_f32(const void* p, int t, long long i, float* o) {
+  auto from = [&](auto* q) {
+    Raw8<std::remove_const_t<std::remove_pointer_t<decltype(q)>>> r;
+    r.load(q + i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = r.get(j);
+  };
+  if (t == EMB_T_F32) from((const float*)p);
+  else if (t == EMB_T_BF16) from((const __nv_bfloat16*)p);
+  else from((const __half*)p);
+}
 // The matrix that number `at` of a list belongs to.
 __device__ __forceinline__ int mat_of(const MuonArgs& a, int list, int at) {
   int lo = 0, hi = a.mats - 1;
@@ -109,22 +121,63 @@ __device__ __forceinline__ float update_of(const MuonArgs& a, float g, float m) 
 
 // ------------------------------------------------------------------ momentum and norm
 
+// This block's elements [at, end): the momentum, and the sum of its updates' squares over this thread's.
+template <typename G>
+__device__ __forceinline__ float momentum_of(const MuonArgs& a, const Mat& t, long long at, long long end, float gs) {
+  float sum = 0.0f;
+  const G* g = (const G*)t.g;
+  if (t.vec) {
+    long long e = at + threadIdx.x * 8LL;
+    constexpr int kBatch = 2;
+    for (; e + (kBatch - 1) * 2048 + 8 <= end; e += kBatch * 2048) {  // all loads before any store
+      Raw8<G> gr[kBatch];
+      Raw8<float> m[kBatch];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        gr[q].load(g + e + q * 2048);
+        m[q].load(t.m + e + q * 2048);
+      }
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = gr[q].get(j) * gs;
+          m[q].v[j] = a.beta * m[q].v[j] + (1.0f - a.beta) * x;
+          const float u = update_of(a, x, m[q].v[j]);
+          sum += u * u;
+        }
+        m[q].store(t.m + e + q * 2048);
+      }
+    }
+    for (; e < end; e += 2048) {
+      for (long long i = e; i < min(end, e + 8); ++i) {
+        const float x = to_f32<G>(g[i]) * gs, m = a.beta * t.m[i] + (1.0f - a.beta) * x, u = update_of(a, x, m);
+        t.m[i] = m;
+        sum += u * u;
+      }
+    }
+    return sum;
+  }
+#pragma unroll 4
+  for (long long i = at + threadIdx.x; i < end; i += 256) {
+    const float x = to_f32<G>(g[i]) * gs, m = a.beta * t.m[i] + (1.0f - a.beta) * x, u = update_of(a, x, m);
+    t.m[i] = m;
+    sum += u * u;
+  }
+  return sum;
+}
+
+// Bound by memory: gradient and momentum in, momentum out (52.6M elements with float32 gradients 100 us).
 __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ MuonArgs a) {
   __shared__ float part[8];
   __shared__ bool last;
   const int i = mat_of(a, 3, blockIdx.x);
   const Mat& t = a.mat[i];
-  const long long n = (long long)t.rows * t.cols, at = (long long)(blockIdx.x - t.first[3]) * kChunk;
+  const long long n = (long long)t.rows * t.cols, at = (long long)(blockIdx.x - t.first[3]) * kChunk, end = min(n, at + kChunk);
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
-  float sum = 0.0f;
-#pragma unroll 4
-  for (long long e = at + threadIdx.x; e < min(n, at + kChunk); e += 256) {
-    const float g = load_f32(t.g, t.grad_t, e) * gs;
-    const float m = a.beta * t.m[e] + (1.0f - a.beta) * g;
-    t.m[e] = m;
-    const float u = update_of(a, g, m);
-    sum += u * u;
-  }
+  float sum = t.grad_t == EMB_T_F32    ? momentum_of<float>(a, t, at, end, gs)
+              : t.grad_t == EMB_T_BF16 ? momentum_of<__nv_bfloat16>(a, t, at, end, gs)
+                                       : momentum_of<__half>(a, t, at, end, gs);
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
@@ -202,12 +255,22 @@ __global__ void __launch_bounds__(256) fill_kernel(const __grid_constant__ MuonA
     const int r = tall ? at & 127 : at >> 3, c = tall ? at >> 7 : at & 7;  // neighbouring lanes: neighbours in memory
     const int row = rb * kTileRows + r, col = slab * kSlab + c * 8;
     float v[8];
+    if (t.vec && !tall && t.cols % 8 == 0 && row < t.s && col < t.l) {  // eight elements an access
+      const long long e = (long long)row * t.cols + col;
+      float g[8];
+      load8_f32(t.g, t.grad_t, e, g);
+      Raw8<float> m;
+      m.load(t.m + e);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = 0.0f;
-      if (row < t.s && col + j < t.l) {
-        const long long e = tall ? (long long)(col + j) * t.cols + row : (long long)row * t.cols + col + j;
-        v[j] = update_of(a, load_f32(t.g, t.grad_t, e) * gs, t.m[e]) * inv;
+      for (int j = 0; j < 8; ++j) v[j] = update_of(a, g[j] * gs, m.v[j]) * inv;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = 0.0f;
+        if (row < t.s && col + j < t.l) {
+          const long long e = tall ? (long long)(col + j) * t.cols + row : (long long)row * t.cols + col + j;
+          v[j] = update_of(a, load_f32(t.g, t.grad_t, e) * gs, t.m[e]) * inv;
+        }
       }
     }
     uint4 hi, lo;
@@ -963,7 +1026,11 @@ extern "C" emb_status emb_muon_step(const emb_muon_tensor* tensors, const void* 
     plan_group(tensors + at, n, o.products == EMB_MUON_SPLIT ? 2 : 1, &a, &pl);
     if (a.mats == 0) continue;
     for (int i = 0, j = 0; i < n; ++i)
-      if (tensors[at + i].rows && tensors[at + i].cols) a.mat[j++].g = grads[at + i];
+      if (tensors[at + i].rows && tensors[at + i].cols) {
+        Mat& m = a.mat[j++];
+        m.g = grads[at + i];
+        m.vec = aligned_to(m.m, 32) && aligned_to(m.g, 8 * ftype_bytes(m.grad_t));
+      }
     unsigned char* ws = (unsigned char*)workspace_d;
     a.ws = ws;
     a.partial = (float*)(ws + pl.partial);
