@@ -783,7 +783,7 @@ EMB_API emb_status emb_muon_step(const emb_muon_tensor* tensors, const void* con
  *   dW[v]  = scale * (sum over i with t_i = v of grad[i])     float32, rounded once to weight_t
  * Rows that no token names get a gradient of zero; with accumulate != 0 the sums are added to what
  * dW holds and the other rows are left alone.  A row's gradients are summed in float32 in an order
- * that depends on the tokens alone, so results repeat bitwise.
+ * that depends on the tokens and the sizes alone, so results repeat bitwise.
  *   tokens_d   token_t[n].  A token equal to `padding` (any number; -1 is usual) reads as zeros
  *              and has no gradient.  Any other outside [0, vocab) does the same and raises EMB_FLAG_BAD_TOKEN
  *              (emb_check_op_flag).

@@ -24,7 +24,8 @@ namespace {
 constexpr int kDigits = 256;
 constexpr int kSortThreads = 256, kSortItems = 16, kSortTile = kSortThreads * kSortItems;
 constexpr int kMaxPasses = 4;
-constexpr int kChunk = 64;                    // sorted positions of one thread's walk
+constexpr long long kWalks = 32768;           // threads that walk, below which walks are shortened
+constexpr int kMaxChunk = 64, kMinChunk = 8;  // sorted positions of one thread's walk
 constexpr unsigned kAggregate = 1u << 30, kInclusive = 2u << 30, kCount = (1u << 30) - 1;
 
 struct TokenArgs {
@@ -111,6 +112,20 @@ struct RawV<T, 4> {
   __device__ __forceinline__ float get(int i) const { return to_f32<T>(reinterpret_cast<const T*>(w)[i]); }
 };
 
+// V = kStrided: rows off the vectors' alignment.  A thread has four columns, a quarter of a row apart,
+// so that neighbouring threads still read side by side, and asks four times less often where its
+// rows are (488,277 x 261 float32: 244 us with one column a thread).
+constexpr int kStrided = -4;
+template <typename T>
+struct RawV<T, kStrided> {
+  T v[4];
+  __device__ __forceinline__ void load(const T* p, int step, int n) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = j < n ? p[j * step] : from_f32<T>(0.0f);
+  }
+  __device__ __forceinline__ float get(int i) const { return to_f32<T>(v[i]); }
+};
+
 // ------------------------------------------------------------------ lookup
 
 struct LookupArgs {
@@ -160,6 +175,7 @@ struct ZeroArgs {
   void* dw;
   long long ldw, rows_a_launch, vocab;
   int pieces, w_t, blocks;   // pieces of V elements, in a row; blocks 0: nothing to do
+  int rows_a_warp;           // at a time: up to 32, about 1024 pieces
 };
 template <int V>
 __device__ __forceinline__ void zero_rows(const ZeroArgs& z, int launch, int block) {
@@ -168,8 +184,8 @@ __device__ __forceinline__ void zero_rows(const ZeroArgs& z, int launch, int blo
   float zero[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) zero[j] = 0.0f;
-  for (long long w = from + (block * (kSortThreads / 32) + (threadIdx.x >> 5)) * 32LL; w < to; w += warps * 32LL) {  // 32 rows a warp
-    const int rows = (int)min(32LL, to - w);
+  for (long long w = from + (long long)(block * (kSortThreads / 32) + (threadIdx.x >> 5)) * z.rows_a_warp; w < to; w += (long long)warps * z.rows_a_warp) {
+    const int rows = (int)min((long long)z.rows_a_warp, to - w);
     int r = lane / z.pieces, p = lane - r * z.pieces;
     while (r < rows) {
       const long long e = (w + r) * z.ldw + p * V;
@@ -435,7 +451,7 @@ struct SumArgs {
   void* dw;
   float *head, *tail;    // [chunks][dim]
   long long ldg, ldw, n;   // n: all tokens
-  int dim, pieces, w_t, accumulate;
+  int dim, pieces, w_t, accumulate, chunk;
   float scale;
 };
 
@@ -466,16 +482,35 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArg
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const long long chunk = i / a.pieces;
   const int piece = (int)(i - chunk * a.pieces);
-  if (chunk * kChunk >= n) return;
-  const unsigned s = (unsigned)(chunk * kChunk), e = min(n, s + kChunk);
+  if (chunk * a.chunk >= n) return;
+  const unsigned s = (unsigned)(chunk * a.chunk), e = min(n, s + a.chunk);
   unsigned cur = a.key[s];
   bool head = s > 0 && a.key[s - 1] == cur;
-  float acc[V];
+  constexpr int N = V == kStrided ? 4 : V;
+  const int step = a.pieces, mine = V == kStrided ? (a.dim - piece + step - 1) / step : N;  // columns of this thread that there are
+  float acc[N];
 #pragma unroll
-  for (int j = 0; j < V; ++j) acc[j] = 0.0f;
-  float* const hp = a.head + chunk * a.dim + piece * V;
-  auto flush = [&](float* to) { store_v<float, V>(to, acc); };
-  constexpr int kRows = V * sizeof(GT) > 16 ? 4 : 8;   // on their way at a time
+  for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+  const long long first = chunk * a.dim + (V == kStrided ? piece : piece * V);
+  auto flush = [&](float* to) {
+    if constexpr (V == kStrided) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < mine) to[first + j * step] = acc[j];
+    } else {
+      store_v<float, V>(to + first, acc);
+    }
+  };
+  auto whole = [&](unsigned row) {  // a run that is complete
+    if constexpr (V == kStrided) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < mine) write_row<1>(a, row, piece + j * step, acc + j);
+    } else {
+      write_row<V>(a, row, piece, acc);
+    }
+  };
+  constexpr int kRows = V * sizeof(GT) > 16 || V == kStrided ? 4 : 8;   // on their way at a time
   unsigned k[kRows], v[kRows];
   auto ask = [&](unsigned b) {
 #pragma unroll
@@ -491,7 +526,8 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArg
     unsigned now[kRows];
 #pragma unroll
     for (int q = 0; q < kRows; ++q) {
-      x[q].load((const GT*)a.g + v[q] * a.ldg + piece * V);
+      if constexpr (V == kStrided) x[q].load((const GT*)a.g + v[q] * a.ldg + piece, step, mine);
+      else x[q].load((const GT*)a.g + v[q] * a.ldg + piece * V);
       now[q] = k[q];
     }
     if (b + kRows < e) ask(b + kRows);                  // the next ones' places, while these are on their way
@@ -499,44 +535,45 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArg
     for (int q = 0; q < kRows; ++q) {
       if (b + q < e) {
         if (now[q] != cur) {
-          if (head) flush(hp);
-          else write_row<V>(a, cur, piece, acc);
+          if (head) flush(a.head);
+          else whole(cur);
           head = false;
           cur = now[q];
 #pragma unroll
-          for (int j = 0; j < V; ++j) acc[j] = 0.0f;
+          for (int j = 0; j < N; ++j) acc[j] = 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] += x[q].get(j);
+        for (int j = 0; j < N; ++j) acc[j] += x[q].get(j);
       }
     }
   }
-  if (head) flush(hp);
-  else if (e < n && a.key[e] == cur) flush(a.tail + chunk * a.dim + piece * V);
-  else write_row<V>(a, cur, piece, acc);
+  if (head) flush(a.head);
+  else if (e < n && a.key[e] == cur) flush(a.tail);
+  else whole(cur);
 }
 
 // Joins the run that passes the end of `chunk` and begins in it: its tail here and the heads of the
-// chunks up to `last`.  `threads` threads (this one is the `me`-th) take columns, and where
-// those are fewer, groups of them take consecutive shares of the heads, added in order.
+// chunks up to `last`.  `threads` threads (this one is the `me`-th) take this block's 32 pieces of a
+// row, and where threads are left, groups of them take consecutive shares of the heads, added in order.
 template <int V, typename Sync>
 __device__ __forceinline__ void join_run(const SumArgs& a, unsigned row, long long chunk, int last, int threads, int me, float* share, Sync sync) {
-  const int heads = last - (int)chunk;
-  for (int p0 = 0; p0 < a.pieces; p0 += threads) {
-    const int width = min(threads, a.pieces - p0), groups = min(threads / width, heads), g = me / width, piece = p0 + me % width;
+  const int heads = last - (int)chunk, p0 = blockIdx.y * 32;
+  {
+    const int width = min(32, a.pieces - p0), groups = min(threads / width, heads), g = me / width, piece = p0 + me % width;
     float acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.0f;
     if (g < groups) {
       const int from = (int)chunk + 1 + (int)((long long)heads * g / groups), to = (int)chunk + 1 + (int)((long long)heads * (g + 1) / groups);
       if (g == 0) load_v<float, V>(a.tail + chunk * a.dim + piece * V, acc);
+      constexpr int kBatch = V == 1 ? 16 : 4;
       int c = from;
-      for (; c + 4 <= to; c += 4) {
-        float x[4][V];
+      for (; c + kBatch <= to; c += kBatch) {
+        float x[kBatch][V];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) load_v<float, V>(a.head + (long long)(c + q) * a.dim + piece * V, x[q]);
+        for (int q = 0; q < kBatch; ++q) load_v<float, V>(a.head + (long long)(c + q) * a.dim + piece * V, x[q]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < kBatch; ++q)
 #pragma unroll
           for (int j = 0; j < V; ++j) acc[j] += x[q][j];
       }
@@ -570,18 +607,18 @@ __global__ void __launch_bounds__(256, 5) join_runs_kernel(const __grid_constant
   __shared__ float share[256 * V];
   __shared__ int last_of[8];            // of a warp's run that is long, else -1
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long chunk = blockIdx.x * 8LL + warp, e = (chunk + 1) * kChunk;
+  const long long chunk = blockIdx.x * 8LL + warp, e = (chunk + 1) * a.chunk;
   // All that the usual run needs is asked for at once: keys past the valid ones are there, but mean nothing.
   const unsigned n = *a.valid;
-  const long long ahead = e + lane * (long long)kChunk;
+  const long long ahead = e + lane * (long long)a.chunk;
   const unsigned start = ahead < a.n ? a.key[ahead] : 0;                // of the chunks that follow, one a lane
   unsigned here = 0, first = 0, before = 0;
   if (e < a.n) {
     here = a.key[e - 1];
-    first = a.key[e - kChunk];
-    before = chunk > 0 ? a.key[e - kChunk - 1] : ~0u;
+    first = a.key[e - a.chunk];
+    before = chunk > 0 ? a.key[e - a.chunk - 1] : ~0u;
   }
-  const int chunks = (int)((n + kChunk - 1LL) / kChunk);
+  const int chunks = (int)((n + a.chunk - 1LL) / a.chunk);
   if (blockIdx.x * 8LL >= chunks) return;
   const unsigned cur = __shfl_sync(0xffffffffu, start, 0);
   // a run passes the end, and it began here
@@ -594,7 +631,7 @@ __global__ void __launch_bounds__(256, 5) join_runs_kernel(const __grid_constant
     if (same != ~0u) hi = lo;
     while (lo < hi) {  // 32 places at a time
       const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-      const unsigned more = __ballot_sync(0xffffffffu, at <= hi && a.key[(long long)at * kChunk] == cur);
+      const unsigned more = __ballot_sync(0xffffffffu, at <= hi && a.key[(long long)at * a.chunk] == cur);
       lo += __popc(more) * step;
       hi = min(hi, lo + step - 1);
     }
@@ -606,14 +643,14 @@ __global__ void __launch_bounds__(256, 5) join_runs_kernel(const __grid_constant
   for (int w = 0; w < 8; ++w) {
     if (last_of[w] < 0) continue;       // the same for the block
     const long long c = blockIdx.x * 8LL + w;
-    join_run<V>(a, a.key[(c + 1) * kChunk], c, last_of[w], 256, threadIdx.x, share, [] { __syncthreads(); });
+    join_run<V>(a, a.key[(c + 1) * a.chunk], c, last_of[w], 256, threadIdx.x, share, [] { __syncthreads(); });
   }
 }
 
 // ------------------------------------------------------------------ host side
 
 struct TokenPlan {
-  int passes = 0, bits = 0, tiles = 0;
+  int passes = 0, bits = 0, tiles = 0, chunk = kMaxChunk;
   long long chunks = 0;
   size_t zero_bytes = 0;  // hist, next, status, from the start on
   size_t next = 0, status = 0, key[2] = {}, val[2] = {}, head = 0, tail = 0, bytes = 0;
@@ -627,7 +664,10 @@ TokenPlan plan_tokens(long long n, long long vocab, long long dim) {
   pl.passes = (bits + 7) / 8;
   pl.bits = (bits + pl.passes - 1) / pl.passes;
   pl.tiles = (int)((n + kSortTile - 1) / kSortTile);
-  pl.chunks = (n + kChunk - 1) / kChunk;
+  // Shorter walks where there are few of them: half as many additions one after the other, twice as many
+  // pieces to join.
+  while (pl.chunk > kMinChunk && (n + pl.chunk - 1) / pl.chunk * ((dim + 7) / 8) < kWalks) pl.chunk /= 2;
+  pl.chunks = (n + pl.chunk - 1) / pl.chunk;
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   pl.next = kMaxPasses * kDigits * 4;
   pl.status = pl.next + 256;
@@ -690,11 +730,13 @@ void launch_lookup_to(const LookupArgs& a, emb_ftype out_t, int v, cudaStream_t 
 
 template <typename GT, int V>
 cudaError_t launch_sums(const SumArgs& a, long long chunks, cudaStream_t st) {
-  const long long blocks = (chunks * a.pieces + 255) / 256;
-  sum_kernel<GT, V><<<(unsigned)blocks, 256, 0, st>>>(a);
+  SumArgs w = a;
+  if (V == 1) w.pieces = (a.dim + 3) / 4;
+  const long long blocks = (chunks * w.pieces + 255) / 256;
+  sum_kernel<GT, V == 1 ? kStrided : V><<<(unsigned)blocks, 256, 0, st>>>(w);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (chunks > 1) join_runs_kernel<V><<<(unsigned)((chunks + 7) / 8), 256, 0, st>>>(a);
+  if (chunks > 1) join_runs_kernel<V><<<dim3((unsigned)((chunks + 7) / 8), (a.pieces + 31) / 32), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 template <int V>
@@ -798,11 +840,14 @@ extern "C" emb_status emb_token_bwd(const void* grad_d, emb_ftype grad_t, int64_
   }
   const int end = (pl.passes - 1) & 1;
   const SumArgs a{s.key[end], s.val[end], s.valid, grad_d, dweight_d, (float*)(ws + pl.head), (float*)(ws + pl.tail),
-                  ldg, ldw, n, (int)dim, (int)dim / v, weight_t, accumulate != 0, scale};
-  // blocks that write zeros: 32 rows a warp; one an SM beside a sort's, four beside one block
+                  ldg, ldw, n, (int)dim, (int)dim / v, weight_t, accumulate != 0, pl.chunk, scale};
+  // blocks that write zeros: one an SM beside a sort's, four beside one block
   const long long share = pl.tiles == 1 ? vocab : (vocab + pl.passes) / (pl.passes + 1);   // of a launch's
+  const int rows_a_warp = (int)std::max<long long>(1, std::min<long long>(32, 1024 / (dim / v)));
+  const long long rows_a_block = rows_a_warp * (kSortThreads / 32);
   const ZeroArgs z{dweight_d, ldw, share, vocab, (int)dim / v, weight_t,
-                   accumulate ? 0 : (int)std::min<long long>((share + kSortThreads - 1) / kSortThreads, (pl.tiles == 1 ? 4LL : 1LL) * sm_count())};
+                   accumulate ? 0 : (int)std::min<long long>((share + rows_a_block - 1) / rows_a_block, (pl.tiles == 1 ? 4LL : 1LL) * sm_count()),
+                   rows_a_warp};
   const cudaError_t e = v == 8 ? launch_grad<8>(s, z, a, grad_t, pl.chunks, pl.zero_bytes, st)
                         : v == 4 ? launch_grad<4>(s, z, a, grad_t, pl.chunks, pl.zero_bytes, st)
                                  : launch_grad<1>(s, z, a, grad_t, pl.chunks, pl.zero_bytes, st);
