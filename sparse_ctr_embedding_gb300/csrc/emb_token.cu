@@ -477,7 +477,7 @@ __device__ __forceinline__ void write_row(const SumArgs& a, unsigned row, int pi
 }
 
 template <typename GT, int V>
-__global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArgs a) {
+__global__ void __launch_bounds__(256, V == kStrided ? 3 : 2) sum_kernel(const __grid_constant__ SumArgs a) {
   const unsigned n = *a.valid;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const long long chunk = i / a.pieces;
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(256) sum_kernel(const __grid_constant__ SumArg
       write_row<V>(a, row, piece, acc);
     }
   };
-  constexpr int kRows = V * sizeof(GT) > 16 || V == kStrided ? 4 : 8;   // on their way at a time
+  constexpr int kRows = V * (int)sizeof(GT) > 16 || V == kStrided ? 4 : 8;   // on their way at a time
   unsigned k[kRows], v[kRows];
   auto ask = [&](unsigned b) {
 #pragma unroll
