@@ -834,6 +834,8 @@ EMB_API emb_status emb_check_op_flag(void* stream, uint32_t* flags_out);
  *    the operands, 1 of the one that issues the products, 2 of the one that loads
  *    the scales (emb_fp8_matmul only); role 3, whatever the step: another one, when the last loads are
  *    on their way.  The products then end early and raise EMB_FLAG_OP_TIMEOUT.
+ *    In emb_token_bwd of more than 4096 tokens, role 0: in each pass of the sort the wait of tile `step`
+ *    (4096 tokens; tile 0 waits for nothing) for the tiles before it.  No row is summed then.
  *    role -1: none (the default).  Process-wide.
  *  - emb_debug_fp8_matmul_plan(m, n, k, plan): how emb_fp8_matmul splits a
  *    product on the current device: plan[0] columns of a tile (0: no tiles), [1]

@@ -114,7 +114,7 @@ struct RawV<T, 4> {
 
 // V = kStrided: rows off the vectors' alignment.  A thread has four columns, a quarter of a row apart,
 // so that neighbouring threads still read side by side, and asks four times less often where its
-// rows are (488,277 x 261 float32: 244 us with one column a thread).
+// rows are (488,277 x 261 float32: 211 us, and 244 with one column a thread).
 constexpr int kStrided = -4;
 template <typename T>
 struct RawV<T, kStrided> {
@@ -163,9 +163,10 @@ struct SortArgs {
   unsigned *hist;        // [kMaxPasses][kDigits]
   unsigned *next;        // [kMaxPasses]: the next tile of each pass
   unsigned *status;      // [passes][tiles][kDigits]: a tile's counts, alone or with all before it
-  unsigned *valid;       // tokens that name rows
+  unsigned *valid;       // tokens that name rows; and whether a wait ran out
   unsigned *key[2], *val[2];
   int passes, bits, tiles;
+  int lost_tile;         // the tile whose wait counts as run out; -1: none
 };
 
 // Zeros into dW, before the sums are written.  The sort is a chain of latencies that leaves the memory
@@ -333,7 +334,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_one_kernel(const __grid_con
       a.val[end][at + q * 32] = v[q];
     }
   }
-  if (threadIdx.x == 0) *a.valid = all;
+  if (threadIdx.x == 0) {
+    a.valid[0] = all;
+    a.valid[1] = 0;
+  }
 }
 
 // One stable pass.  Tiles are numbered as they start, so those before one are at work or
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(kSortThreads, 4) sort_kernel(const __grid_cons
     // most of a pass.  A word that is not there yet is asked for again, from it on.
     constexpr int kLook = 16;
     int j = tile - 1;
-    for (unsigned i = 0; j >= 0 && i < kWaitLimit; ++i) {
+    for (unsigned i = 0; j >= 0 && i < kWaitLimit && tile != a.lost_tile; ++i) {
       unsigned word[kLook];
 #pragma unroll
       for (int q = 0; q < kLook; ++q)
@@ -426,7 +430,10 @@ __global__ void __launch_bounds__(kSortThreads, 4) sort_kernel(const __grid_cons
         more = more && word[q] >= kAggregate && word[q] < kInclusive;
       }
     }
-    if (j >= 0) atomicOr(a.t.flags, EMB_FLAG_OP_TIMEOUT);     // the wait ran out
+    if (j >= 0) {                                             // the wait ran out
+      atomicOr(a.t.flags, EMB_FLAG_OP_TIMEOUT);
+      *(volatile unsigned*)(a.valid + 1) = 1u;
+    }
     if (tile) *(volatile unsigned*)st = (before + mine) | kInclusive;
   }
   base[d] = first + before - local;                           // less the item's place in the tile
@@ -455,6 +462,13 @@ struct SumArgs {
   float scale;
 };
 
+// Sorted positions to sum.  None after a wait that ran out: places that no token was written
+// to hold anything, and would be taken for rows.
+__device__ __forceinline__ unsigned sorted(const SumArgs& a) {
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(a.valid));
+  return v.y ? 0u : v.x;
+}
+
 template <int V>
 __device__ __forceinline__ void write_row(const SumArgs& a, unsigned row, int piece, float* acc) {
   const long long e = row * a.ldw + piece * V;
@@ -478,7 +492,7 @@ __device__ __forceinline__ void write_row(const SumArgs& a, unsigned row, int pi
 
 template <typename GT, int V>
 __global__ void __launch_bounds__(256, V == kStrided ? 3 : 2) sum_kernel(const __grid_constant__ SumArgs a) {
-  const unsigned n = *a.valid;
+  const unsigned n = sorted(a);
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const long long chunk = i / a.pieces;
   const int piece = (int)(i - chunk * a.pieces);
@@ -609,7 +623,7 @@ __global__ void __launch_bounds__(256, 5) join_runs_kernel(const __grid_constant
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long chunk = blockIdx.x * 8LL + warp, e = (chunk + 1) * a.chunk;
   // All that the usual run needs is asked for at once: keys past the valid ones are there, but mean nothing.
-  const unsigned n = *a.valid;
+  const unsigned n = sorted(a);
   const long long ahead = e + lane * (long long)a.chunk;
   const unsigned start = ahead < a.n ? a.key[ahead] : 0;                // of the chunks that follow, one a lane
   unsigned here = 0, first = 0, before = 0;
@@ -833,7 +847,11 @@ extern "C" emb_status emb_token_bwd(const void* grad_d, emb_ftype grad_t, int64_
   if ((pl.chunks * (dim / v) + 255) / 256 > 0x7fffffffLL) return fail(EMB_ERR_UNSUPPORTED, "n * dim too large");
   unsigned char* ws = (unsigned char*)workspace_d;
   SortArgs s{{tokens_d, n, vocab, padding, token_t == EMB_I64, flags},
-             (unsigned*)ws, (unsigned*)(ws + pl.next), (unsigned*)(ws + pl.status), (unsigned*)(ws + pl.next) + kMaxPasses, {}, {}, pl.passes, pl.bits, pl.tiles};
+             (unsigned*)ws, (unsigned*)(ws + pl.next), (unsigned*)(ws + pl.status), (unsigned*)(ws + pl.next) + kMaxPasses, {}, {}, pl.passes, pl.bits, pl.tiles, -1};
+  int lost;
+  unsigned lost_step;
+  lost_wait(&lost, &lost_step);
+  if (lost == 0) s.lost_tile = (int)std::min(lost_step, 0x7fffffffu);
   for (int j = 0; j < 2; ++j) {
     s.key[j] = (unsigned*)(ws + pl.key[j]);
     s.val[j] = (unsigned*)(ws + pl.val[j]);

@@ -169,3 +169,24 @@ def test_graph_stream_and_differences():
         slope = (loss(up) - loss(down)) / 2
         size = float((g.double().abs() * (t == v)[:, None])[:, c].sum()) * 3
         assert abs(slope - float(a[v, c])) <= 1e-4 * (size + 1)
+
+
+@pytest.mark.parametrize("dim", [5, 64])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_a_wait_that_runs_out(dim, accumulate):
+    """The flag is raised and no row is summed: the gradient is zeros, or stays what it was."""
+    n, vocab = 20000, 70000            # five tiles of the sort, three passes
+    t = ids(n, vocab, dim, hot=0.3)
+    g = torch.randn(n, dim, generator=torch.Generator().manual_seed(dim)).cuda()
+    want = E.emb_token_bwd(g, t, vocab)
+    for tile in (1, 4):
+        out = torch.full((vocab, dim), 0.25, device="cuda")
+        try:
+            E.emb_debug_lose_op_wait("load", tile)
+            E.emb_token_bwd(g, t, vocab, out=out, accumulate=accumulate)
+        finally:
+            E.emb_debug_lose_op_wait(None)
+        assert E.emb_check_op_flag() == E.EMB_FLAG_OP_TIMEOUT
+        assert bool((out == (0.25 if accumulate else 0.0)).all())
+        assert torch.equal(E.emb_token_bwd(g, t, vocab), want)
+        assert E.emb_check_op_flag() == 0
