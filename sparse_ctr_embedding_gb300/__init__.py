@@ -551,7 +551,8 @@ def emb_debug_set_probe_bound(table: Table, bound: int) -> None:
 
 def emb_debug_lose_op_wait(role: Optional[str], step: int = 0) -> None:
     """From now on the wait of this role ("load", "product", "scales", "other") at this step of a tiled
-    emb_fp8_matmul counts as run out (None: none, the default)."""
+    emb_fp8_matmul, emb_fp4_matmul or emb_muon_step counts as run out, and "load" that of this tile of
+    emb_token_bwd's sort (None: none, the default)."""
     _check(lib().emb_debug_lose_op_wait(-1 if role is None else ("load", "product", "scales", "other").index(role), int(step)))
 
 
@@ -1225,6 +1226,9 @@ class Muon:
         for t in used:
             if (t.storage_offset() + t.numel()) * t.itemsize > t.untyped_storage().nbytes():
                 raise ValueError("a parameter or momentum has lost its storage")
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in used if t.numel())
+        if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
+            raise ValueError("parameters and momenta must not overlap")
         if self.workspace is None:
             self.workspace = torch.empty(emb_muon_workspace_size(tensors, self.products), dtype=_U8, device=self.device)
         self._tensors, self._addresses, self._aliases = tensors, list(map(torch.Tensor.data_ptr, used)), [t.detach() for t in used]

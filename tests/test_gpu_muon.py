@@ -185,3 +185,11 @@ def test_a_wait_that_runs_out(products):
             assert all(bool((x == 0.25).all()) for x in p)
             got, _ = updates(shapes, grads, m, products)
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_overlapping_matrices_are_refused():
+    p = torch.zeros(8, 16, device="cuda")
+    for other in (p, p[2:4], p[7:]):
+        with pytest.raises(ValueError, match="overlap"):
+            E.Muon([p, other])
+    E.Muon([p[:4], p[4:], torch.zeros(0, 5, device="cuda")])      # side by side
