@@ -86,7 +86,7 @@ struct MuonArgs {
   int mats, planes;
   int slot0[3], slots;      // first slot, by phase; slots of items, after which the blocks' own lie
   int total[5];             // items of the three phases, chunks, tiles of X
-  float beta, decay, lr;
+  float beta, omb, decay, lr;   // omb: 1 - beta, rounded once (from the rounded beta it is 1.3e-5 of itself off at 0.999)
   int nesterov;
   int lost_warp;
   unsigned lost_step;
@@ -120,7 +120,7 @@ __device__ __forceinline__ int mat_of(const MuonArgs& a, int list, int at) {
   return lo;
 }
 __device__ __forceinline__ float update_of(const MuonArgs& a, float g, float m) {
-  return a.nesterov ? (1.0f - a.beta) * g + a.beta * m : m;
+  return a.nesterov ? a.omb * g + a.beta * m : m;
 }
 
 // ------------------------------------------------------------------ momentum and norm
@@ -146,7 +146,7 @@ __device__ __forceinline__ float momentum_of(const MuonArgs& a, const Mat& t, lo
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float x = gr[q].get(j) * gs;
-          m[q].v[j] = a.beta * m[q].v[j] + (1.0f - a.beta) * x;
+          m[q].v[j] = a.beta * m[q].v[j] + a.omb * x;
           const float u = update_of(a, x, m[q].v[j]);
           sum += u * u;
         }
@@ -155,7 +155,7 @@ __device__ __forceinline__ float momentum_of(const MuonArgs& a, const Mat& t, lo
     }
     for (; e < end; e += 2048) {
       for (long long i = e; i < min(end, e + 8); ++i) {
-        const float x = to_f32<G>(g[i]) * gs, m = a.beta * t.m[i] + (1.0f - a.beta) * x, u = update_of(a, x, m);
+        const float x = to_f32<G>(g[i]) * gs, m = a.beta * t.m[i] + a.omb * x, u = update_of(a, x, m);
         t.m[i] = m;
         sum += u * u;
       }
@@ -164,7 +164,7 @@ __device__ __forceinline__ float momentum_of(const MuonArgs& a, const Mat& t, lo
   }
 #pragma unroll 4
   for (long long i = at + threadIdx.x; i < end; i += 256) {
-    const float x = to_f32<G>(g[i]) * gs, m = a.beta * t.m[i] + (1.0f - a.beta) * x, u = update_of(a, x, m);
+    const float x = to_f32<G>(g[i]) * gs, m = a.beta * t.m[i] + a.omb * x, u = update_of(a, x, m);
     t.m[i] = m;
     sum += u * u;
   }
@@ -1048,6 +1048,7 @@ extern "C" emb_status emb_muon_step(const emb_muon_tensor* tensors, const void* 
     a.flags = flags;
     a.grad_scale = o.grad_scale_d;
     a.beta = (float)o.momentum;
+    a.omb = (float)(1.0 - o.momentum);
     a.decay = (float)(1.0 - o.lr * o.weight_decay);
     a.lr = (float)o.lr;
     a.nesterov = o.nesterov != 0;

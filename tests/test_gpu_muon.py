@@ -193,3 +193,22 @@ def test_overlapping_matrices_are_refused():
         with pytest.raises(ValueError, match="overlap"):
             E.Muon([p, other])
     E.Muon([p[:4], p[4:], torch.zeros(0, 5, device="cuda")])      # side by side
+
+
+@pytest.mark.parametrize("beta", [0.95, 0.99, 0.999])
+def test_momentum_near_one(beta):
+    """Each of m = beta m + (1 - beta) g's two terms has two roundings, the coefficient's and the product's, and the sum one:
+    3 u of the terms' magnitudes, u = 2^-24, and a u for what is of second order.  The update's direction then follows
+    within what its own products cost, also where the gradient is only as large as the momentum in it."""
+    shapes = [(96, 200), (200, 96), (33, 65)]
+    grads, m = data(shapes, seed=11)
+    m = [x * (1 - beta) for x in m]                # the new gradient counts for as much as what was there
+    m[1].zero_()
+    got, opt = updates(shapes, grads, m, "split", beta=beta)
+    for o, g, m0, m1 in zip(got, grads, m, opt.m):
+        want, u = momentum(g, m0, beta)
+        size = beta * m0.double().abs() + (1 - beta) * g.double().abs()
+        assert bool(((m1.double() - want).abs() <= 4 * 2.0 ** -24 * size).all()), float(((m1.double() - want).abs() / size).max() * 2 ** 24)
+        exact, rounded = orthogonal(u), orthogonal(u, 2)
+        far = float((rounded - exact).norm()) + 64 * 2.0 ** -24 * float(exact.norm())
+        assert float((o - exact).norm()) <= 3 * far
