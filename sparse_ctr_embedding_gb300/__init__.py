@@ -707,6 +707,27 @@ def _row_stride(t: torch.Tensor, name: str, dev: int) -> int:
     return ld if rows > 1 else max(ld, cols)
 
 
+def _whole_rows(t: torch.Tensor, ld: int, stream) -> Tuple[torch.Tensor, int]:
+    """Codes (a byte an element) whose rows can be read in whole 16 bytes, and the rows' distance: the matrix
+    itself, or a copy where its last row's would pass the end of its storage."""
+    rows, width = t.shape
+    if ld % 16 and (rows <= 1 or width == 0):
+        ld = -(-ld // 16) * 16              # one row: any distance will do
+    if width % 16 == 0 or rows == 0 or ld % 16:
+        return t, ld
+    end = t.storage_offset() + (rows - 1) * ld + -(-width // 16) * 16
+    if end <= t.untyped_storage().nbytes():
+        return t, ld
+    ld = -(-width // 16) * 16
+    hold = _empty(stream, t, (rows, ld), t.dtype)[:, :width]
+    if stream is None:
+        hold.copy_(t)
+    else:
+        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+            hold.copy_(t)
+    return hold, ld
+
+
 def _code_stride(t: torch.Tensor, name: str, dev: int) -> int:
     if t.dtype is not _F8:
         raise TypeError(f"{name} must be {_F8}, got {t.dtype}")
@@ -790,11 +811,10 @@ def emb_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
     return out
 
 
-def _packed_stride(t: torch.Tensor, name: str, dev: int) -> int:
+def _packed(t: torch.Tensor, name: str, dev: int, stream) -> Tuple[torch.Tensor, int]:
     if t.dtype is not _U8:
         raise TypeError(f"{name} must be {_U8}, got {t.dtype}")
-    ld = _row_stride(t, name, dev)
-    return -(-ld // 16) * 16 if ld % 16 and (t.shape[0] <= 1 or t.shape[1] == 0) else ld
+    return _whole_rows(t, _row_stride(t, name, dev), stream)
 
 
 def _scale4(s: torch.Tensor, rows: int, cols: int, name: str, dev: int) -> int:
@@ -835,7 +855,7 @@ def emb_fp4_dequantize(q: torch.Tensor, s: torch.Tensor, cols: Optional[int] = N
     """The values [rows, cols] that 4-bit codes and scales stand for.  cols: default
     two per byte of q (give it where it is odd)."""
     dev = _launch_device(q, "q")
-    ldq = _packed_stride(q, "q", dev)
+    q, ldq = _packed(q, "q", dev, stream)
     rows, width = q.shape
     if cols is None:
         cols = 2 * width
@@ -867,7 +887,7 @@ def emb_fp4_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
     workspace: emb_fp4_matmul_workspace_size bytes (k: twice the bytes of a row) that
     the caller keeps; made for the call if None."""
     dev = _launch_device(a, "a")
-    lda, ldb = _packed_stride(a, "a", dev), _packed_stride(b, "b", dev)
+    (a, lda), (b, ldb) = _packed(a, "a", dev, stream), _packed(b, "b", dev, stream)
     (m, w), (n, wb) = a.shape, b.shape
     if wb != w:
         raise ValueError(f"a and b must have the same columns, got {w} and {wb} bytes")

@@ -206,3 +206,48 @@ def test_constants_match_the_header():
     text = open(E.HEADER).read()
     for name in ("EMB_FP4_BLOCK", "EMB_MUON_MAX_DIM", "EMB_MAX_TOKENS", "EMB_FLAG_BAD_TOKEN"):
         assert int(re.search(rf"^#define {name}\s+(\d+)", text, re.M).group(1)) == getattr(E, name)
+
+
+class Reads:
+    """The library as far as a launch, which reads rows of codes as the kernels do: in whole 16 bytes."""
+
+    def __init__(self, lib, short):
+        self.lib, self.short, self.rows = lib, {t.data_ptr() for t in short}, []
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_size"):
+            return getattr(self.lib, name)
+
+        def launched(*args):
+            k = {"emb_fp4_dequantize": lambda q, ld, s, r, c, *_: [(q, ld, r, -(-c // 2))],
+                 "emb_fp4_matmul": lambda a, lda, sa, b, ldb, sb, m, n, k, *_: [(a, lda, m, -(-k // 2)), (b, ldb, n, -(-k // 2))]}[name](*args)
+            for at, ld, rows, width in k:
+                assert at not in self.short, "reads past the end of a tensor"
+                assert ld % 16 == 0
+                whole = -(-width // 16) * 16
+                self.rows.append([ctypes.string_at(at + i * ld, whole)[:width] for i in range(rows)])
+            return 0
+        return launched
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("width", [1, 15, 20, 500])
+def test_rows_are_not_read_past_their_storage(monkeypatch, rows, width):
+    """Codes whose storage ends with the last row's last byte are laid out anew; others are taken as they are."""
+    ld = -(-width // 16) * 16
+    g = torch.Generator().manual_seed(width)
+    short = torch.randint(0, 256, ((rows - 1) * ld + width,), dtype=torch.uint8, generator=g).as_strided((rows, width), (ld, 1))
+    room = torch.randint(0, 256, (5, ld), dtype=torch.uint8, generator=g)[:, :width]
+    sc = lambda r: torch.zeros(1, -(-2 * width // 128), 32, 4, 4, dtype=torch.uint8)  # noqa: E731
+    stub = Reads(E.lib(), [short])
+    monkeypatch.setattr(E, "lib", lambda: stub)
+    monkeypatch.setattr(E, "_current_device", lambda: 0)
+    monkeypatch.setattr(E, "_raw_stream", lambda stream, dev=None: 0)
+    want = [bytes(r.tolist()) for r in short]
+    assert E.emb_fp4_dequantize(on(0, short), on(0, sc(rows)), out=on(0, torch.zeros(rows, 2 * width))).shape == (rows, 2 * width)
+    for a, b in ((short, room), (room, short)):
+        E.emb_fp4_matmul(on(0, a), on(0, sc(1)), on(0, b), on(0, sc(1)), out=on(0, torch.zeros(a.shape[0], b.shape[0])))
+    assert stub.rows[0] == want and stub.rows[1] == want and stub.rows[4] == want
+    assert stub.rows[2] == stub.rows[3] == [bytes(r.tolist()) for r in room]
+    kept = torch.zeros(1, ld, dtype=torch.uint8)[:, :width]
+    assert E._packed(on(0, kept), "q", 0, None)[0].data_ptr() == kept.data_ptr()      # there is room: no copy

@@ -310,3 +310,33 @@ def test_plans():
         assert workers <= 152 // blocks or cols == 0
     assert {(0, 1, False), (256, 2, False), (256, 2, True)} <= seen, seen
     print(seen)
+
+
+@pytest.mark.parametrize("cols", [2, 31, 33, 40, 63, 129, 1000, 1007, 2078, 10_001])
+def test_rows_that_end_their_tensor(cols):
+    """Codes whose storage ends with the last row's last byte: products and values are those of padded rows, and
+    what lies behind the row does not count."""
+    g = torch.Generator().manual_seed(cols)
+    w = -(-cols // 2)
+    ld = -(-w // 16) * 16
+    for rows in (1, 2, 3):
+        x = torch.randn(rows, cols, generator=g).cuda()
+        q, s = E.emb_fp4_quantize(x)
+        room = torch.full((rows * ld + 64,), 0x77, dtype=torch.uint8, device="cuda")
+        short = torch.empty((rows - 1) * ld + w, dtype=torch.uint8, device="cuda")     # not a byte more
+        for hold in (room[:(rows - 1) * ld + w], short):
+            t = hold.as_strided((rows, w), (ld, 1), hold.storage_offset())
+            t.copy_(q)
+            for dtype in (F32, BF16, F16):
+                assert torch.equal(E.emb_fp4_dequantize(t, s, cols, dtype=dtype), E.emb_fp4_dequantize(q, s, cols, dtype=dtype))
+            for n in (1, 40, 10_001 if cols < 2000 else 500):
+                b, sb = E.emb_fp4_quantize(torch.randn(n, cols, generator=g).cuda() / cols ** 0.5)
+                got = E.emb_fp4_matmul(t, s, b, sb, out_dtype=F32)
+                assert torch.equal(got, E.emb_fp4_matmul(q, s, b, sb, out_dtype=F32))
+                check(got, q, s, b, sb)
+                back = E.emb_fp4_matmul(b, sb, t, s, out_dtype=F32)
+                assert torch.equal(back, E.emb_fp4_matmul(b, sb, q, s, out_dtype=F32))
+                check(back, b, sb, q, s)
+    one = E.emb_fp4_quantize(torch.randn(1, cols, generator=g).cuda())
+    clone = one[0].clone(memory_format=torch.contiguous_format)
+    assert clone.untyped_storage().nbytes() == w and torch.equal(E.emb_fp4_dequantize(clone, one[1], cols), E.emb_fp4_dequantize(*one, cols))
