@@ -728,11 +728,10 @@ def _whole_rows(t: torch.Tensor, ld: int, stream) -> Tuple[torch.Tensor, int]:
     return hold, ld
 
 
-def _code_stride(t: torch.Tensor, name: str, dev: int) -> int:
+def _codes(t: torch.Tensor, name: str, dev: int, stream) -> Tuple[torch.Tensor, int]:
     if t.dtype is not _F8:
         raise TypeError(f"{name} must be {_F8}, got {t.dtype}")
-    ld = _row_stride(t, name, dev)
-    return -(-ld // 16) * 16 if ld % 16 and (t.shape[0] <= 1 or t.shape[1] == 0) else ld
+    return _whole_rows(t, _row_stride(t, name, dev), stream)
 
 
 def emb_fp8_quantize(x: torch.Tensor, block_rows: int = 1, transpose: bool = False, stream=None):
@@ -781,7 +780,7 @@ def emb_fp8_matmul(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
     workspace: emb_fp8_matmul_workspace_size bytes that the caller keeps; made
     for the call if None."""
     dev = _launch_device(a, "a")
-    lda, ldb = _code_stride(a, "a", dev), _code_stride(b, "b", dev)
+    (a, lda), (b, ldb) = _codes(a, "a", dev, stream), _codes(b, "b", dev, stream)
     (m, k), (n, kb) = a.shape, b.shape
     if kb != k:
         raise ValueError(f"a and b must have the same columns, got {k} and {kb}")

@@ -237,3 +237,41 @@ def test_plan_of_a_product():
     assert E.emb_debug_fp8_matmul_plan(1, 100, 300)[0] == 0
     cols, tiles, blocks, steps = E.emb_debug_fp8_matmul_plan(1000, 300, 500)
     assert cols in (64, 128, 256) and tiles == 8 * -(-300 // cols) and blocks >= 1 and steps >= 0
+
+
+class Reads:
+    """The library as far as a product, which reads rows of codes as its kernels do: in whole 16 bytes."""
+
+    def __init__(self, lib, short):
+        self.lib, self.short, self.rows = lib, short.data_ptr(), []
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_size"):
+            return getattr(self.lib, name)
+
+        def product(a, lda, sa, ar, b, ldb, sb, br, m, n, k, *_):
+            for at, ld, rows in ((a, lda, m), (b, ldb, n)):
+                assert at != self.short, "reads past the end of a tensor"
+                assert ld % 16 == 0
+                self.rows.append([ctypes.string_at(at + i * ld, -(-k // 16) * 16)[:k] for i in range(rows)])
+            return 0
+        return product
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("k", [1, 15, 20, 500])
+def test_rows_are_not_read_past_their_storage(monkeypatch, rows, k):
+    """Codes whose storage ends with the last row's last byte are laid out anew; others are taken as they are."""
+    ld = -(-k // 16) * 16
+    g = torch.Generator().manual_seed(k)
+    short = torch.randint(0, 127, ((rows - 1) * ld + k,), dtype=torch.uint8, generator=g).view(F8).as_strided((rows, k), (ld, 1))
+    room = torch.randint(0, 127, (5, ld), dtype=torch.uint8, generator=g).view(F8)[:, :k]
+    stub = Reads(E.lib(), short)
+    monkeypatch.setattr(E, "lib", lambda: stub)
+    monkeypatch.setattr(E, "_current_device", lambda: 0)
+    monkeypatch.setattr(E, "_raw_stream", lambda stream, dev=None: 0)
+    for a, b in ((short, room), (room, short)):
+        E.emb_fp8_matmul(on(0, a), on(0, torch.zeros(-(-k // 128), a.shape[0])), on(0, b), on(0, torch.zeros(-(-k // 128), b.shape[0])),
+                         out=on(0, torch.zeros(a.shape[0], b.shape[0])))
+    want = [bytes(r.tolist()) for r in short.contiguous().view(torch.uint8)]
+    assert stub.rows[0] == stub.rows[3] == want and stub.rows[1] == stub.rows[2]

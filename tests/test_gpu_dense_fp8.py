@@ -319,3 +319,23 @@ def test_matmul_of_several_tiles_a_block(m, n, k, bn, out, wide, b_rows):
     got = E.emb_fp8_matmul(a, sa, b, sb, bias=bias, out=hold[:, :n])
     check(got, a, sa, b, sb, bias)
     assert bool((hold[:, n:] == 7.0).all())
+
+
+@pytest.mark.parametrize("k", [1, 15, 17, 40, 129, 1000, 1007, 2063, 10_001])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_rows_that_end_their_tensor(k, block_rows):
+    """Codes whose storage ends with the last row's last byte: products are those of padded rows."""
+    ld = -(-k // 16) * 16
+    for rows in (1, 2, 3):
+        for n in (1, 40, 10_001 if k < 2000 else 500):
+            q, s, b, sb = operands(rows, n, k, block_rows, block_rows, seed=k)
+            short = torch.empty((rows - 1) * ld + k, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)   # not a byte more
+            t = short.as_strided((rows, k), (ld, 1))
+            t.view(torch.uint8).copy_(q.view(torch.uint8))
+            assert t.untyped_storage().nbytes() == (rows - 1) * ld + k
+            got = E.emb_fp8_matmul(t, s, b, sb, out_dtype=F32)
+            assert torch.equal(got, E.emb_fp8_matmul(q, s, b, sb, out_dtype=F32))
+            check(got, q, s, b, sb)
+            back = E.emb_fp8_matmul(b, sb, t, s, out_dtype=F32)
+            assert torch.equal(back, E.emb_fp8_matmul(b, sb, q, s, out_dtype=F32))
+            check(back, b, sb, q, s)
