@@ -1046,8 +1046,8 @@ class AdamW:
     which with `step_count` is the checkpoint; load_state takes per-tensor lists.
     A parameter, copy or state that is given other storage (p.data = ..., half(),
     set_()) is found by its address at the next step and described anew (the old
-    storage is held until then); its size and device must stay.  A CUDA
-    graph replays the step number, the rates and the addresses it was captured with."""
+    storage is held until then); its size and device must stay, and over the same
+    memory its type and strides.  A CUDA graph replays the step number, the rates and the addresses it was captured with."""
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999),
                  eps: float = 1e-8, weight_decay: float = 0.01, state: str = "f32", seed: int = 0,
@@ -1197,9 +1197,11 @@ class Muon:
     matrix.  products "half" (one float16 product each) or "split" (float32's accuracy,
     three of them).  The momenta `m` (float32, one per matrix) are the
     checkpoint; load_state sets them.  A parameter or momentum that is given other
-    storage is found by its address at the next step and described anew (the old storage
-    is held until then).  `workspace` is used by every step: steps must be ordered.  A
-    CUDA graph replays the rates and the addresses it was captured with."""
+    storage, another type or other strides is found at the next step and described anew
+    (the old storage is held until then), as are another `scale` or `products`; one that is
+    not contiguous, or of another shape, is refused.  `workspace` is used by every
+    step: steps must be ordered.  A CUDA graph replays the rates, the types and the addresses
+    it was captured with."""
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, momentum: float = 0.95, weight_decay: float = 0.0,
                  nesterov: bool = True, scale="rms", products: str = "half"):
@@ -1227,7 +1229,7 @@ class Muon:
         self.m = [torch.zeros(s, dtype=_F32, device=self.device) for s in self._shapes]
         self._devs = [self._dev] * len(self.params)
         self._grad_dtypes = [p.dtype for p in self.params]
-        self.workspace = None
+        self.workspace, self._outgrown = None, []
         self._bind()
 
     def _bind(self) -> None:
@@ -1235,6 +1237,8 @@ class Muon:
         is kept: as long as it lives no other tensor can come to lie at its address."""
         if len(self.params) != len(self._shapes) or len(self.m) != len(self._shapes):
             raise ValueError("the number of parameters or momenta has changed")
+        if len(self.scale) != len(self._shapes):
+            raise ValueError("scale must have one entry per parameter")
         tensors = (_MuonTensor * len(self.params))()
         for i, (p, m, s) in enumerate(zip(self.params, self.m, self._shapes)):
             if tuple(p.shape) != s or tuple(m.shape) != s:
@@ -1248,9 +1252,18 @@ class Muon:
         spans = sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in used if t.numel())
         if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
             raise ValueError("parameters and momenta must not overlap")
-        if self.workspace is None:
-            self.workspace = torch.empty(emb_muon_workspace_size(tensors, self.products), dtype=_U8, device=self.device)
-        self._tensors, self._addresses, self._aliases = tensors, list(map(torch.Tensor.data_ptr, used)), [t.detach() for t in used]
+        need = emb_muon_workspace_size(tensors, self.products)
+        if self.workspace is None or self.workspace.nbytes < need:
+            if self.workspace is not None:
+                self._outgrown.append(self.workspace)       # captured graphs go on using it
+            self.workspace = torch.empty(need, dtype=_U8, device=self.device)
+        self._tensors, self._bound, self._aliases = tensors, self._description(), [t.detach() for t in used]
+
+    def _description(self):
+        """What the library has been told, or would be told now, the gradients apart."""
+        used, T = [*self.params, *self.m], torch.Tensor
+        return (list(map(T.data_ptr, used)), list(map(T.size, used)), list(map(T.stride, used)), list(map(_dtype_of, used)),
+                list(self.scale), self.products)
 
     def load_state(self, m: Sequence[torch.Tensor]) -> None:
         """Sets the momenta from one float32 tensor per parameter: all of them, or none if one does not fit."""
@@ -1272,8 +1285,8 @@ class Muon:
             raise ValueError(f"each gradient must be a contiguous tensor on cuda:{self._dev} of its parameter's shape")
         if _current_device() != self._dev:
             raise ValueError(f"the parameters are on cuda:{self._dev}, the current device is cuda:{_current_device()}")
-        if list(map(T.data_ptr, self.params)) + list(map(T.data_ptr, self.m)) != self._addresses:
-            self._bind()                    # a parameter or momentum has moved
+        if self._description() != self._bound:
+            self._bind()                    # a parameter or momentum has moved or changed
         dtypes = list(map(_dtype_of, grads))
         if dtypes != self._grad_dtypes:
             kinds = [_ftype(g, "grad") for g in dtypes]

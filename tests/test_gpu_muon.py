@@ -212,3 +212,65 @@ def test_momentum_near_one(beta):
         exact, rounded = orthogonal(u), orthogonal(u, 2)
         far = float((rounded - exact).norm()) + 64 * 2.0 ** -24 * float(exact.norm())
         assert float((o - exact).norm()) <= 3 * far
+
+
+def test_changes_over_the_same_memory():
+    """Other strides, types, scales or products at an address that stays: a step follows them or refuses, with
+    nothing changed."""
+    shapes = [(64, 64), (48, 80)]
+    grads, m = data(shapes, seed=12)
+
+    def step(p, products="half", scale=(1.0, 1.0), m=m):
+        opt = E.Muon(p, lr=0.5, scale=scale, products=products)
+        opt.load_state(m)
+        return opt
+    p = [torch.full(s, 0.25, device="cuda") for s in shapes]
+    opt = step(p)
+    opt.step(grads)
+    kept, moved = [x.clone() for x in p], [x.clone() for x in opt.m]
+    for change, back in ((lambda: setattr(p[0], "data", p[0].data.t()), lambda: setattr(p[0], "data", p[0].data.t())),
+                         (lambda: opt.m.__setitem__(0, opt.m[0].t()), lambda: opt.m.__setitem__(0, opt.m[0].t())),
+                         (lambda: opt.m.__setitem__(1, opt.m[1].view(torch.int32)), lambda: opt.m.__setitem__(1, opt.m[1].view(F32))),
+                         (lambda: setattr(p[1], "data", p[1].data.view(80, 48)), lambda: setattr(p[1], "data", p[1].data.view(48, 80))),
+                         (lambda: setattr(opt, "scale", [1.0]), lambda: setattr(opt, "scale", [1.0, 1.0]))):
+        change()
+        with pytest.raises((ValueError, TypeError)):
+            opt.step(grads)
+        back()
+        assert all(map(torch.equal, p, kept)) and all(map(torch.equal, opt.m, moved))
+    opt.step(grads)                                            # as it was
+    want = [torch.full(s, 0.25, device="cuda") for s in shapes]
+    ref = step(want)
+    ref.step(grads)
+    ref.step(grads)
+    assert all(map(torch.equal, p, want)) and all(map(torch.equal, opt.m, ref.m))
+    # the same bytes as another type of its size
+    a, b = [[torch.full(s, 0.25, dtype=BF16, device="cuda") for s in shapes] for _ in range(2)]
+    oa, bits = step(a), a[0].data
+    oa.step(grads)
+    a[0].data = bits.view(F16)
+    ob = step(b)
+    ob.step(grads)
+    ob = step([b[0].data.view(F16), b[1]], m=ob.m)
+    oa.step(grads)
+    ob.step(grads)
+    assert a[0].dtype == F16 and torch.equal(a[0], ob.params[0]) and torch.equal(a[1], b[1])
+    # scale and products
+    a, b, c = [[torch.full(s, 0.25, device="cuda") for s in shapes] for _ in range(3)]
+    oa, ob, oc = step(a), step(b, "split", (2.0, 0.5)), step(c)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        oa.step(grads)
+    old = oa.workspace.data_ptr()
+    oa.products, oa.scale = "split", [2.0, 0.5]
+    oa.step(grads)
+    ob.step(grads)
+    assert oa.workspace.data_ptr() != old and all(map(torch.equal, a, b)) and all(map(torch.equal, oa.m, ob.m))
+    for x, y in zip(a + oa.m, c + oc.m):
+        x.copy_(y)
+    other = torch.full((1 << 24,), 255, dtype=torch.uint8, device="cuda")      # would lie where the graph's workspace was
+    graph.replay()
+    oc.step(grads)
+    torch.cuda.synchronize()
+    assert all(map(torch.equal, a, c)) and all(map(torch.equal, oa.m, oc.m)) and bool((other == 255).all())
+    assert E.emb_check_op_flag() == 0
