@@ -768,7 +768,8 @@ typedef struct {
  * emb_muon_workspace_size() bytes, 256-byte aligned (about 4 bytes an element, 8 with
  * EMB_MUON_SPLIT, and as much for the short sides' squares); calls that share it must be
  * ordered.  Results repeat bitwise.  Where a bounded wait runs out before the last
- * products, the weights are left as they were. */
+ * products (EMB_FLAG_OP_TIMEOUT), the weights of its launch (128 matrices at most) are left as they were, but the
+ * momenta already hold the gradients: they are set back before the step is repeated. */
 EMB_API emb_status emb_muon_workspace_size(const emb_muon_tensor* tensors, int32_t n_tensors, emb_muon_products products,
                                            size_t* bytes);
 EMB_API emb_status emb_muon_step(const emb_muon_tensor* tensors, const void* const* grads, int32_t n_tensors,

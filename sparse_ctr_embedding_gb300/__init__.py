@@ -1201,7 +1201,8 @@ class Muon:
     (the old storage is held until then), as are another `scale` or `products`; one that is
     not contiguous, or of another shape, is refused.  `workspace` is used by every
     step: steps must be ordered.  A CUDA graph replays the rates, the types and the addresses
-    it was captured with."""
+    it was captured with.  After a step that raised EMB_FLAG_OP_TIMEOUT the momenta hold its
+    gradients while the weights do not: load_state with those from before it, then repeat it."""
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, momentum: float = 0.95, weight_decay: float = 0.0,
                  nesterov: bool = True, scale="rms", products: str = "half"):

@@ -274,3 +274,35 @@ def test_changes_over_the_same_memory():
     torch.cuda.synchronize()
     assert all(map(torch.equal, a, c)) and all(map(torch.equal, oa.m, oc.m)) and bool((other == 255).all())
     assert E.emb_check_op_flag() == 0
+
+
+@pytest.mark.parametrize("products", ["half", "split"])
+def test_momenta_after_a_wait_that_ran_out(products):
+    """The momenta have taken the gradients, the weights have not: repeated after the momenta were set back the step
+    is the one that was lost; repeated as things are, it counts the gradients twice."""
+    shapes = [(300, 700), (64, 100)]
+    grads, m = data(shapes, seed=13)
+    make = lambda: E.Muon([torch.full(s, 0.25, device="cuda") for s in shapes], lr=0.1, products=products)  # noqa: E731
+    ref = make()
+    ref.load_state(m)
+    ref.step(grads)
+    once = [x.clone() for x in ref.m]
+    twice = make()
+    twice.load_state(once)
+    twice.step(grads)
+    for role in ("load", "product", "other"):
+        opts = [make(), make()]
+        for opt in opts:
+            opt.load_state(m)
+            try:
+                E.emb_debug_lose_op_wait(role, 1)
+                opt.step(grads)
+            finally:
+                E.emb_debug_lose_op_wait(None)
+            assert E.emb_check_op_flag() == E.EMB_FLAG_OP_TIMEOUT
+            assert all(bool((x == 0.25).all()) for x in opt.params) and all(map(torch.equal, opt.m, once))
+        opts[0].load_state(m)
+        for opt, want in zip(opts, (ref, twice)):
+            opt.step(grads)
+            assert all(map(torch.equal, opt.m, want.m)) and all(map(torch.equal, opt.params, want.params))
+        assert E.emb_check_op_flag() == 0
