@@ -340,3 +340,77 @@ def test_rows_that_end_their_tensor(cols):
     one = E.emb_fp4_quantize(torch.randn(1, cols, generator=g).cuda())
     clone = one[0].clone(memory_format=torch.contiguous_format)
     assert clone.untyped_storage().nbytes() == w and torch.equal(E.emb_fp4_dequantize(clone, one[1], cols), E.emb_fp4_dequantize(*one, cols))
+
+
+# (columns of a tile or 0, blocks of a worker, steps shared out) of every product, and sizes that reach it on a GPU of 152 SMs
+PLANS = {(0, 1, False): [(1, 1024, 8190), (2, 777, 1002)],
+         (64, 1, False): [(123, 835, 1490), (307, 1233, 622)],
+         (64, 1, True): [(64, 1024, 8192), (570, 81, 5426)],
+         (128, 1, False): [(1024, 1664, 16384), (1471, 3423, 1602)],
+         (128, 1, True): [(581, 210, 33658), (9, 67, 39406)],
+         (256, 1, False): [(2051, 3657, 4846), (1813, 1301, 322)],
+         (256, 1, True): [(50, 8734, 15630), (7, 2197, 32284), (1303, 910, 22926)],
+         (256, 2, False): [(20_011, 1024, 8192), (1843, 1358, 7090)],
+         (256, 2, True): [(133, 3037, 14134), (1000, 520, 80_000)]}
+
+
+def plan_of(m, n, k):
+    cols, _, _, steps, blocks = E.emb_debug_fp4_matmul_plan(m, n, k)
+    return cols, blocks, steps > 0
+
+
+def sizes_of(plan, count):
+    """Sizes that this GPU runs by this plan: those above where they do, else the first of a seeded search that do."""
+    found = [s for s in sum(PLANS.values(), []) if plan_of(*s) == plan]
+    g = torch.Generator().manual_seed(1)
+    for u in torch.rand(100_000, 3, generator=g, dtype=torch.float64).tolist() if len(found) < count else ():
+        m, n, k = int(60_000 ** u[0]), int(32 * 300 ** u[1]), 2 * int(16 * 1000 ** u[2])
+        if m * k <= 8e7 and n * k <= 8e7 and m * n * k <= 1.2e11 and plan_of(m, n, k) == plan:
+            found.append((m, n, k))
+            if len(found) >= count:
+                break
+    assert len(found) >= count, plan
+    return found
+
+
+@pytest.mark.parametrize("plan", PLANS, ids=str)
+def test_every_plan(plan):
+    """Each kernel and way to cut the work, into aligned rows of output (whole vectors) and others, in all three types."""
+    for m, n, k in sizes_of(plan, 2):
+        a, sa, b, sb = operands(m, n, k, seed=21)
+        bias = torch.randn(n, generator=torch.Generator().manual_seed(n)).cuda()
+        A, B = matrix(a, sa).cuda(), matrix(b, sb).cuda()
+        ref, size = A @ B.t() + bias.double(), A.abs() @ B.abs().t() + bias.double().abs()
+        del A, B
+        for dtype in (BF16, F32, F16):
+            got = []
+            for ld in (-(-n // 16) * 16, n | 1):
+                hold = torch.full((m, ld), 7.0, dtype=dtype, device="cuda")
+                out = E.emb_fp4_matmul(a, sa, b, sb, bias=bias, out=hold[:, :n])
+                close("out", out, ref, size, ulps(k))
+                assert bool((hold[:, n:] == 7.0).all())
+                got.append(out)
+            assert torch.equal(*got), (m, n, k, dtype)
+        assert E.emb_check_op_flag() == 0
+
+
+@pytest.mark.parametrize("plan", [p for p in PLANS if p[0]], ids=str)
+def test_a_wait_of_every_plan_that_runs_out(plan):
+    """As test_a_wait_that_runs_out, for pairs of SMs and each width of a tile, whole and shared."""
+    m, n, k = sizes_of(plan, 1)[0]
+    a, sa, b, sb = operands(m, n, k, seed=22)
+    want = E.emb_fp4_matmul(a, sa, b, sb)
+    check(want, a, sa, b, sb)
+    steps = E.emb_debug_fp4_matmul_plan(m, n, k)[3] or -(-k // 256)        # that a worker takes at least
+    try:
+        for role in ("load", "product", "other"):
+            for step in sorted({0, min(steps - 1, 1), min(steps - 1, 6)}):
+                E.emb_debug_lose_op_wait(role, step)
+                E.emb_fp4_matmul(a, sa, b, sb)
+                E.emb_debug_lose_op_wait(None)
+                assert E.emb_check_op_flag() == E.EMB_FLAG_OP_TIMEOUT, (role, step)
+                assert E.emb_check_op_flag() == 0
+                assert torch.equal(E.emb_fp4_matmul(a, sa, b, sb), want), (role, step)
+                assert E.emb_check_op_flag() == 0
+    finally:
+        E.emb_debug_lose_op_wait(None)
