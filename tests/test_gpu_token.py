@@ -190,3 +190,40 @@ def test_a_wait_that_runs_out(dim, accumulate):
         assert bool((out == (0.25 if accumulate else 0.0)).all())
         assert torch.equal(E.emb_token_bwd(g, t, vocab), want)
         assert E.emb_check_op_flag() == 0
+
+
+@pytest.mark.parametrize("dim", [5, 12, 64])
+@pytest.mark.parametrize("kind", [torch.int32, torch.int64])
+@pytest.mark.parametrize("vocab", [201, 70_001])
+def test_bad_tokens_among_many(dim, kind, vocab):
+    """Tokens that name no row, in every tile of the sort and between equal tokens: counted nowhere, summed
+    nowhere, whatever row their low bits would name; the others' sums are those without them."""
+    n = 20_001
+    t = ids(n, vocab, dim, kind, pad=0.1, hot=0.3)
+    low, high = (-(1 << 31), (1 << 31) - 1) if kind == torch.int32 else (-(1 << 62), 1 << 62)
+    bad = [vocab, vocab + 1, vocab + 256, 65_536 * 4, -2, -256, low, high, high - 255] + ([1 << 32, (1 << 40) + 7, -(1 << 32)] if kind == torch.int64 else [])
+    at = torch.randperm(n, generator=torch.Generator().manual_seed(vocab))[:5000].cuda()
+    at = torch.cat([at, torch.tensor([0, 4095, 4096, n - 1], device="cuda")])
+    t[at] = torch.tensor(bad, device="cuda").to(kind)[torch.arange(len(at), device="cuda") % len(bad)]
+    clean = torch.where((t >= 0) & (t < vocab), t, -1)
+    assert int((clean >= 0).sum()) > 5000
+    g = torch.randn(n, dim, generator=torch.Generator().manual_seed(dim)).cuda()
+    g[clean < 0] = float("nan")                    # their gradients are not read
+    for padding in (-1, vocab // 2):               # the second one: the token that occurs most
+        keep = torch.where(clean == padding, -1, clean)
+        ref, size = grad64(g, keep, vocab, 0.5)
+        got = E.emb_token_bwd(g, t, vocab, scale=0.5, padding=padding)
+        assert E.emb_check_op_flag() == E.EMB_FLAG_BAD_TOKEN and E.emb_check_op_flag() == 0
+        held(got, ref, size, keep, vocab)
+        assert torch.equal(got, E.emb_token_bwd(g, keep, vocab, scale=0.5)) and E.emb_check_op_flag() == 0
+        out = torch.full((vocab, dim), 2.0, device="cuda")
+        E.emb_token_bwd(g, t, vocab, scale=0.5, padding=padding, out=out, accumulate=True)
+        seen = torch.zeros(vocab, dtype=torch.bool, device="cuda")
+        seen[keep[keep >= 0].long()] = True
+        assert bool((out[~seen] == 2.0).all()) and torch.equal(out[seen], got[seen] + 2.0)
+        w = torch.randn(vocab, dim, device="cuda")
+        rows = E.emb_token_fwd(w, t, padding=padding)
+        assert torch.equal(rows, torch.where((keep >= 0)[:, None], w[keep.clamp_min(0).long()], 0.0))
+        assert E.emb_check_op_flag() == E.EMB_FLAG_BAD_TOKEN
+    t.fill_(vocab)
+    assert bool((E.emb_token_bwd(g, t, vocab) == 0).all()) and E.emb_check_op_flag() == E.EMB_FLAG_BAD_TOKEN
