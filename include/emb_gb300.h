@@ -744,7 +744,7 @@ EMB_API emb_status emb_adamw_step(const emb_adamw_tensor* tensors, const void* c
  * X ends with singular values near 1.  Products are of float16 values with float32 sums:
  * EMB_MUON_HALF of one each (an update's error is about 2^-9 of it; more where u has a
  * low rank, whose other directions the steps raise from rounding noise), EMB_MUON_SPLIT
- * of two each (float32's accuracy, at a third of the rate).  The rest is float32; w is
+ * of two each (about float32's accuracy, at a third of the rate: 2e-6 to 7e-6 of an update, float32 products 2e-6 to 5e-6).  The rest is float32; w is
  * rounded to nearest-even in its own type.  A matrix whose u has a value that is not
  * finite, or squares that sum past float32, becomes NaN.
  */
@@ -765,8 +765,10 @@ typedef struct {
 } emb_muon_params;
 /* tensors and grads (device pointers grad_t[rows, cols], one per matrix) are host arrays,
  * read before the call returns.  Matrices must not overlap.  workspace_d:
- * emb_muon_workspace_size() bytes, 256-byte aligned (about 4 bytes an element, 8 with
- * EMB_MUON_SPLIT, and as much for the short sides' squares); calls that share it must be
+ * emb_muon_workspace_size() bytes, 256-byte aligned: 4 bytes an element (8 with EMB_MUON_SPLIT), and as much for
+ * each element of two squares of the short side, all sides rounded up to 256; 256 KB for each tile of 256 x 256, or part of
+ * one, of a phase that shares out its summed index, and with EMB_MUON_SPLIT for each pair of SMs (19.9 MB on 152 SMs,
+ * however small the matrices); calls that share it must be
  * ordered.  Results repeat bitwise.  Where a bounded wait runs out before the last
  * products (EMB_FLAG_OP_TIMEOUT), the weights of its launch (128 matrices at most) are left as they were, but the
  * momenta already hold the gradients: they are set back before the step is repeated. */
@@ -787,7 +789,7 @@ EMB_API emb_status emb_muon_step(const emb_muon_tensor* tensors, const void* con
  * that depends on the tokens and the sizes alone, so results repeat bitwise.
  *   tokens_d   token_t[n].  A token equal to `padding` (any number; -1 is usual) reads as zeros
  *              and has no gradient.  Any other outside [0, vocab) does the same and raises EMB_FLAG_BAD_TOKEN
- *              (emb_check_op_flag).
+ *              (emb_check_op_flag).  A call with n, dim or (the gradient) vocab 0 reads no token.
  *   weight_d, dweight_d  rows ldw elements apart; out_d, grad_d rows ldo / ldg apart.
  *   workspace_d  emb_token_bwd_workspace_size() bytes, 256-byte aligned; calls that share it
  *              must be ordered.

@@ -1194,7 +1194,7 @@ class Muon:
     matrices (float32, bfloat16 or float16), updated in place.  scale: of each update,
     "rms" (0.2 sqrt(max(rows, cols)): a root mean square of 0.2, the size of AdamW's, so
     its learning rates serve), "spectral" (sqrt(max(1, rows / cols))), or one number per
-    matrix.  products "half" (one float16 product each) or "split" (float32's accuracy,
+    matrix.  products "half" (one float16 product each) or "split" (about float32's accuracy,
     three of them).  The momenta `m` (float32, one per matrix) are the
     checkpoint; load_state sets them.  A parameter or momentum that is given other
     storage, another type or other strides is found at the next step and described anew

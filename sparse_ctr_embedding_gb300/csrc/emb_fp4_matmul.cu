@@ -121,7 +121,7 @@ struct TileCfg4 {
   static constexpr int kSlabBytes = (kBM + BN) * 128;
   static constexpr int kRowBlocks = 1 + (BN + 127) / 128;       // scale tiles of 128 rows in a step: a's, b's
   static constexpr int kScaleBytes = kRowBlocks * 1024;         // of 256 k's
-  static constexpr int kStages = (204 * 1024 + 4096) / (kSlabBytes + kScaleBytes);  // 4, 6 or 7
+  static constexpr int kStages = (204 * 1024 + 4096) / (kSlabBytes + kScaleBytes);  // 4, 6 or 8
   static constexpr int kAccs = BN == 256 ? 1 : 2;
   static constexpr int kScaleCols = kRowBlocks * 8;             // TMEM columns of a stage's scales
   static constexpr int kUsedCols = kAccs * BN + kStages * kScaleCols;
@@ -593,7 +593,9 @@ Plan4 make_plan4(long long m, long long n, long long k) {
   const int sms = sm_count();
   // The tile's width, or pairs' tiles, and whole tiles or even shares of the steps: whichever a model of
   // the time (us, fitted to 17 shapes from 64 x 1024 x 8192 to 131,072 x 1024 x 8192, each run in all four
-  // ways; within 20 % of most) puts first.  A step takes 0.33, 0.245 or 0.23 at 256, 128 or 64 columns and 0.284
+  // ways) puts first.  It is within 7 % from 60 us on, but leaves out what every product takes (launch, the ring's
+  // first loads, the last tile's way out: 3 to 12 us), so small ones take up to several times what it
+  // says (64 x 1024 x 8192: 4.7 by it, 6.9 measured; 1813 x 1301 x 322: 2.1 and 12.6); there it only orders the ways.  A step takes 0.33, 0.245 or 0.23 at 256, 128 or 64 columns and 0.284
   // by pairs, a tile's end 1.4, 0.6, 0.5 and 2.6; sharing costs the second launch and 0.3 a megabyte
   // of partial tiles.  Measured: 131,072 x 1024 x 8192 311 by pairs and 339 at 256; x 1024 77 at 256 and 90 by
   // pairs; 1024 x 1664 x 16,384 19 whole at 128 and 22 at 256; 64 x 1024 x 8192 7.6 shared and 10.7 whole.

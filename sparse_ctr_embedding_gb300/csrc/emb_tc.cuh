@@ -176,7 +176,8 @@ __device__ __forceinline__ void pair_arrive(unsigned bar, unsigned rank) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(bar, rank)) : "memory");
 }
 // After a wait has run out: waits for a barrier of what is still in flight.  Where the other block
-// gave up first the barrier may never complete, so a millisecond at most: loads take microseconds.
+// gave up first the barrier may never complete, so a millisecond at most (for each barrier; a ring has up to six):
+// loads take microseconds.
 __device__ __forceinline__ void pair_drain(unsigned bar, unsigned parity) {
   const long long from = clock64();
   while (!mbar_try(bar, parity) && clock64() - from < 2000000) {}

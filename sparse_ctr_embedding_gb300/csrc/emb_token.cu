@@ -117,7 +117,8 @@ struct RawV<T, 4> {
 
 // V = kStrided: rows off the vectors' alignment.  A thread has four columns, a quarter of a row apart,
 // so that neighbouring threads still read side by side, and asks four times less often where its
-// rows are (488,277 x 261 float32: 211 us, and 244 with one column a thread).
+// rows are (488,277 x 261 float32: 211 us, and 244 with one column a thread), though at three blocks an SM 376 bytes a
+// thread are spilled.
 constexpr int kStrided = -4;
 template <typename T>
 struct RawV<T, kStrided> {
