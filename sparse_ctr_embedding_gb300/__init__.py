@@ -713,8 +713,8 @@ def _whole_rows(t: torch.Tensor, ld: int, stream) -> Tuple[torch.Tensor, int]:
     rows, width = t.shape
     if ld % 16 and (rows <= 1 or width == 0):
         ld = -(-ld // 16) * 16              # one row: any distance will do
-    if width % 16 == 0 or rows == 0 or ld % 16:
-        return t, ld
+    if width % 16 == 0 or rows == 0 or ld % 16 or ld < width or t.data_ptr() % 16:
+        return t, ld                        # nothing past a row, or refused by the library
     end = t.storage_offset() + (rows - 1) * ld + -(-width // 16) * 16
     if end <= t.untyped_storage().nbytes():
         return t, ld

@@ -251,3 +251,15 @@ def test_rows_are_not_read_past_their_storage(monkeypatch, rows, width):
     assert stub.rows[2] == stub.rows[3] == [bytes(r.tolist()) for r in room]
     kept = torch.zeros(1, ld, dtype=torch.uint8)[:, :width]
     assert E._packed(on(0, kept), "q", 0, None)[0].data_ptr() == kept.data_ptr()      # there is room: no copy
+
+
+def test_rows_that_the_library_refuses_are_left_to_it():
+    """Off the alignment, over one another or at odd distances: refused where the storage ends with them as elsewhere."""
+    for off, rows, ld in ((1, 1, 32), (8, 3, 32), (0, 3, 0), (0, 3, 16), (0, 3, 20)):
+        for end in (off + (rows - 1) * ld + 20, 400):      # with the last row's last byte, or later
+            hold = torch.zeros(end, dtype=torch.uint8)
+            assert hold.data_ptr() % 16 == 0
+            t = hold.as_strided((rows, 20), (ld, 1), off)
+            got, dist = E._packed(on(0, t), "q", 0, None)
+            assert got.data_ptr() == t.data_ptr()
+            refused(back(q=got.data_ptr(), ldq=dist, rows=rows, cols=40, out=P, ldo=40))
